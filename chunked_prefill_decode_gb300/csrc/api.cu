@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -26,6 +27,8 @@ __device__ int g_hb_device_error = 0;
 
 namespace hb {
 cudaError_t launch_kv_append(const AppendParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv8_append(Append8Params p, int head_dim, cudaStream_t stream);
+cudaError_t launch_kv8_widen(const WidenParams& p, cudaStream_t stream);
 cudaError_t launch_linear(const LinearParams& p, const CUtensorMap& xmap, const CUtensorMap& wmap,
                           int num_sms, cudaStream_t stream);
 int linear_w_box_rows();
@@ -211,6 +214,37 @@ hb_status check_ptr(const void* p, const char* name) {
   return HB_OK;
 }
 
+// What hb_attention and hb_kv8_attention check alike: the batch, that the
+// plan is one of this batch and cache, and (unless the batch is empty: then
+// there is nothing more to do) the scale, q and out.
+hb_status check_planned(const hb_batch* batch, const void* h_plan, bool kv8, const void* q,
+                        const void* out, float softmax_scale, PlanHeader* hp) {
+  hb_status s = check_batch(batch);
+  if (s != HB_OK) return s;
+  if (!h_plan) return fail(HB_ERR_INVALID_ARG, "h_plan is NULL");
+  PlanHeader& h = *hp;
+  std::memcpy(&h, h_plan, sizeof(h));
+  if (h.magic != kPlanMagic || h.version != kPlanVersion)
+    return fail(HB_ERR_WORKSPACE, "h_plan is not a plan written by hb_plan");
+  if (h.num_seqs != batch->num_seqs || h.total_q != batch->total_q ||
+      h.num_q_heads != batch->num_q_heads || h.num_kv_heads != batch->num_kv_heads ||
+      h.head_dim != batch->head_dim || h.page_size != batch->page_size ||
+      h.max_pages_per_seq != batch->max_pages_per_seq ||
+      h.sliding_window != batch->sliding_window)
+    return fail(HB_ERR_WORKSPACE, "plan was made for a different batch geometry");
+  if ((h.kv8 != 0) != kv8)
+    return fail(HB_ERR_WORKSPACE, kv8 ? "h_plan is a plan of the bf16 cache (hb_plan)"
+                                      : "h_plan is a plan of the 8-bit cache (hb_kv8_plan)");
+  if (batch->total_q == 0) return ok();
+  if (!(softmax_scale > 0.f) && !(softmax_scale <= 0.f))
+    return fail(HB_ERR_INVALID_ARG, "softmax_scale is NaN");
+  // (masked scores are -infinity before the scale is applied)
+  if (kv8 && !(softmax_scale > 0.f && softmax_scale < INFINITY))
+    return fail(HB_ERR_INVALID_ARG, "softmax_scale %g: must be positive and finite", softmax_scale);
+  if ((s = check_ptr(q, "q")) != HB_OK) return s;
+  return check_ptr(out, "out");
+}
+
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // A named range on the profiler's host timeline around each entry point of
@@ -245,6 +279,7 @@ struct PlanScratch {
   std::vector<DecodeItem> dec;
   std::vector<int32_t> cta_off;
   std::vector<double> t_end;
+  std::vector<WidenItem> widen;
 };
 
 PlanScratch& plan_scratch() {
@@ -386,6 +421,11 @@ bool follows_own_append(void* stream, const hb_batch* b, const void* kc, const v
 
 void internal_note_other_launch(void* stream) { note_launch(stream, LastLaunch{}); }
 
+// hb_plan and hb_kv8_plan (defined below)
+hb_status internal_plan(const hb_batch* batch, const int32_t* h_q_len, const int32_t* h_context_len,
+                        int32_t num_sms, void* h_plan, size_t* plan_bytes, void* d_workspace,
+                        size_t* workspace_bytes, void* stream, bool kv8);
+
 // hb_kv_append, optionally gated on a flag raised by a copy on another
 // stream (defined below)
 hb_status internal_kv_append(const hb_batch* batch, const void* k_new, const void* v_new,
@@ -397,7 +437,7 @@ hb_status internal_kv_append(const hb_batch* batch, const void* k_new, const voi
 hb_status internal_attention(const hb_batch* batch, const void* h_plan, const void* q,
                              const void* k_new, const void* v_new, const void* k_cache,
                              const void* v_cache, float softmax_scale, void* out,
-                             void* d_workspace, void* stream);
+                             void* d_workspace, void* stream, bool kv8 = false);
 
 }  // namespace hb
 
@@ -569,7 +609,28 @@ hb_status hb_plan(const hb_batch* batch, const int32_t* h_q_len,
                   const int32_t* h_context_len, int32_t num_sms, void* h_plan,
                   size_t* plan_bytes, void* d_workspace, size_t* workspace_bytes,
                   void* stream) {
-  NvtxRange range("hb_plan");
+  return hb::internal_plan(batch, h_q_len, h_context_len, num_sms, h_plan, plan_bytes,
+                           d_workspace, workspace_bytes, stream, false);
+}
+
+hb_status hb_kv8_plan(const hb_batch* batch, const int32_t* h_q_len,
+                      const int32_t* h_context_len, int32_t num_sms, void* h_plan,
+                      size_t* plan_bytes, void* d_workspace, size_t* workspace_bytes,
+                      void* stream) {
+  return hb::internal_plan(batch, h_q_len, h_context_len, num_sms, h_plan, plan_bytes,
+                           d_workspace, workspace_bytes, stream, true);
+}
+
+}  // extern "C"
+
+// hb_plan, and with kv8 the plan of the 8-bit cache's attention: the same
+// items, and for the rows whose pages are widened to bf16 first their items
+// and their room in the workspace.
+hb_status hb::internal_plan(const hb_batch* batch, const int32_t* h_q_len,
+                            const int32_t* h_context_len, int32_t num_sms, void* h_plan,
+                            size_t* plan_bytes, void* d_workspace, size_t* workspace_bytes,
+                            void* stream, bool kv8) {
+  NvtxRange range(kv8 ? "hb_kv8_plan" : "hb_plan");
   try {
     hb_status s = check_batch(batch);
     if (s != HB_OK) return s;
@@ -886,18 +947,46 @@ hb_status hb_plan(const hb_batch* batch, const int32_t* h_q_len,
     const size_t n_off = (size_t)(part.grid + part.n_dynamic + 1);
     const int n_slots = part.n_slots, n_merge = part.n_merge;
 
+    // ---- 8-bit cache: the pages to widen, sequence by sequence
+    ps.widen.clear();
+    int64_t widen_pages = 0;
+    if (kv8) {
+      for (int i = 0; i < S; ++i) {
+        const int first = W > 0 ? std::max(0, h_context_len[i] - h_q_len[i] - W + 1) / kPageSize : 0;
+        ps.widen.push_back(WidenItem{i, first, (int32_t)widen_pages, 0});
+        widen_pages += (h_context_len[i] + kPageSize - 1) / kPageSize - first;
+        if (widen_pages * kPageSize > 0x7fffffffLL)
+          return fail(HB_ERR_UNSUPPORTED, "the chunk rows' contexts add up to over 2^31 tokens");
+      }
+    }
+    const size_t n_widen = ps.widen.size();
+
     // ---- sizes
     const size_t offsets_at = n_dec * sizeof(DecodeItem) + n_chk * sizeof(ChunkItem);
-    const size_t items_bytes = align_up(offsets_at + n_off * sizeof(int32_t), 256);
-    const size_t need_plan = sizeof(PlanHeader) + items_bytes;
+    const size_t widen_at = align_up(offsets_at + n_off * sizeof(int32_t), 16);
+    const size_t items_bytes =
+        align_up(kv8 ? widen_at + n_widen * sizeof(WidenItem) : offsets_at + n_off * sizeof(int32_t), 256);
+    const size_t need_plan = sizeof(PlanHeader) + items_bytes + (kv8 ? sizeof(Plan8) : 0);
     const size_t ws_counters = items_bytes;
     const size_t ws_partial_o = align_up(ws_counters + (size_t)(kCounterMerge0 + n_merge) * 4, 256);
     const size_t ws_partial_ml = align_up(ws_partial_o + (size_t)n_slots * Hq * D * 4, 256);
     const size_t ws_chunk_counters = align_up(ws_partial_ml + (size_t)n_slots * Hq * 8, 256);
     const size_t ws_chunk_o = align_up(ws_chunk_counters + (size_t)n_cmerge * 4, 256);
     const size_t ws_chunk_ml = align_up(ws_chunk_o + (size_t)n_cslots * D * kChunkRows * 4, 256);
-    const size_t ws_total =
+    const size_t ws_bf16 =
         std::max<size_t>(256, align_up(ws_chunk_ml + (size_t)n_cslots * 2 * kChunkRows * 4, 256));
+    Plan8 p8{};
+    size_t ws_total = ws_bf16;
+    if (n_widen > 0) {
+      const size_t pool = (size_t)widen_pages * kPageSize * Hkv * D * 2;
+      p8.num_widen = (int32_t)n_widen;
+      p8.widen_pages = (int32_t)widen_pages;
+      p8.ws_widen_items = widen_at;
+      p8.ws_table = ws_bf16;
+      p8.ws_k = align_up(p8.ws_table + (size_t)S * batch->max_pages_per_seq * 4, 256);
+      p8.ws_v = align_up(p8.ws_k + pool, 256);
+      ws_total = align_up(p8.ws_v + pool, 256);
+    }
 
     const size_t have_plan = *plan_bytes, have_ws = *workspace_bytes;
     *plan_bytes = need_plan;
@@ -956,6 +1045,7 @@ hb_status hb_plan(const hb_batch* batch, const int32_t* h_q_len,
     h.ws_partial_ml = ws_partial_ml;
     h.ws_total = ws_total;
     h.plan_bytes = need_plan;
+    h.kv8 = kv8 ? sizeof(PlanHeader) + items_bytes : 0;
     uint8_t* hp = static_cast<uint8_t*>(h_plan);
     std::memcpy(hp, &h, sizeof(h));
     uint8_t* items = hp + sizeof(PlanHeader);
@@ -964,6 +1054,8 @@ hb_status hb_plan(const hb_batch* batch, const int32_t* h_q_len,
     std::memcpy(items + offsets_at, ps.cta_off.data(), n_off * sizeof(int32_t));
     const size_t used = offsets_at + n_off * sizeof(int32_t);
     std::memset(items + used, 0, items_bytes - used);   // alignment padding
+    if (n_widen) std::memcpy(items + widen_at, ps.widen.data(), n_widen * sizeof(WidenItem));
+    if (kv8) std::memcpy(hp + h.kv8, &p8, sizeof(p8));
 
     if (d_workspace == nullptr) return ok();  // host plan only
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -982,6 +1074,8 @@ hb_status hb_plan(const hb_batch* batch, const int32_t* h_q_len,
     return fail(HB_ERR_CUDA, "unexpected exception in hb_plan");
   }
 }
+
+extern "C" {
 
 hb_status hb_attention(const hb_batch* batch, const void* h_plan, const void* q,
                        const void* k_cache, const void* v_cache, float softmax_scale,
@@ -1006,27 +1100,12 @@ hb_status hb_attention_new_kv(const hb_batch* batch, const void* h_plan, const v
 hb_status hb::internal_attention(const hb_batch* batch, const void* h_plan, const void* q,
                                  const void* k_new, const void* v_new, const void* k_cache,
                                  const void* v_cache, float softmax_scale, void* out,
-                                 void* d_workspace, void* stream) {
-  NvtxRange range("hb_attention");
+                                 void* d_workspace, void* stream, bool kv8) {
+  NvtxRange range(kv8 ? "hb_kv8_attention" : "hb_attention");
   try {
-    hb_status s = check_batch(batch);
-    if (s != HB_OK) return s;
-    if (!h_plan) return fail(HB_ERR_INVALID_ARG, "h_plan is NULL");
     PlanHeader h;
-    std::memcpy(&h, h_plan, sizeof(h));
-    if (h.magic != kPlanMagic || h.version != kPlanVersion)
-      return fail(HB_ERR_WORKSPACE, "h_plan is not a plan written by hb_plan");
-    if (h.num_seqs != batch->num_seqs || h.total_q != batch->total_q ||
-        h.num_q_heads != batch->num_q_heads || h.num_kv_heads != batch->num_kv_heads ||
-        h.head_dim != batch->head_dim || h.page_size != batch->page_size ||
-        h.max_pages_per_seq != batch->max_pages_per_seq ||
-        h.sliding_window != batch->sliding_window)
-      return fail(HB_ERR_WORKSPACE, "plan was made for a different batch geometry");
-    if (batch->total_q == 0) return ok();
-    if (!(softmax_scale > 0.f) && !(softmax_scale <= 0.f))
-      return fail(HB_ERR_INVALID_ARG, "softmax_scale is NaN");
-    if ((s = check_ptr(q, "q")) != HB_OK) return s;
-    if ((s = check_ptr(out, "out")) != HB_OK) return s;
+    hb_status s = check_planned(batch, h_plan, kv8, q, out, softmax_scale, &h);
+    if (s != HB_OK || batch->total_q == 0) return s;
     if ((s = check_ptr(k_cache, "k_cache")) != HB_OK) return s;
     if ((s = check_ptr(v_cache, "v_cache")) != HB_OK) return s;
     if (k_new && (s = check_ptr(k_new, "k_new")) != HB_OK) return s;
@@ -1150,7 +1229,110 @@ hb_status hb::internal_attention(const hb_batch* batch, const void* h_plan, cons
   }
 }
 
+namespace {
+
+hb_status check_kv8(const void* k_cache, const void* v_cache, const void* k_exp, const void* v_exp) {
+  hb_status s;
+  if ((s = check_ptr(k_cache, "k_cache")) != HB_OK) return s;
+  if ((s = check_ptr(v_cache, "v_cache")) != HB_OK) return s;
+  if (!k_exp || !v_exp) return fail(HB_ERR_INVALID_ARG, "k_exp and v_exp must be non-NULL");
+  return HB_OK;
+}
+
+}  // namespace
+
 extern "C" {
+
+hb_status hb_kv8_append(const hb_batch* batch, const void* k_new, const void* v_new, void* k_cache,
+                        void* v_cache, int8_t* k_exp, int8_t* v_exp, void* stream) {
+  NvtxRange range("hb_kv8_append");
+  try {
+    hb_status s = check_batch(batch);
+    if (s != HB_OK) return s;
+    if (batch->total_q == 0) return ok();
+    if ((s = check_ptr(k_new, "k_new")) != HB_OK) return s;
+    if ((s = check_ptr(v_new, "v_new")) != HB_OK) return s;
+    if ((s = check_kv8(k_cache, v_cache, k_exp, v_exp)) != HB_OK) return s;
+    DevState* dev = nullptr;
+    if ((s = device_state(&dev)) != HB_OK) return s;
+    Append8Params p{};
+    p.cu_q_len = batch->cu_q_len;
+    p.context_len = batch->context_len;
+    p.block_table = batch->block_table;
+    p.num_seqs = batch->num_seqs;
+    p.total_q = batch->total_q;
+    p.max_pages_per_seq = batch->max_pages_per_seq;
+    p.num_pages = batch->num_pages;
+    p.num_kv_heads = batch->num_kv_heads;
+    p.k_new = static_cast<const uint16_t*>(k_new);
+    p.v_new = static_cast<const uint16_t*>(v_new);
+    p.k_cache = static_cast<uint8_t*>(k_cache);
+    p.v_cache = static_cast<uint8_t*>(v_cache);
+    p.k_exp = k_exp;
+    p.v_exp = v_exp;
+    p.dev_error = dev->err;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    LaunchTimer t(0, st);
+    cudaError_t e = launch_kv8_append(p, batch->head_dim, st);
+    t.done();
+    if (e != cudaSuccess) return cuda_fail(e, "kv8_append launch");
+    note_launch(stream, LastLaunch{});
+    g_launches.fetch_add(1);
+    return ok();
+  } catch (...) {
+    return fail(HB_ERR_CUDA, "unexpected exception in hb_kv8_append");
+  }
+}
+
+hb_status hb_kv8_attention(const hb_batch* batch, const void* h_plan, const void* q,
+                           const void* k_cache, const void* v_cache, const int8_t* k_exp,
+                           const int8_t* v_exp, float softmax_scale, void* out, void* d_workspace,
+                           void* stream) {
+  try {
+    PlanHeader h;
+    hb_status s = check_planned(batch, h_plan, true, q, out, softmax_scale, &h);
+    if (s != HB_OK || batch->total_q == 0) return s;
+    if ((s = check_kv8(k_cache, v_cache, k_exp, v_exp)) != HB_OK) return s;
+    if (!d_workspace || (reinterpret_cast<uintptr_t>(d_workspace) & 255u))
+      return fail(HB_ERR_INVALID_ARG, "d_workspace must be non-NULL and 256-byte aligned");
+    DevState* dev = nullptr;
+    if ((s = device_state(&dev)) != HB_OK) return s;
+    Plan8 p8;
+    std::memcpy(&p8, static_cast<const uint8_t*>(h_plan) + h.kv8, sizeof(p8));
+    uint8_t* ws = static_cast<uint8_t*>(d_workspace);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    WidenParams wp{};
+    wp.items = reinterpret_cast<const WidenItem*>(ws + p8.ws_widen_items);
+    wp.num_items = p8.num_widen;
+    wp.num_units = p8.widen_pages;
+    wp.block_table = batch->block_table;
+    wp.ws_table = reinterpret_cast<int32_t*>(ws + p8.ws_table);
+    wp.max_pages_per_seq = batch->max_pages_per_seq;
+    wp.num_pages = batch->num_pages;
+    wp.num_kv_heads = batch->num_kv_heads;
+    wp.head_dim = batch->head_dim;
+    wp.cache[0] = static_cast<const uint8_t*>(k_cache);
+    wp.cache[1] = static_cast<const uint8_t*>(v_cache);
+    wp.exps[0] = k_exp;
+    wp.exps[1] = v_exp;
+    wp.wide[0] = reinterpret_cast<uint16_t*>(ws + p8.ws_k);
+    wp.wide[1] = reinterpret_cast<uint16_t*>(ws + p8.ws_v);
+    wp.dev_error = dev->err;
+    LaunchTimer t(1, st);
+    cudaError_t e = launch_kv8_widen(wp, st);
+    t.done();
+    if (e != cudaSuccess) return cuda_fail(e, "kv8_widen launch");
+    note_launch(stream, LastLaunch{});
+    g_launches.fetch_add(1);
+    hb_batch b = *batch;
+    b.block_table = wp.ws_table;
+    b.num_pages = p8.widen_pages;
+    return hb::internal_attention(&b, h_plan, q, nullptr, nullptr, wp.wide[0], wp.wide[1],
+                                  softmax_scale, out, d_workspace, stream, true);
+  } catch (...) {
+    return fail(HB_ERR_CUDA, "unexpected exception in hb_kv8_attention");
+  }
+}
 
 hb_status hb_check(void* stream) {
   try {
@@ -1167,7 +1349,10 @@ hb_status hb_check(void* stream) {
     cudaMemcpy(dev->err, &zero, sizeof(int), cudaMemcpyHostToDevice);
     if (v & HB_DEVERR_INDEX)
       return fail(HB_ERR_DEVICE_INDEX, "a kernel met a page index outside [0, num_pages) (word %d)", v);
-    return fail(HB_ERR_TIMEOUT, "a kernel wait gave up (word %d)", v);
+    if (v & HB_DEVERR_TIMEOUT) return fail(HB_ERR_TIMEOUT, "a kernel wait gave up (word %d)", v);
+    if (v & HB_DEVERR_PAGES)
+      return fail(HB_ERR_OUT_OF_PAGES, "hb_pages_assign found too few free pages (word %d)", v);
+    return fail(HB_ERR_SHAPE, "hb_pages_* met lengths or a ring state that break their rules (word %d)", v);
   } catch (...) {
     return fail(HB_ERR_CUDA, "unexpected exception in hb_check");
   }

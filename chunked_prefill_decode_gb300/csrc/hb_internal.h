@@ -7,6 +7,8 @@
 
 #define HB_DEVERR_INDEX 1
 #define HB_DEVERR_TIMEOUT 2
+#define HB_DEVERR_PAGES 4     // the ring holds too few free pages
+#define HB_DEVERR_LENGTHS 8   // lengths or a ring state that break their rules
 
 #if defined(__CUDACC__)
 #define HB_HD __host__ __device__
@@ -107,7 +109,7 @@ struct PlanHeader {
   uint64_t ws_chunk_counters;   // [num_chunk_merges] arrivals per split tile
   uint64_t ws_chunk_o;          // [num_chunk_slots, D, 128] fp32
   uint64_t ws_chunk_ml;         // [num_chunk_slots, 2, 128] fp32: (m in log2 units, l)
-  uint64_t pad1;
+  uint64_t kv8;                 // offset of the Plan8 record (host), 0: a bf16 plan
 };
 static_assert(sizeof(PlanHeader) == 176, "header size");
 static_assert(sizeof(PlanHeader) % 16 == 0, "header alignment");
@@ -204,6 +206,54 @@ struct AppendParams {
   // the kernel reads nothing and starts the next kernel only after that
   const uint32_t* ready_flag;
   uint32_t ready_value;
+};
+
+// The append into the 8-bit cache (kv8_append.cu, kv8.cuh).
+struct Append8Params {
+  const int32_t* cu_q_len;
+  const int32_t* context_len;
+  const int32_t* block_table;
+  int32_t num_seqs, total_q, max_pages_per_seq, num_pages, num_kv_heads;
+  int64_t num_units;      // page units of the grid (set by the launcher)
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  int8_t* k_exp;          // [num_pages, Hkv]
+  int8_t* v_exp;
+  int* dev_error;
+};
+
+// What an 8-bit plan adds to a plan (hb_kv8_plan): its host copy holds this
+// record behind the items (PlanHeader.kv8 = its offset, 0 in a bf16 plan).
+// The chunk rows' pages are spelt out as bf16 in the workspace before the
+// attention launch reads them; `widen` items, one per chunk sequence, say
+// which (kv8_widen.cu).
+struct Plan8 {
+  int32_t num_widen;        // WidenItem entries, among the uploaded items
+  int32_t widen_pages;      // pages of all of them
+  uint64_t ws_widen_items;  // device offsets (bytes from workspace start)
+  uint64_t ws_table;        // [num_seqs, max_pages_per_seq] int32
+  uint64_t ws_k, ws_v;      // [widen_pages, 16, Hkv, D] bf16
+};
+
+struct WidenItem {
+  int32_t seq;
+  int32_t page_begin;   // first logical page
+  int32_t ws_page;      // its page in the workspace pools; the next item's ends this one
+  int32_t pad;
+};
+
+struct WidenParams {
+  const WidenItem* items;
+  int32_t num_items, num_units;   // units: pages of all items
+  const int32_t* block_table;
+  int32_t* ws_table;
+  int32_t max_pages_per_seq, num_pages, num_kv_heads, head_dim;
+  const uint8_t* cache[2];        // K, V
+  const int8_t* exps[2];
+  uint16_t* wide[2];
+  int* dev_error;
 };
 
 }  // namespace hb

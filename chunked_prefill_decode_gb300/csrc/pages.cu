@@ -1,0 +1,378 @@
+// pages.cu -- page bookkeeping on the GPU: block tables, slot maps and prefix
+// sums of a step built from its requests' lengths (hb_pages_assign), and the
+// pages of finished requests put back (hb_pages_release).
+//
+// "In-flight Batching", §KV Cache 管理的协同优化: fixed-size pages that a block
+// table maps, handed out as a sequence grows and freed when it finishes.  The
+// host builder (builder.cpp) keeps that list on the host; here it is a ring
+// of page ids in device memory, so that a loop whose lengths are known on the
+// GPU (or a captured graph) needs no trip to the host for its tables.
+//
+// The mathematics is two prefix sums over the sequences: cu[s], the new
+// tokens before s, and pg[s], the new pages before s, where s takes pages
+// first .. last-1 with first = ceil((ctx - q) / 16), last = ceil(ctx / 16).
+// Then everything is a direct lookup: logical page lp >= first of s is ring
+// entry head + pg[s] + lp - first, and token t of s sits at position
+// ctx - q + t - cu[s].  So no CTA reads what another one writes: each CTA
+// stages the lengths in shared memory, takes both sums for itself (a few
+// microseconds at thousands of sequences, far less than a second launch or a
+// grid-wide wait) and then writes its share of the tokens and of the pages.
+//
+// The ring's head and tail may be read and written in place: every CTA reads
+// them first, then counts itself in; the last one to do so writes them back.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+
+#include "hb.h"
+#include "hb_internal.h"
+#include "ptx.cuh"
+
+namespace hb {
+
+hb_status internal_fail(hb_status s, const char* msg);
+hb_status internal_ok();
+hb_status internal_device(int** err, int* num_sms);
+void internal_count_launch();
+void internal_note_other_launch(void* stream);
+
+namespace {
+
+constexpr int kPagesThreads = 512;
+constexpr int kPagesMaxSeqs = 16384;      // three int32 per sequence in shared memory
+
+struct PagesParams {
+  const int32_t* q_len;                   // NULL: release
+  const int32_t* ctx;                     // context lengths, or lengths to release
+  int32_t num_seqs, max_tokens, max_pages_per_seq, num_pages;
+  const int64_t* state_in;
+  int64_t* state_out;
+  int32_t* ring;
+  int32_t* block_table;
+  int32_t* cu_q_len;
+  int64_t* slot_map;
+  int* dev_error;
+};
+
+// What the sums need and give: s_q[s] becomes cu[s], s_pg[s] becomes pg[s]
+// (both with the total at [S]); s_off[s] = ctx - q.  Returns 0, or the error
+// for lengths outside 0 <= q <= ctx <= table room (which every CTA finds
+// alike, so that nothing is written then).
+struct Sums {
+  int32_t *s_q, *s_pg, *s_off;
+  int64_t tokens, pages;
+};
+
+__device__ int prefix_sums(const PagesParams& p, Sums& a) {
+  __shared__ int64_t w_q[kPagesThreads / 32], w_pg[kPagesThreads / 32];
+  const int S = p.num_seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t room = (int64_t)p.max_pages_per_seq * kPageSize;
+  int bad = 0;
+  for (int s = tid; s < S; s += kPagesThreads) {
+    const int ctx = p.ctx[s];
+    const int q = p.q_len ? p.q_len[s] : ctx;
+    if (q < 0 || ctx < q || ctx > room) {
+      bad = 1;
+      continue;
+    }
+    const int off = ctx - q;
+    a.s_q[s] = p.q_len ? q : 0;   // (a release counts pages only)
+    // (in 64 bits: a length near 2^31 must not wrap)
+    a.s_pg[s] = (int32_t)(((int64_t)ctx + kPageSize - 1) / kPageSize -
+                          ((int64_t)off + kPageSize - 1) / kPageSize);
+    a.s_off[s] = off;
+  }
+  if (__syncthreads_or(bad)) return HB_DEVERR_LENGTHS;
+  // each thread sums a run of sequences, the block scans the runs
+  const int per = (S + kPagesThreads - 1) / kPagesThreads;
+  const int s0 = min(S, tid * per), s1 = min(S, s0 + per);
+  int64_t q = 0, pg = 0;
+  for (int s = s0; s < s1; ++s) {
+    q += a.s_q[s];
+    pg += a.s_pg[s];
+  }
+  int64_t iq = q, ipg = pg;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, iq, d), y = __shfl_up_sync(0xffffffffu, ipg, d);
+    if (lane >= d) {
+      iq += x;
+      ipg += y;
+    }
+  }
+  if (lane == 31) {
+    w_q[warp] = iq;
+    w_pg[warp] = ipg;
+  }
+  __syncthreads();
+  int64_t bq = 0, bpg = 0, tq = 0, tpg = 0;
+#pragma unroll
+  for (int w = 0; w < kPagesThreads / 32; ++w) {
+    if (w < warp) {
+      bq += w_q[w];
+      bpg += w_pg[w];
+    }
+    tq += w_q[w];
+    tpg += w_pg[w];
+  }
+  a.tokens = tq;
+  a.pages = tpg;
+  // sums past 32 bits are refused by the caller, so what is stored fits
+  if (tq > INT_MAX || tpg > INT_MAX) return HB_DEVERR_LENGTHS;
+  int32_t rq = (int32_t)(bq + iq - q), rpg = (int32_t)(bpg + ipg - pg);
+  for (int s = s0; s < s1; ++s) {
+    const int32_t x = a.s_q[s], y = a.s_pg[s];
+    a.s_q[s] = rq;
+    a.s_pg[s] = rpg;
+    rq += x;
+    rpg += y;
+  }
+  if (tid == 0) {
+    a.s_q[S] = (int32_t)tq;
+    a.s_pg[S] = (int32_t)tpg;
+  }
+  __syncthreads();
+  return 0;
+}
+
+// the largest s in 0 .. S-1 with sums[s] <= x (x below the total: the
+// sequence that owns x, empty ones skipped)
+__device__ __forceinline__ int owner(const int32_t* sums, int S, int x) {
+  int lo = 0, hi = S - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (sums[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Head and tail as they were before the launch; every CTA then counts itself
+// in, and the last one writes them back moved by `dh` / `dt`.
+__device__ void read_state(const PagesParams& p, int64_t* s_state) {
+  if (threadIdx.x == 0) {
+    s_state[0] = __ldcg(p.state_in);
+    s_state[1] = __ldcg(p.state_in + 1);
+  }
+  __syncthreads();
+}
+__device__ void write_state(const PagesParams& p, const int64_t* s_state, int64_t dh, int64_t dt) {
+  if (threadIdx.x != 0) return;
+  bool last = gridDim.x == 1;
+  if (!last) {
+    __threadfence();
+    last = atomicAdd(reinterpret_cast<unsigned long long*>(p.state_out + 2), 1ull) + 1ull == gridDim.x;
+    __threadfence();
+  }
+  if (last) {
+    p.state_out[0] = s_state[0] + dh;
+    p.state_out[1] = s_state[1] + dt;
+    p.state_out[2] = 0;
+    p.state_out[3] = 0;
+  }
+}
+
+__global__ void __launch_bounds__(kPagesThreads) pages_assign_kernel(const PagesParams p) {
+  extern __shared__ int32_t s_dyn[];
+  __shared__ int64_t s_state[2];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int S = p.num_seqs;
+  Sums a{s_dyn, s_dyn + S + 1, s_dyn + 2 * (S + 1), 0, 0};
+  read_state(p, s_state);
+  int err = prefix_sums(p, a);
+  const int64_t head = s_state[0], tail = s_state[1];
+  if (!err && (head < 0 || tail < head || tail - head > p.num_pages || a.tokens > p.max_tokens))
+    err = HB_DEVERR_LENGTHS;
+  const bool lengths_ok = !err;
+  if (!err && a.pages > tail - head) err = HB_DEVERR_PAGES;
+  write_state(p, s_state, err ? 0 : a.pages, 0);
+  if (err && blockIdx.x == 0 && threadIdx.x == 0) report_error(p.dev_error, err);
+  if (!lengths_ok) return;
+
+  const int64_t first_thread = (int64_t)blockIdx.x * kPagesThreads + threadIdx.x;
+  const int64_t step = (int64_t)gridDim.x * kPagesThreads;
+  for (int64_t s = first_thread; s <= S; s += step) p.cu_q_len[s] = S > 0 ? a.s_q[s] : 0;
+  if (S == 0) return;
+  const int32_t* cu = a.s_q;
+  if (err) {   // too few pages: no table entry changes, and no token has a slot
+    if (p.slot_map)
+      for (int64_t t = first_thread; t < a.tokens; t += step) p.slot_map[t] = -1;
+    return;
+  }
+  const int64_t at0 = head % p.num_pages;
+  // ring entry k past the head (k below the pages taken, so at most one wrap)
+  auto fresh_page = [&](int64_t k) -> int {
+    int64_t i = at0 + k;
+    if (i >= p.num_pages) i -= p.num_pages;
+    const int page = __ldcg(p.ring + i);
+    return (unsigned)page < (unsigned)p.num_pages ? page : -1;
+  };
+  // table entries of the pages taken
+  for (int64_t k = first_thread; k < a.pages; k += step) {
+    const int s = owner(a.s_pg, S, (int)k);
+    const int lp = (a.s_off[s] + kPageSize - 1) / kPageSize + (int)k - a.s_pg[s];
+    const int page = fresh_page(k);
+    if (page < 0) report_error(p.dev_error, HB_DEVERR_INDEX);
+    p.block_table[(size_t)s * p.max_pages_per_seq + lp] = page;
+  }
+  if (!p.slot_map) return;
+  for (int64_t t = first_thread; t < a.tokens; t += step) {
+    const int s = owner(cu, S, (int)t);
+    const int off = a.s_off[s];
+    const int pos = off + (int)t - cu[s];
+    const int lp = pos / kPageSize, first = (off + kPageSize - 1) / kPageSize;
+    int page;
+    if (lp >= first) {
+      page = fresh_page((int64_t)a.s_pg[s] + lp - first);
+    } else {
+      page = p.block_table[(size_t)s * p.max_pages_per_seq + lp];
+      if ((unsigned)page >= (unsigned)p.num_pages) page = -1;
+    }
+    if (page < 0) report_error(p.dev_error, HB_DEVERR_INDEX);
+    p.slot_map[t] = page < 0 ? -1 : (int64_t)page * kPageSize + pos % kPageSize;
+  }
+}
+
+__global__ void __launch_bounds__(kPagesThreads) pages_release_kernel(const PagesParams p) {
+  extern __shared__ int32_t s_dyn[];
+  __shared__ int64_t s_state[2];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int S = p.num_seqs;
+  Sums a{s_dyn, s_dyn + S + 1, s_dyn + 2 * (S + 1), 0, 0};
+  read_state(p, s_state);
+  int err = prefix_sums(p, a);
+  const int64_t head = s_state[0], tail = s_state[1];
+  if (!err && (head < 0 || tail < head || tail - head > p.num_pages ||
+               a.pages > p.num_pages - (tail - head)))
+    err = HB_DEVERR_LENGTHS;
+  write_state(p, s_state, 0, err ? 0 : a.pages);
+  if (err) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) report_error(p.dev_error, err);
+    return;
+  }
+  const int64_t at0 = tail % p.num_pages;
+  const int64_t step = (int64_t)gridDim.x * kPagesThreads;
+  for (int64_t k = (int64_t)blockIdx.x * kPagesThreads + threadIdx.x; k < a.pages; k += step) {
+    const int s = owner(a.s_pg, S, (int)k);
+    int page = p.block_table[(size_t)s * p.max_pages_per_seq + (int)k - a.s_pg[s]];
+    if ((unsigned)page >= (unsigned)p.num_pages) {
+      report_error(p.dev_error, HB_DEVERR_INDEX);
+      page = -1;   // found again by the call that would hand it out
+    }
+    int64_t i = at0 + k;
+    if (i >= p.num_pages) i -= p.num_pages;
+    p.ring[i] = page;
+  }
+}
+
+hb_status check_common(int32_t num_seqs, int32_t max_pages_per_seq, int32_t num_pages, int32_t page_size,
+                       const void* lens, const void* ring, const void* state_in, const void* state_out,
+                       const void* block_table) {
+  if (num_seqs < 0) return internal_fail(HB_ERR_SHAPE, "num_seqs must be >= 0");
+  if (num_seqs > kPagesMaxSeqs) return internal_fail(HB_ERR_UNSUPPORTED, "num_seqs above 16384");
+  if (page_size != kPageSize) return internal_fail(HB_ERR_UNSUPPORTED, "only page_size 16 is built");
+  if (max_pages_per_seq <= 0 || num_pages <= 0)
+    return internal_fail(HB_ERR_SHAPE, "max_pages_per_seq and num_pages must be > 0");
+  if ((int64_t)max_pages_per_seq * kPageSize > INT_MAX || (int64_t)num_pages * kPageSize > INT_MAX)
+    return internal_fail(HB_ERR_UNSUPPORTED, "max_pages_per_seq or num_pages too large");
+  if (num_seqs > 0 && (!lens || !block_table))
+    return internal_fail(HB_ERR_INVALID_ARG, "the length arrays and block_table must be non-NULL");
+  if (!ring || !state_in || !state_out)
+    return internal_fail(HB_ERR_INVALID_ARG, "free_pages, state_in and state_out must be non-NULL");
+  if ((reinterpret_cast<uintptr_t>(lens) | reinterpret_cast<uintptr_t>(ring) |
+       reinterpret_cast<uintptr_t>(block_table)) & 3u)
+    return internal_fail(HB_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(state_in) | reinterpret_cast<uintptr_t>(state_out)) & 7u)
+    return internal_fail(HB_ERR_INVALID_ARG, "state_in and state_out must be 8-byte aligned");
+  return HB_OK;
+}
+
+using Kernel = void (*)(const PagesParams);
+
+// One CTA per kPagesThreads * 4 elements, at most two per SM.
+hb_status launch(Kernel kernel, PagesParams& p, int64_t elements, void* stream, const char* what) {
+  int num_sms = 0;
+  const hb_status s = internal_device(&p.dev_error, &num_sms);
+  if (s != HB_OK) return s;
+  const int64_t want = (elements + 4 * kPagesThreads - 1) / (4 * kPagesThreads);
+  const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(want, 2LL * num_sms));
+  const size_t smem = 3 * ((size_t)p.num_seqs + 1) * sizeof(int32_t);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  if (e == cudaSuccess)
+    e = launch_serialized(kernel, grid, kPagesThreads, smem, static_cast<cudaStream_t>(stream), p);
+  if (e != cudaSuccess) return internal_fail(HB_ERR_CUDA, what);
+  internal_note_other_launch(stream);
+  internal_count_launch();
+  return internal_ok();
+}
+
+}  // namespace
+}  // namespace hb
+
+using namespace hb;
+
+extern "C" hb_status hb_pages_assign(int32_t num_seqs, int32_t max_tokens, int32_t max_pages_per_seq,
+                                     int32_t num_pages, int32_t page_size, const int32_t* q_len,
+                                     const int32_t* context_len, const int32_t* free_pages,
+                                     const int64_t* state_in, int64_t* state_out,
+                                     int32_t* block_table, int32_t* cu_q_len, int64_t* slot_map,
+                                     void* stream) {
+  try {
+    hb_status s = check_common(num_seqs, max_pages_per_seq, num_pages, page_size, context_len,
+                               free_pages, state_in, state_out, block_table);
+    if (s != HB_OK) return s;
+    if (max_tokens < 0) return internal_fail(HB_ERR_SHAPE, "max_tokens must be >= 0");
+    if (!cu_q_len || (num_seqs > 0 && !q_len))
+      return internal_fail(HB_ERR_INVALID_ARG, "q_len and cu_q_len must be non-NULL");
+    if ((reinterpret_cast<uintptr_t>(q_len) | reinterpret_cast<uintptr_t>(cu_q_len)) & 3u)
+      return internal_fail(HB_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+    if (reinterpret_cast<uintptr_t>(slot_map) & 7u)
+      return internal_fail(HB_ERR_INVALID_ARG, "slot_map must be 8-byte aligned");
+    PagesParams p{};
+    p.q_len = q_len;
+    p.ctx = context_len;
+    p.num_seqs = num_seqs;
+    p.max_tokens = max_tokens;
+    p.max_pages_per_seq = max_pages_per_seq;
+    p.num_pages = num_pages;
+    p.state_in = state_in;
+    p.state_out = state_out;
+    p.ring = const_cast<int32_t*>(free_pages);
+    p.block_table = block_table;
+    p.cu_q_len = cu_q_len;
+    p.slot_map = slot_map;
+    // tokens for the slots, at least one page per 16 of them and sequence
+    const int64_t elements = (slot_map ? (int64_t)max_tokens : (int64_t)max_tokens / kPageSize) + num_seqs;
+    return launch(pages_assign_kernel, p, elements, stream, "pages_assign launch failed");
+  } catch (...) {
+    return internal_fail(HB_ERR_CUDA, "unexpected exception in hb_pages_assign");
+  }
+}
+
+extern "C" hb_status hb_pages_release(int32_t num_seqs, int32_t max_pages_per_seq, int32_t num_pages,
+                                      int32_t page_size, const int32_t* lengths,
+                                      const int32_t* block_table, int32_t* free_pages,
+                                      const int64_t* state_in, int64_t* state_out, void* stream) {
+  try {
+    hb_status s = check_common(num_seqs, max_pages_per_seq, num_pages, page_size, lengths,
+                               free_pages, state_in, state_out, block_table);
+    if (s != HB_OK) return s;
+    PagesParams p{};
+    p.ctx = lengths;
+    p.num_seqs = num_seqs;
+    p.max_pages_per_seq = max_pages_per_seq;
+    p.num_pages = num_pages;
+    p.state_in = state_in;
+    p.state_out = state_out;
+    p.ring = free_pages;
+    p.block_table = const_cast<int32_t*>(block_table);
+    // the lengths are on the GPU: at most every page comes back
+    const int64_t elements =
+        std::min<int64_t>(num_pages, (int64_t)num_seqs * max_pages_per_seq) + num_seqs;
+    return launch(pages_release_kernel, p, elements, stream, "pages_release launch failed");
+  } catch (...) {
+    return internal_fail(HB_ERR_CUDA, "unexpected exception in hb_pages_release");
+  }
+}

@@ -61,7 +61,8 @@ EXPORTED = (
     "hb_builder_free_list", "hb_builder_last_error", "hb_decode_attention_noalloc",
     "hb_selftest_wait_timeout", "hb_selftest_flag_timeout", "hb_linear", "hb_linear_workspace_size",
     "hb_timing_durations", "hb_step_layout", "hb_step_slot_create", "hb_step_slot_destroy",
-    "hb_step_slot_sync", "hb_step",
+    "hb_step_slot_sync", "hb_step", "hb_kv8_append", "hb_kv8_plan", "hb_kv8_attention",
+    "hb_pages_assign", "hb_pages_release",
 )
 
 LINEAR_STORE, LINEAR_GATED, LINEAR_RESIDUAL = 0, 1, 2
@@ -142,6 +143,16 @@ def load():
     L.hb_step.restype = ctypes.c_int
     L.hb_step.argtypes = [P(HbBatch), vp, vp, i32, vp, P(HbStepBuffers), vp, vp,
                           ctypes.c_float, vp, vp, vp]
+    L.hb_kv8_append.restype = ctypes.c_int
+    L.hb_kv8_append.argtypes = [P(HbBatch), vp, vp, vp, vp, vp, vp, vp]
+    L.hb_kv8_plan.restype = ctypes.c_int
+    L.hb_kv8_plan.argtypes = [P(HbBatch), vp, vp, i32, vp, P(sz), vp, P(sz), vp]
+    L.hb_kv8_attention.restype = ctypes.c_int
+    L.hb_kv8_attention.argtypes = [P(HbBatch), vp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp]
+    L.hb_pages_assign.restype = ctypes.c_int
+    L.hb_pages_assign.argtypes = [i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.hb_pages_release.restype = ctypes.c_int
+    L.hb_pages_release.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
     L.hb_launch_count.restype = i64
     L.hb_launch_count.argtypes = []
     L.hb_builder_create.restype = ctypes.c_int
@@ -222,22 +233,25 @@ def hb_kv_append(batch, k_new, v_new, k_cache, v_cache, stream=None):
                                _bf16(v_cache, "v_cache"), _stream(stream)))
 
 
-def hb_plan_sizes(batch, q_len, context_len, num_sms):
+def hb_plan_sizes(batch, q_len, context_len, num_sms, kv8=False):
     """(plan_bytes, workspace_bytes) for the batch; host-only."""
     ql = np.ascontiguousarray(q_len, dtype=np.int32)
     cl = np.ascontiguousarray(context_len, dtype=np.int32)
     pb, wb = ctypes.c_size_t(0), ctypes.c_size_t(0)
-    _check(load().hb_plan(ctypes.byref(batch), _ptr(ql), _ptr(cl), int(num_sms), None,
-                          ctypes.byref(pb), None, ctypes.byref(wb), None))
+    call = load().hb_kv8_plan if kv8 else load().hb_plan
+    _check(call(ctypes.byref(batch), _ptr(ql), _ptr(cl), int(num_sms), None,
+                ctypes.byref(pb), None, ctypes.byref(wb), None))
     return pb.value, wb.value
 
 
 def hb_plan(batch, q_len, context_len, num_sms, workspace=None, stream=None,
-            plan=None, upload=True):
+            plan=None, upload=True, kv8=False):
     """Write the plan; returns (plan as a host uint8 array, device workspace).
 
     `workspace` (a uint8 device tensor) is allocated when None or too small.
-    With upload=False only the host plan is built (no CUDA call)."""
+    With upload=False only the host plan is built (no CUDA call).  kv8: the
+    plan of the 8-bit cache's attention (hb_kv8_plan)."""
+    call = load().hb_kv8_plan if kv8 else load().hb_plan
     ql = np.ascontiguousarray(q_len, dtype=np.int32)
     cl = np.ascontiguousarray(context_len, dtype=np.int32)
     if plan is not None and (workspace is not None or not upload):
@@ -246,14 +260,14 @@ def hb_plan(batch, q_len, context_len, num_sms, workspace=None, stream=None,
         ws = workspace if upload else None
         pb = ctypes.c_size_t(plan.nbytes)
         wb = ctypes.c_size_t(ws.numel() if ws is not None else 0)
-        st = load().hb_plan(ctypes.byref(batch), _ptr(ql), _ptr(cl), int(num_sms), _ptr(plan),
-                            ctypes.byref(pb), _ptr(ws), ctypes.byref(wb),
-                            _stream(stream) if upload else None)
+        st = call(ctypes.byref(batch), _ptr(ql), _ptr(cl), int(num_sms), _ptr(plan),
+                  ctypes.byref(pb), _ptr(ws), ctypes.byref(wb),
+                  _stream(stream) if upload else None)
         if st == 0:
             return plan, ws
         if st != 4:   # anything but HB_ERR_WORKSPACE
             _check(st)
-    need_p, need_w = hb_plan_sizes(batch, ql, cl, num_sms)
+    need_p, need_w = hb_plan_sizes(batch, ql, cl, num_sms, kv8)
     if plan is None or plan.nbytes < need_p:
         plan = np.zeros(need_p, dtype=np.uint8)
     if upload and (workspace is None or workspace.numel() < need_w):
@@ -262,9 +276,9 @@ def hb_plan(batch, q_len, context_len, num_sms, workspace=None, stream=None,
         workspace = None
     pb = ctypes.c_size_t(plan.nbytes)
     wb = ctypes.c_size_t(workspace.numel() if workspace is not None else 0)
-    _check(load().hb_plan(ctypes.byref(batch), _ptr(ql), _ptr(cl), int(num_sms),
-                          _ptr(plan), ctypes.byref(pb), _ptr(workspace),
-                          ctypes.byref(wb), _stream(stream) if upload else None))
+    _check(call(ctypes.byref(batch), _ptr(ql), _ptr(cl), int(num_sms),
+                _ptr(plan), ctypes.byref(pb), _ptr(workspace),
+                ctypes.byref(wb), _stream(stream) if upload else None))
     return plan, workspace
 
 
@@ -329,6 +343,111 @@ def hb_attention_new_kv(batch, plan, q, k_new, v_new, k_cache, v_cache, scale, o
                                       _bf16(k_cache, "k_cache"), _bf16(v_cache, "v_cache"),
                                       ctypes.c_float(scale), _bf16(out, "out"), _ptr(workspace),
                                       _stream(stream)))
+
+
+# ---------------------------------------------------------------- 8-bit cache
+def _tensor(t, name, dtype, shape):
+    """Pointer of a contiguous tensor of the given dtype and shape (None in the
+    shape: any size) on the current CUDA device."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor")
+    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} must have shape {tuple('*' if w is None else w for w in shape)}, "
+                         f"got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return _ptr(t)
+
+
+def _kv8_args(batch, k_cache, v_cache, k_exp, v_exp):
+    pool = (batch.num_pages, batch.page_size, batch.num_kv_heads, batch.head_dim)
+    exps = (batch.num_pages, batch.num_kv_heads)
+    return (_tensor(k_cache, "k_cache", torch.float8_e4m3fn, pool),
+            _tensor(v_cache, "v_cache", torch.float8_e4m3fn, pool),
+            _tensor(k_exp, "k_exp", torch.int8, exps), _tensor(v_exp, "v_exp", torch.int8, exps))
+
+
+def kv8_cache(num_pages, num_kv_heads, head_dim, page_size=16, device="cuda"):
+    """A zeroed 8-bit cache: (k_cache, v_cache, k_exp, v_exp)."""
+    pools = [torch.zeros(num_pages, page_size, num_kv_heads, head_dim, dtype=torch.uint8,
+                         device=device).view(torch.float8_e4m3fn) for _ in range(2)]
+    exps = [torch.zeros(num_pages, num_kv_heads, dtype=torch.int8, device=device) for _ in range(2)]
+    return (*pools, *exps)
+
+
+def hb_kv8_append(batch, k_new, v_new, k_cache, v_cache, k_exp, v_exp, stream=None):
+    """Quantise the batch's new K/V rows (bf16) into the 8-bit cache."""
+    new = (batch.total_q, batch.num_kv_heads, batch.head_dim)
+    _check(load().hb_kv8_append(ctypes.byref(batch), _tensor(k_new, "k_new", torch.bfloat16, new),
+                                _tensor(v_new, "v_new", torch.bfloat16, new),
+                                *_kv8_args(batch, k_cache, v_cache, k_exp, v_exp), _stream(stream)))
+
+
+def hb_kv8_plan(batch, q_len, context_len, num_sms, workspace=None, stream=None, plan=None,
+                upload=True):
+    """hb_plan for hb_kv8_attention."""
+    return hb_plan(batch, q_len, context_len, num_sms, workspace, stream, plan, upload, kv8=True)
+
+
+def hb_kv8_attention(batch, plan, q, k_cache, v_cache, k_exp, v_exp, scale, out, workspace,
+                     stream=None):
+    """hb_attention over the 8-bit cache."""
+    rows = (batch.total_q, batch.num_q_heads, batch.head_dim)
+    need = plan_header(plan)["ws_total"]
+    if workspace is not None and workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace has {workspace.numel()} bytes, the plan needs {need}")
+    _check(load().hb_kv8_attention(ctypes.byref(batch), _ptr(plan),
+                                   _tensor(q, "q", torch.bfloat16, rows),
+                                   *_kv8_args(batch, k_cache, v_cache, k_exp, v_exp),
+                                   ctypes.c_float(scale), _tensor(out, "out", torch.bfloat16, rows),
+                                   _ptr(workspace), _stream(stream)))
+
+
+# ---------------------------------------------------------------- pages on the GPU
+def pages_ring(num_pages, page_order=None, device="cuda"):
+    """A ring with every page free: (free_pages, state) for hb_pages_*."""
+    ring = torch.arange(num_pages, dtype=torch.int32) if page_order is None else \
+        torch.as_tensor(page_order, dtype=torch.int32)
+    if ring.numel() != num_pages:
+        raise ValueError("page_order must list every page")
+    return ring.to(device), torch.tensor([0, num_pages, 0, 0], dtype=torch.int64, device=device)
+
+
+def hb_pages_assign(q_len, context_len, free_pages, state_in, state_out, block_table, cu_q_len,
+                    slot_map=None, page_size=16, stream=None):
+    """Block-table entries, prefix sums and (if given) slots of a step from its
+    lengths on the GPU, with pages taken from the ring free_pages / state_in
+    (state_out receives the ring's new state and may be state_in)."""
+    n = q_len.numel()
+    _check(load().hb_pages_assign(
+        n, slot_map.numel() if slot_map is not None else 0x7fffffff,
+        block_table.shape[1] if block_table.dim() == 2 else 0, free_pages.numel(), int(page_size),
+        _tensor(q_len, "q_len", torch.int32, (n,)),
+        _tensor(context_len, "context_len", torch.int32, (n,)),
+        _tensor(free_pages, "free_pages", torch.int32, (None,)),
+        _tensor(state_in, "state_in", torch.int64, (4,)),
+        _tensor(state_out, "state_out", torch.int64, (4,)),
+        _tensor(block_table, "block_table", torch.int32, (n, None)),
+        _tensor(cu_q_len, "cu_q_len", torch.int32, (n + 1,)),
+        _tensor(slot_map, "slot_map", torch.int64, (None,)) if slot_map is not None else None,
+        _stream(stream)))
+
+
+def hb_pages_release(lengths, free_pages, state_in, state_out, block_table, page_size=16,
+                     stream=None):
+    """The pages of the sequences with lengths > 0 (tokens in the cache) go back
+    to the ring."""
+    n = lengths.numel()
+    _check(load().hb_pages_release(
+        n, block_table.shape[1] if block_table.dim() == 2 else 0, free_pages.numel(),
+        int(page_size), _tensor(lengths, "lengths", torch.int32, (n,)),
+        _tensor(block_table, "block_table", torch.int32, (n, None)),
+        _tensor(free_pages, "free_pages", torch.int32, (None,)),
+        _tensor(state_in, "state_in", torch.int64, (4,)),
+        _tensor(state_out, "state_out", torch.int64, (4,)), _stream(stream)))
 
 
 def hb_decode_attention_noalloc(batch, q_len, context_len, q, k_cache, v_cache, scale,

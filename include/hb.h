@@ -78,7 +78,8 @@ typedef enum hb_status {
   HB_ERR_CUDA = 5,          /* a CUDA runtime/driver call failed             */
   HB_ERR_DEVICE_INDEX = 6,  /* a kernel met an out-of-range page index       */
   HB_ERR_TIMEOUT = 7,       /* a kernel wait gave up                         */
-  HB_ERR_OUT_OF_PAGES = 8   /* batch builder: no free page for a decode      */
+  HB_ERR_OUT_OF_PAGES = 8   /* batch builder: no free page for a decode;      */
+                            /* hb_pages_assign: too few free pages            */
 } hb_status;
 
 /* Message for the last failed call on this thread ("" if none).  The string
@@ -244,6 +245,119 @@ hb_status hb_decode_attention_noalloc(const hb_batch* batch,
                                       void* out, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * The 8-bit KV cache.  Half the bytes of the bf16 cache, for the same batch
+ * descriptors, shapes (sliding windows included) and page layout:
+ *   k_cache, v_cache device, [num_pages, 16, Hkv, D] e4m3 (the finite-only
+ *                    8-bit float: 4 significant bits, +-448, NaN, no infinity),
+ *                    16-byte aligned
+ *   k_exp, v_exp     device, [num_pages, Hkv] int8: an element of page p and
+ *                    kv head h stands for value * 2^exp[p, h]; exponents are
+ *                    read as if held to [-64, 64]
+ * Call order as with the bf16 cache: hb_kv8_append, then hb_kv8_attention
+ * with a plan of hb_kv8_plan.  Cited passages as for hb_kv_append and
+ * hb_attention (the pages do not speak of quantised caches).
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Quantising append.  For every page and kv head that receives new tokens,
+ * with need = the smallest e in [-64, 64] such that the largest |x| of the
+ * new finite elements is <= 448 * 2^e (-64 if they are all zero; 64 if none
+ * reaches):
+ *   - a page whose first slot is new gets exp = need; a page that holds older
+ *     tokens of the sequence gets exp = max(its old exp, need), and if that
+ *     grew, the older elements become round(value * 2^(old exp - exp));
+ *   - a new element becomes round(x * 2^-exp), held to +-448; infinities and
+ *     NaN become NaN and do not count towards need.
+ * Rounding is to nearest even.  Other pages are not written; slots of a page
+ * behind the sequence's last token keep their bytes.  A page must belong to
+ * one sequence's new tokens only (a prefix may be shared between sequences
+ * in whole pages that no batch row appends to).
+ *   k_new, v_new     device, [total_q, Hkv, D] bf16, 16-byte aligned
+ * Errors as hb_kv_append; HB_ERR_INVALID_ARG for NULL exponents.
+ */
+hb_status hb_kv8_append(const hb_batch* batch, const void* k_new, const void* v_new,
+                        void* k_cache, void* v_cache, int8_t* k_exp, int8_t* v_exp,
+                        void* stream);
+
+/* hb_plan for hb_kv8_attention (same arguments, rules and errors).  A plan
+ * serves one of the two: hb_attention refuses this one, hb_kv8_attention
+ * refuses hb_plan's (HB_ERR_WORKSPACE).  The workspace also holds the chunk
+ * rows' pages as bf16 (4 * Hkv * D bytes per visible token of theirs). */
+hb_status hb_kv8_plan(const hb_batch* batch, const int32_t* h_q_len,
+                      const int32_t* h_context_len, int32_t num_sms, void* h_plan,
+                      size_t* plan_bytes, void* d_workspace, size_t* workspace_bytes,
+                      void* stream);
+
+/* hb_attention over the 8-bit cache: the same result, of the elements' values,
+ * with the same masks, precision and errors; HB_ERR_INVALID_ARG for a
+ * softmax_scale that is not positive and finite.  What unwritten slots of a
+ * page hold (NaN included) never shows. */
+hb_status hb_kv8_attention(const hb_batch* batch, const void* h_plan, const void* q,
+                           const void* k_cache, const void* v_cache, const int8_t* k_exp,
+                           const int8_t* v_exp, float softmax_scale, void* out,
+                           void* d_workspace, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Page bookkeeping on the GPU: what hb_builder_* keeps on the host, for loops
+ * whose lengths are known on the device.  "In-flight Batching", §KV Cache
+ * 管理的协同优化: fixed-size pages handed out as sequences grow and freed when
+ * they finish.
+ *
+ * The free pages are a ring in device memory: free_pages [num_pages] int32
+ * and a state of four int64: state[0] pages taken so far (head), state[1]
+ * pages put in so far (tail), 0 <= head <= tail <= head + num_pages;
+ * the free pages are free_pages[i % num_pages] for head <= i < tail, taken in
+ * that order.  state[2] and state[3] must be zero before the first call and
+ * are left zero (a full pool starts as free_pages = 0 .. num_pages-1, state =
+ * {0, num_pages, 0, 0}).  state_in is read and state_out written (its four
+ * entries); both may be the same array.  Calls on one ring must be ordered.
+ *
+ * Lengths are read on the device, so mistakes in them are found there: the
+ * call then changes nothing but the error word (state_out = state_in), and
+ * hb_check() gives HB_ERR_SHAPE, or HB_ERR_OUT_OF_PAGES where only the free
+ * pages were too few.  num_seqs is at most 16384 (HB_ERR_UNSUPPORTED).
+ * ------------------------------------------------------------------------- */
+
+/*
+ * For sequences with q_len[s] new tokens of context_len[s] after them (both
+ * device int32, 0 <= q_len <= context_len <= max_pages_per_seq * 16; q_len 0:
+ * a row that stands still):
+ *   cu_q_len     [num_seqs+1] receives the prefix sums of q_len
+ *   block_table  [num_seqs, max_pages_per_seq]: the entries of the logical
+ *                pages that hold only new tokens, ceil((context_len - q_len)
+ *                / 16) up to ceil(context_len / 16), receive pages from the
+ *                ring, sequence by sequence in ascending order; the others
+ *                stay as they are
+ *   slot_map     [max_tokens] int64 or NULL: entry t receives page * 16 + slot
+ *                of the t-th new token of the batch; entries behind the last
+ *                token stay as they are
+ * The sum of q_len must not exceed max_tokens.  With too few free pages
+ * cu_q_len is written, block_table and the ring are not, and the tokens'
+ * slots are -1.  A ring entry (or, for a token on an older page, a table
+ * entry) outside [0, num_pages) becomes -1 and is reported by hb_check() as
+ * HB_ERR_DEVICE_INDEX.
+ */
+hb_status hb_pages_assign(int32_t num_seqs, int32_t max_tokens, int32_t max_pages_per_seq,
+                          int32_t num_pages, int32_t page_size, const int32_t* q_len,
+                          const int32_t* context_len, const int32_t* free_pages,
+                          const int64_t* state_in, int64_t* state_out, int32_t* block_table,
+                          int32_t* cu_q_len, int64_t* slot_map, void* stream);
+
+/*
+ * The pages of finished sequences go back to the end of the ring: the first
+ * ceil(lengths[s] / 16) entries of block_table row s, row by row in ascending
+ * order (lengths: device int32, tokens in the cache, 0 for a row that keeps
+ * its pages; the table is not changed).  Pages shared with a live sequence
+ * must not be released.  HB_ERR_SHAPE by hb_check() if more come back than
+ * were taken; a table entry outside [0, num_pages) is reported as
+ * HB_ERR_DEVICE_INDEX and goes in as -1.
+ */
+hb_status hb_pages_release(int32_t num_seqs, int32_t max_pages_per_seq, int32_t num_pages,
+                           int32_t page_size, const int32_t* lengths, const int32_t* block_table,
+                           int32_t* free_pages, const int64_t* state_in, int64_t* state_out,
+                           void* stream);
+
+/* ---------------------------------------------------------------------------
  * One step from host memory.  For a serving loop that keeps a few steps in
  * flight: the step's inputs cross the host link as one packed block, the
  * plan goes up ahead of them on the input-copy stream, hb_kv_append and
@@ -318,8 +432,9 @@ hb_status hb_step(const hb_batch* shape, const int32_t* h_q_len,
 
 /*
  * Synchronise `stream`, then read and clear the device error word of the
- * current device: HB_OK, HB_ERR_DEVICE_INDEX or HB_ERR_TIMEOUT (or
- * HB_ERR_CUDA if the stream itself failed).  Blocking.
+ * current device: HB_OK, HB_ERR_DEVICE_INDEX or HB_ERR_TIMEOUT, after
+ * hb_pages_* also HB_ERR_OUT_OF_PAGES or HB_ERR_SHAPE (or HB_ERR_CUDA if the
+ * stream itself failed).  Blocking.
  */
 hb_status hb_check(void* stream);
 
@@ -395,8 +510,9 @@ size_t hb_linear_workspace_size(int32_t M, int32_t N, int32_t K, int32_t epilogu
 /* ---------------------------------------------------------------------------
  * Instrumentation.  When enabled, every kernel launch of this library is
  * bracketed by CUDA events recorded on its launch stream.
- *   kernel ids: 0 = kv append, 1 = attention (decode and chunk work in one
- *   launch), 2 = linear layer
+ *   kernel ids: 0 = kv append (either cache), 1 = attention (decode and chunk
+ *   work in one launch; over the 8-bit cache its widening launch is a record
+ *   of its own), 2 = linear layer; hb_pages_* are counted but not timed
  * ------------------------------------------------------------------------- */
 #define HB_NUM_KERNEL_IDS 3
 
