@@ -29,6 +29,11 @@ namespace hb {
 cudaError_t launch_kv_append(const AppendParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv8_append(Append8Params p, int head_dim, cudaStream_t stream);
 cudaError_t launch_kv8_widen(const WidenParams& p, cudaStream_t stream);
+cudaError_t launch_attention8(const DecodeParams& dec, const Decode8Params& dec8, int decode_grid,
+                              const ChunkParams& chk, int head_dim, const CUtensorMap& dec_k,
+                              const CUtensorMap& dec_v, const CUtensorMap& chunk_q,
+                              const CUtensorMap& chunk_k, const CUtensorMap& chunk_v,
+                              cudaStream_t stream, bool early, int pairs_mode);
 cudaError_t launch_linear(const LinearParams& p, const CUtensorMap& xmap, const CUtensorMap& wmap,
                           int num_sms, cudaStream_t stream);
 int linear_w_box_rows();
@@ -121,11 +126,13 @@ hb_status get_encoder() {
 
 hb_status encode_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
                      const cuuint64_t* strides_bytes, const cuuint32_t* box,
-                     const char* what) {
+                     const char* what,
+                     CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                     CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   cuuint32_t elem[5] = {1, 1, 1, 1, 1};
-  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
+  CUresult r = g_encode(map, type, (cuuint32_t)rank,
                         const_cast<void*>(base), dims, strides_bytes, box, elem,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(HB_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed: %d", what, (int)r);
@@ -437,7 +444,7 @@ hb_status internal_kv_append(const hb_batch* batch, const void* k_new, const voi
 hb_status internal_attention(const hb_batch* batch, const void* h_plan, const void* q,
                              const void* k_new, const void* v_new, const void* k_cache,
                              const void* v_cache, float softmax_scale, void* out,
-                             void* d_workspace, void* stream, bool kv8 = false);
+                             void* d_workspace, void* stream);
 
 }  // namespace hb
 
@@ -752,7 +759,7 @@ hb_status hb::internal_plan(const hb_batch* batch, const int32_t* h_q_len,
     double decode_bytes = 0.0;
     for (int i = 0; i < S; ++i)
       if (h_q_len[i] == 1)
-        decode_bytes += (double)(W > 0 ? std::min(h_context_len[i], W) : h_context_len[i]) * Hkv * D * 4.0;
+        decode_bytes += (double)(W > 0 ? std::min(h_context_len[i], W) : h_context_len[i]) * Hkv * D * (kv8 ? 2.0 : 4.0);
     auto t_decode = [&](int G) {
       return decode_bytes / std::min(kHbmBytesPerUs, G * kSmBytesPerUs);
     };
@@ -947,11 +954,12 @@ hb_status hb::internal_plan(const hb_batch* batch, const int32_t* h_q_len,
     const size_t n_off = (size_t)(part.grid + part.n_dynamic + 1);
     const int n_slots = part.n_slots, n_merge = part.n_merge;
 
-    // ---- 8-bit cache: the pages to widen, sequence by sequence
+    // ---- 8-bit cache: the chunk rows' pages to widen, sequence by sequence
     ps.widen.clear();
     int64_t widen_pages = 0;
     if (kv8) {
       for (int i = 0; i < S; ++i) {
+        if (h_q_len[i] == 1) continue;   // decode rows read the 8-bit pages
         const int first = W > 0 ? std::max(0, h_context_len[i] - h_q_len[i] - W + 1) / kPageSize : 0;
         ps.widen.push_back(WidenItem{i, first, (int32_t)widen_pages, 0});
         widen_pages += (h_context_len[i] + kPageSize - 1) / kPageSize - first;
@@ -1095,16 +1103,78 @@ hb_status hb_attention_new_kv(const hb_batch* batch, const void* h_plan, const v
 
 }  // extern "C"
 
+// ---------------------------------------------------------------- kernel parameters
+namespace {
+
+// The decode rows' parameters, from a plan in workspace `ws`.
+void fill_decode(DecodeParams* dp, const PlanHeader& h, const hb_batch* batch, uint8_t* ws,
+                 const void* q, void* out, float scale_log2, const DevState* dev) {
+  dp->items = reinterpret_cast<const DecodeItem*>(ws);
+  dp->cta_offsets = reinterpret_cast<const int32_t*>(ws + h.ws_decode_offsets);
+  dp->num_static = h.decode_grid;
+  dp->num_dynamic = h.num_decode_dynamic;
+  dp->num_items = h.num_decode_items;
+  dp->counters = reinterpret_cast<int32_t*>(ws + h.ws_counters);
+  dp->part_o = reinterpret_cast<float*>(ws + h.ws_partial_o);
+  dp->part_ml = reinterpret_cast<float*>(ws + h.ws_partial_ml);
+  dp->cu_q_len = batch->cu_q_len;
+  dp->context_len = batch->context_len;
+  dp->block_table = batch->block_table;
+  dp->max_pages_per_seq = batch->max_pages_per_seq;
+  dp->num_pages = batch->num_pages;
+  dp->q = static_cast<const uint16_t*>(q);
+  dp->out = static_cast<uint16_t*>(out);
+  dp->num_q_heads = batch->num_q_heads;
+  dp->num_kv_heads = batch->num_kv_heads;
+  dp->scale_log2 = scale_log2;
+  dp->dev_error = dev->err;
+  dp->window = batch->sliding_window;
+}
+
+// The chunk rows' parameters, from a plan in workspace `ws`.
+void fill_chunk(ChunkParams* cp, const PlanHeader& h, const hb_batch* batch, uint8_t* ws, void* out,
+                float scale_log2, const DevState* dev) {
+  cp->items = reinterpret_cast<const ChunkItem*>(ws + (size_t)h.num_decode_items * sizeof(DecodeItem));
+  cp->num_items = h.num_chunk_items;
+  cp->cu_q_len = batch->cu_q_len;
+  cp->context_len = batch->context_len;
+  cp->block_table = batch->block_table;
+  cp->max_pages_per_seq = batch->max_pages_per_seq;
+  cp->num_pages = batch->num_pages;
+  cp->out = static_cast<uint16_t*>(out);
+  cp->num_q_heads = batch->num_q_heads;
+  cp->num_kv_heads = batch->num_kv_heads;
+  cp->tokens_per_tile = h.chunk_tokens_per_tile;
+  cp->scale_log2 = scale_log2;
+  cp->dev_error = dev->err;
+  cp->window = batch->sliding_window;
+  cp->counters = reinterpret_cast<int32_t*>(ws + h.ws_chunk_counters);
+  cp->part_o = reinterpret_cast<float*>(ws + h.ws_chunk_o);
+  cp->part_ml = reinterpret_cast<float*>(ws + h.ws_chunk_ml);
+}
+
+// q viewed as (D, head, token), one box per query tile and 64 head dims.
+hb_status encode_chunk_q(CUtensorMap* map, const hb_batch* batch, const PlanHeader& h, const void* q) {
+  const int Hq = batch->num_q_heads, D = batch->head_dim;
+  const cuuint64_t qdims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)batch->total_q};
+  const cuuint64_t qstr[2] = {(cuuint64_t)D * 2, (cuuint64_t)Hq * D * 2};
+  const cuuint32_t qbox[3] = {64, (cuuint32_t)(Hq / batch->num_kv_heads),
+                              (cuuint32_t)h.chunk_tokens_per_tile};
+  return encode_map(map, q, 3, qdims, qstr, qbox, "chunk Q");
+}
+
+}  // namespace
+
 // hb_attention; with k_new / v_new (the append's inputs) the chunk CTAs read
 // the pages that hold only new tokens from there
 hb_status hb::internal_attention(const hb_batch* batch, const void* h_plan, const void* q,
                                  const void* k_new, const void* v_new, const void* k_cache,
                                  const void* v_cache, float softmax_scale, void* out,
-                                 void* d_workspace, void* stream, bool kv8) {
-  NvtxRange range(kv8 ? "hb_kv8_attention" : "hb_attention");
+                                 void* d_workspace, void* stream) {
+  NvtxRange range("hb_attention");
   try {
     PlanHeader h;
-    hb_status s = check_planned(batch, h_plan, kv8, q, out, softmax_scale, &h);
+    hb_status s = check_planned(batch, h_plan, false, q, out, softmax_scale, &h);
     if (s != HB_OK || batch->total_q == 0) return s;
     if ((s = check_ptr(k_cache, "k_cache")) != HB_OK) return s;
     if ((s = check_ptr(v_cache, "v_cache")) != HB_OK) return s;
@@ -1145,35 +1215,12 @@ hb_status hb::internal_attention(const hb_batch* batch, const void* h_plan, cons
       const cuuint32_t box[4] = {64, (cuuint32_t)kPageSize, (cuuint32_t)kvhb, 1};
       if ((s = encode_map(&dec_k, k_cache, 4, dims, strides, box, "decode K")) != HB_OK) return s;
       if ((s = encode_map(&dec_v, v_cache, 4, dims, strides, box, "decode V")) != HB_OK) return s;
-      dp.items = reinterpret_cast<const DecodeItem*>(ws);
-      dp.cta_offsets = reinterpret_cast<const int32_t*>(ws + h.ws_decode_offsets);
-      dp.num_static = h.decode_grid;
-      dp.num_dynamic = h.num_decode_dynamic;
-      dp.num_items = h.num_decode_items;
-      dp.counters = reinterpret_cast<int32_t*>(ws + h.ws_counters);
-      dp.part_o = reinterpret_cast<float*>(ws + h.ws_partial_o);
-      dp.part_ml = reinterpret_cast<float*>(ws + h.ws_partial_ml);
-      dp.cu_q_len = batch->cu_q_len;
-      dp.context_len = batch->context_len;
-      dp.block_table = batch->block_table;
-      dp.max_pages_per_seq = batch->max_pages_per_seq;
-      dp.num_pages = batch->num_pages;
-      dp.q = static_cast<const uint16_t*>(q);
-      dp.out = static_cast<uint16_t*>(out);
-      dp.num_q_heads = Hq;
-      dp.num_kv_heads = Hkv;
-      dp.scale_log2 = scale_log2;
-      dp.dev_error = dev->err;
-      dp.window = batch->sliding_window;
+      fill_decode(&dp, h, batch, ws, q, out, scale_log2, dev);
     }
     ChunkParams cp{};
     cp.group = g;
     if (h.num_chunk_items > 0) {
-      const int tpt = h.chunk_tokens_per_tile;
-      const cuuint64_t qdims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)batch->total_q};
-      const cuuint64_t qstr[2] = {(cuuint64_t)D * 2, (cuuint64_t)Hq * D * 2};
-      const cuuint32_t qbox[3] = {64, (cuuint32_t)g, (cuuint32_t)tpt};
-      if ((s = encode_map(&chunk_q, q, 3, qdims, qstr, qbox, "chunk Q")) != HB_OK) return s;
+      if ((s = encode_chunk_q(&chunk_q, batch, h, q)) != HB_OK) return s;
       // pools viewed as (D, kv head, token slot) with one box per page
       const cuuint64_t kdims[3] = {(cuuint64_t)D, (cuuint64_t)Hkv,
                                    (cuuint64_t)batch->num_pages * kPageSize};
@@ -1194,23 +1241,7 @@ hb_status hb::internal_attention(const hb_batch* batch, const void* h_plan, cons
         chunk_knew = chunk_k;
         chunk_vnew = chunk_v;
       }
-      cp.items = reinterpret_cast<const ChunkItem*>(ws + (size_t)h.num_decode_items * sizeof(DecodeItem));
-      cp.num_items = h.num_chunk_items;
-      cp.cu_q_len = batch->cu_q_len;
-      cp.context_len = batch->context_len;
-      cp.block_table = batch->block_table;
-      cp.max_pages_per_seq = batch->max_pages_per_seq;
-      cp.num_pages = batch->num_pages;
-      cp.out = static_cast<uint16_t*>(out);
-      cp.num_q_heads = Hq;
-      cp.num_kv_heads = Hkv;
-      cp.tokens_per_tile = tpt;
-      cp.scale_log2 = scale_log2;
-      cp.dev_error = dev->err;
-      cp.window = batch->sliding_window;
-      cp.counters = reinterpret_cast<int32_t*>(ws + h.ws_chunk_counters);
-      cp.part_o = reinterpret_cast<float*>(ws + h.ws_chunk_o);
-      cp.part_ml = reinterpret_cast<float*>(ws + h.ws_chunk_ml);
+      fill_chunk(&cp, h, batch, ws, out, scale_log2, dev);
     }
     if (h.num_decode_items > 0 || h.num_chunk_items > 0) {
       const bool early = follows_own_append(stream, batch, k_cache, v_cache);
@@ -1276,7 +1307,14 @@ hb_status hb_kv8_append(const hb_batch* batch, const void* k_new, const void* v_
     cudaError_t e = launch_kv8_append(p, batch->head_dim, st);
     t.done();
     if (e != cudaSuccess) return cuda_fail(e, "kv8_append launch");
-    note_launch(stream, LastLaunch{});
+    LastLaunch rec;
+    rec.kind = kAppendLaunch;
+    rec.cu = batch->cu_q_len;
+    rec.ctx = batch->context_len;
+    rec.bt = batch->block_table;
+    rec.kc = k_cache;
+    rec.vc = v_cache;
+    note_launch(stream, rec);
     g_launches.fetch_add(1);
     return ok();
   } catch (...) {
@@ -1288,6 +1326,7 @@ hb_status hb_kv8_attention(const hb_batch* batch, const void* h_plan, const void
                            const void* k_cache, const void* v_cache, const int8_t* k_exp,
                            const int8_t* v_exp, float softmax_scale, void* out, void* d_workspace,
                            void* stream) {
+  NvtxRange range("hb_kv8_attention");
   try {
     PlanHeader h;
     hb_status s = check_planned(batch, h_plan, true, q, out, softmax_scale, &h);
@@ -1297,38 +1336,82 @@ hb_status hb_kv8_attention(const hb_batch* batch, const void* h_plan, const void
       return fail(HB_ERR_INVALID_ARG, "d_workspace must be non-NULL and 256-byte aligned");
     DevState* dev = nullptr;
     if ((s = device_state(&dev)) != HB_OK) return s;
+    if ((s = get_encoder()) != HB_OK) return s;
     Plan8 p8;
     std::memcpy(&p8, static_cast<const uint8_t*>(h_plan) + h.kv8, sizeof(p8));
+    const int Hkv = batch->num_kv_heads, D = batch->head_dim;
+    const float scale_log2 = softmax_scale * 1.4426950408889634f;
     uint8_t* ws = static_cast<uint8_t*>(d_workspace);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    WidenParams wp{};
-    wp.items = reinterpret_cast<const WidenItem*>(ws + p8.ws_widen_items);
-    wp.num_items = p8.num_widen;
-    wp.num_units = p8.widen_pages;
-    wp.block_table = batch->block_table;
-    wp.ws_table = reinterpret_cast<int32_t*>(ws + p8.ws_table);
-    wp.max_pages_per_seq = batch->max_pages_per_seq;
-    wp.num_pages = batch->num_pages;
-    wp.num_kv_heads = batch->num_kv_heads;
-    wp.head_dim = batch->head_dim;
-    wp.cache[0] = static_cast<const uint8_t*>(k_cache);
-    wp.cache[1] = static_cast<const uint8_t*>(v_cache);
-    wp.exps[0] = k_exp;
-    wp.exps[1] = v_exp;
-    wp.wide[0] = reinterpret_cast<uint16_t*>(ws + p8.ws_k);
-    wp.wide[1] = reinterpret_cast<uint16_t*>(ws + p8.ws_v);
-    wp.dev_error = dev->err;
+
+    CUtensorMap dec_k, dec_v, chunk_q, chunk_k, chunk_v;
+    for (CUtensorMap* m : {&dec_k, &dec_v, &chunk_q, &chunk_k, &chunk_v}) std::memset(m, 0, sizeof(*m));
+    DecodeParams dp{};
+    dp.group = batch->num_q_heads / Hkv;
+    dp.kvh_block = h.decode_kvh_block;
+    if (h.num_decode_items > 0) {
+      // as the bf16 maps of hb_attention, a whole head's bytes per box row
+      const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)kPageSize, (cuuint64_t)Hkv,
+                                  (cuuint64_t)batch->num_pages};
+      const cuuint64_t strides[3] = {(cuuint64_t)Hkv * D, (cuuint64_t)D, (cuuint64_t)kPageSize * Hkv * D};
+      const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)kPageSize, (cuuint32_t)dp.kvh_block, 1};
+      const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+      if ((s = encode_map(&dec_k, k_cache, 4, dims, strides, box, "decode K (8-bit)",
+                          CU_TENSOR_MAP_DATA_TYPE_UINT8, sw)) != HB_OK)
+        return s;
+      if ((s = encode_map(&dec_v, v_cache, 4, dims, strides, box, "decode V (8-bit)",
+                          CU_TENSOR_MAP_DATA_TYPE_UINT8, sw)) != HB_OK)
+        return s;
+      fill_decode(&dp, h, batch, ws, q, out, scale_log2, dev);
+    }
+    ChunkParams cp{};
+    cp.group = dp.group;
+    bool early = follows_own_append(stream, batch, k_cache, v_cache);
+    if (h.num_chunk_items > 0) {
+      WidenParams wp{};
+      wp.items = reinterpret_cast<const WidenItem*>(ws + p8.ws_widen_items);
+      wp.num_items = p8.num_widen;
+      wp.num_units = p8.widen_pages;
+      wp.block_table = batch->block_table;
+      wp.ws_table = reinterpret_cast<int32_t*>(ws + p8.ws_table);
+      wp.max_pages_per_seq = batch->max_pages_per_seq;
+      wp.num_pages = batch->num_pages;
+      wp.num_kv_heads = Hkv;
+      wp.head_dim = D;
+      wp.cache[0] = static_cast<const uint8_t*>(k_cache);
+      wp.cache[1] = static_cast<const uint8_t*>(v_cache);
+      wp.exps[0] = k_exp;
+      wp.exps[1] = v_exp;
+      wp.wide[0] = reinterpret_cast<uint16_t*>(ws + p8.ws_k);
+      wp.wide[1] = reinterpret_cast<uint16_t*>(ws + p8.ws_v);
+      wp.dev_error = dev->err;
+      if ((s = encode_chunk_q(&chunk_q, batch, h, q)) != HB_OK) return s;
+      const cuuint64_t kdims[3] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)p8.widen_pages * kPageSize};
+      const cuuint64_t kstr[2] = {(cuuint64_t)D * 2, (cuuint64_t)Hkv * D * 2};
+      const cuuint32_t kbox[3] = {64, 1, (cuuint32_t)kPageSize};
+      if ((s = encode_map(&chunk_k, wp.wide[0], 3, kdims, kstr, kbox, "chunk K (widened)")) != HB_OK) return s;
+      if ((s = encode_map(&chunk_v, wp.wide[1], 3, kdims, kstr, kbox, "chunk V (widened)")) != HB_OK) return s;
+      fill_chunk(&cp, h, batch, ws, out, scale_log2, dev);
+      cp.block_table = wp.ws_table;
+      cp.num_pages = p8.widen_pages;
+      LaunchTimer t(1, st);
+      cudaError_t e = launch_kv8_widen(wp, st);
+      t.done();
+      if (e != cudaSuccess) return cuda_fail(e, "kv8_widen launch");
+      note_launch(stream, LastLaunch{});
+      g_launches.fetch_add(1);
+      // the widening lets the next launch start once everything before it is
+      // complete, so only what reads its pages waits
+      early = true;
+    }
     LaunchTimer t(1, st);
-    cudaError_t e = launch_kv8_widen(wp, st);
+    cudaError_t e = launch_attention8(dp, Decode8Params{k_exp, v_exp}, h.decode_grid, cp, D, dec_k, dec_v,
+                                      chunk_q, chunk_k, chunk_v, st, early, h.chunk_pairs_only);
     t.done();
-    if (e != cudaSuccess) return cuda_fail(e, "kv8_widen launch");
+    if (e != cudaSuccess) return cuda_fail(e, "attention launch (8-bit)");
     note_launch(stream, LastLaunch{});
     g_launches.fetch_add(1);
-    hb_batch b = *batch;
-    b.block_table = wp.ws_table;
-    b.num_pages = p8.widen_pages;
-    return hb::internal_attention(&b, h_plan, q, nullptr, nullptr, wp.wide[0], wp.wide[1],
-                                  softmax_scale, out, d_workspace, stream, true);
+    return ok();
   } catch (...) {
     return fail(HB_ERR_CUDA, "unexpected exception in hb_kv8_attention");
   }

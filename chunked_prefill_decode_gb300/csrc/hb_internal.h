@@ -224,6 +224,12 @@ struct Append8Params {
   int* dev_error;
 };
 
+// What the decode rows of the 8-bit cache need besides DecodeParams.
+struct Decode8Params {
+  const int8_t* k_exp;    // [num_pages, Hkv]
+  const int8_t* v_exp;
+};
+
 // What an 8-bit plan adds to a plan (hb_kv8_plan): its host copy holds this
 // record behind the items (PlanHeader.kv8 = its offset, 0 in a bf16 plan).
 // The chunk rows' pages are spelt out as bf16 in the workspace before the

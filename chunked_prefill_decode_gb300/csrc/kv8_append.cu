@@ -78,8 +78,8 @@ __global__ void __launch_bounds__(kA8Threads) kv8_append_kernel(const Append8Par
   const bool staged = p.num_seqs <= kA8SmemSeqs;
   int32_t* s_ctx = s_cu + p.num_seqs + 1;
   if (staged) {
-    for (int i = threadIdx.x; i <= p.num_seqs; i += kA8Threads) s_cu[i] = __ldg(&p.cu_q_len[i]);
-    for (int i = threadIdx.x; i < p.num_seqs; i += kA8Threads) s_ctx[i] = __ldg(&p.context_len[i]);
+    for (int i = threadIdx.x; i <= p.num_seqs; i += kA8Threads) s_cu[i] = __ldcg(&p.cu_q_len[i]);
+    for (int i = threadIdx.x; i < p.num_seqs; i += kA8Threads) s_ctx[i] = __ldcg(&p.context_len[i]);
   }
   __syncthreads();
   const int32_t* cu = staged ? s_cu : p.cu_q_len;
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kA8Threads) kv8_append_kernel(const Append8Par
   // (lp < ceil(ctx / 16), without adding to a length near 2^31)
   if (lp > (ctx - 1) / kPageSize) return;
   int page = -1;
-  if (lp < p.max_pages_per_seq) page = __ldg(&p.block_table[(size_t)s * p.max_pages_per_seq + lp]);
+  if (lp < p.max_pages_per_seq) page = __ldcg(&p.block_table[(size_t)s * p.max_pages_per_seq + lp]);
   if ((unsigned)page >= (unsigned)p.num_pages) {
     if (lane == 0) report_error(p.dev_error, HB_DEVERR_INDEX);
     return;
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kA8Threads) kv8_append_kernel(const Append8Par
   }
   int8_t* exps = (is_v ? p.v_exp : p.k_exp) + (size_t)page * p.num_kv_heads + head;
   uint8_t* dst = (is_v ? p.v_cache : p.k_cache) + ((size_t)page * kPageSize * p.num_kv_heads + head) * D + l * 8;
-  const int old = s0 > 0 ? kv8_exp(*exps) : kKv8MinExp;
+  const int old = s0 > 0 ? kv8_exp(ldcg_s8(exps)) : kKv8MinExp;
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < kIters; ++i)

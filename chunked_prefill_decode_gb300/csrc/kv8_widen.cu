@@ -25,6 +25,7 @@ constexpr int kWidenThreads = 256;
 
 __global__ void __launch_bounds__(kWidenThreads) kv8_widen_kernel(const WidenParams p) {
   griddep_wait();
+  griddep_launch_dependents();
   const int unit = blockIdx.x >> 1, which = blockIdx.x & 1;
   int lo = 0, hi = p.num_items - 1;
   while (lo < hi) {
@@ -34,7 +35,7 @@ __global__ void __launch_bounds__(kWidenThreads) kv8_widen_kernel(const WidenPar
   const WidenItem it = p.items[lo];
   const int lp = it.page_begin + unit - it.ws_page;
   const size_t entry = (size_t)it.seq * p.max_pages_per_seq + lp;
-  const int page = lp < p.max_pages_per_seq ? __ldg(&p.block_table[entry]) : -1;
+  const int page = lp < p.max_pages_per_seq ? __ldcg(&p.block_table[entry]) : -1;
   if ((unsigned)page >= (unsigned)p.num_pages) {
     if (threadIdx.x == 0) {
       report_error(p.dev_error, HB_DEVERR_INDEX);
@@ -49,8 +50,8 @@ __global__ void __launch_bounds__(kWidenThreads) kv8_widen_kernel(const WidenPar
   uint4* dst = reinterpret_cast<uint4*>(p.wide[which]) + (size_t)unit * vecs * 2;
   const int8_t* exps = p.exps[which] + (size_t)page * p.num_kv_heads;
   for (int i = threadIdx.x; i < vecs; i += kWidenThreads) {
-    const uint4 v = __ldg(src + i);
-    const float mul = pow2i(kv8_exp(exps[i / per_head % p.num_kv_heads]));
+    const uint4 v = __ldcg(src + i);
+    const float mul = pow2i(kv8_exp(ldcg_s8(exps + i / per_head % p.num_kv_heads)));
     const uint32_t in[4] = {v.x, v.y, v.z, v.w};
     uint32_t o[8];
 #pragma unroll
