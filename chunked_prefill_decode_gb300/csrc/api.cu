@@ -27,7 +27,7 @@ __device__ int g_hb_device_error = 0;
 
 namespace hb {
 cudaError_t launch_kv_append(const AppendParams& p, int num_sms, cudaStream_t stream);
-cudaError_t launch_kv8_append(Append8Params p, int head_dim, cudaStream_t stream);
+cudaError_t launch_kv8_append(Append8Params p, int head_dim, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv8_widen(const WidenParams& p, cudaStream_t stream);
 cudaError_t launch_attention8(const DecodeParams& dec, const Decode8Params& dec8, int decode_grid,
                               const ChunkParams& chk, int head_dim, const CUtensorMap& dec_k,
@@ -1304,7 +1304,7 @@ hb_status hb_kv8_append(const hb_batch* batch, const void* k_new, const void* v_
     p.dev_error = dev->err;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     LaunchTimer t(0, st);
-    cudaError_t e = launch_kv8_append(p, batch->head_dim, st);
+    cudaError_t e = launch_kv8_append(p, batch->head_dim, dev->num_sms, st);
     t.done();
     if (e != cudaSuccess) return cuda_fail(e, "kv8_append launch");
     LastLaunch rec;

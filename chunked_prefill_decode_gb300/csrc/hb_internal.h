@@ -214,7 +214,7 @@ struct Append8Params {
   const int32_t* context_len;
   const int32_t* block_table;
   int32_t num_seqs, total_q, max_pages_per_seq, num_pages, num_kv_heads;
-  int64_t num_units;      // page units of the grid (set by the launcher)
+  uint32_t num_pieces;    // (page unit, head, K or V) of the batch, set by the launcher
   const uint16_t* k_new;
   const uint16_t* v_new;
   uint8_t* k_cache;

@@ -36,6 +36,7 @@ namespace hb {
 namespace {
 
 constexpr int kA8Threads = 256;
+constexpr int kA8CtasPerSm = 2;     // 128 registers a thread: two pieces' rows of 32
 constexpr int kA8Warps = kA8Threads / 32;
 constexpr int kA8SmemSeqs = 6143;   // cu_q_len and context_len in shared memory up to here (48 KB)
 
@@ -47,62 +48,71 @@ __device__ __forceinline__ uint4 ld_stream16(const void* p) {
   return v;
 }
 
-// bf16 pair (low half first) times a power of two, as e4m3; an infinity
-// becomes NaN.
+// bf16 pair (low half first) times a power of two, as e4m3.
 __device__ __forceinline__ uint32_t quantise2(uint32_t v, float mul) {
-  float lo = bf16lo_to_f32(v), hi = bf16hi_to_f32(v);
-  if ((v & 0x7fffu) == 0x7f80u) lo = __uint_as_float(0x7fc00000u);
-  if ((v & 0x7fff0000u) == 0x7f800000u) hi = __uint_as_float(0x7fc00000u);
-  return e4m3x2(lo * mul, hi * mul);
+  return e4m3x2(bf16lo_to_f32(v) * mul, bf16hi_to_f32(v) * mul);
 }
 
-// the largest |x| (as bits) of the finite values of a pair
-__device__ __forceinline__ uint32_t finite_max2(uint32_t v) {
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+constexpr uint32_t kInf = 0x7f80u;   // bits of a bf16 infinity; NaN is above
+
+// An element that is not finite as NaN (bits 0x7fff), the others as they are.
+__device__ __forceinline__ uint32_t infinite_to_nan2(uint32_t v) {
+  if ((v & 0x7fffu) >= kInf) v |= 0x7fffu;
+  if (((v >> 16) & 0x7fffu) >= kInf) v |= 0x7fff0000u;
+  return v;
+}
+
+// |x| bits of a pair, 0 for what is not finite.
+__device__ __forceinline__ uint32_t finite_abs2(uint32_t v) {
   uint32_t lo = v & 0x7fffu, hi = (v >> 16) & 0x7fffu;
-  lo = lo < 0x7f80u ? lo : 0u;
-  hi = hi < 0x7f80u ? hi : 0u;
-  return max(lo, hi);
+  lo = lo < kInf ? lo : 0u;
+  hi = hi < kInf ? hi : 0u;
+  return lo | hi << 16;
 }
 
-// D bf16 of one token and head are D / 8 lanes' 16 bytes, so a warp access
-// covers kRows tokens and a page takes 16 / kRows of them.
+// One warp's share of the work: the new tokens of one page, one head and one
+// of K and V, with their rows on the way to registers.  D bf16 of one token
+// and head are D / 8 lanes' 16 bytes, so a warp access covers 256 / D tokens
+// and a page takes D / 16 of them.
 template <int D>
-__global__ void __launch_bounds__(kA8Threads) kv8_append_kernel(const Append8Params p) {
-  constexpr int kLanesPerRow = D / 8;
-  constexpr int kRows = 32 / kLanesPerRow;
-  constexpr int kIters = kPageSize / kRows;
-  extern __shared__ int32_t s_cu[];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const bool staged = p.num_seqs <= kA8SmemSeqs;
-  int32_t* s_ctx = s_cu + p.num_seqs + 1;
-  if (staged) {
-    for (int i = threadIdx.x; i <= p.num_seqs; i += kA8Threads) s_cu[i] = __ldcg(&p.cu_q_len[i]);
-    for (int i = threadIdx.x; i < p.num_seqs; i += kA8Threads) s_ctx[i] = __ldcg(&p.context_len[i]);
-  }
-  __syncthreads();
-  const int32_t* cu = staged ? s_cu : p.cu_q_len;
-  const int32_t* ctxs = staged ? s_ctx : p.context_len;
+struct Piece {
+  static constexpr int kLanesPerRow = D / 8;
+  static constexpr int kRows = 32 / kLanesPerRow;
+  static constexpr int kIters = kPageSize / kRows;
+  uint4 x[kIters];
+  int page;        // block-table entry, checked where it is used
+  int part;        // head, or Hkv + head for V; -1: nothing to do
+  int old;         // the page's exponent, where it holds older tokens
+  int s0, s1;      // slots of the page that receive tokens
+};
 
-  const int64_t w = (int64_t)blockIdx.x * kA8Warps + (threadIdx.x >> 5);
-  const int per_unit = 2 * p.num_kv_heads;
-  const int64_t unit = w / per_unit;
-  const int part = (int)(w - unit * per_unit);
-  const bool is_v = part >= p.num_kv_heads;
-  const int head = is_v ? part - p.num_kv_heads : part;
-  if (unit >= p.num_units) return;
+// Finds the piece and starts its loads (the rows' addresses need no page).
+template <int D>
+__device__ __forceinline__ void start_piece(const Append8Params& p, const int32_t* cu,
+                                            const int32_t* ctxs, uint32_t w, Piece<D>& a) {
+  using P = Piece<D>;
+  const int lane = threadIdx.x & 31;
+  const uint32_t per_unit = 2u * (uint32_t)p.num_kv_heads;
+  const uint32_t unit = w / per_unit;
+  a.part = -1;
+  if (w >= p.num_pieces) return;
   // the sequence whose units hold this one
   int lo = 0, hi = p.num_seqs - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if ((cu[mid] >> 4) + 2 * (int64_t)mid <= unit) lo = mid; else hi = mid - 1;
+    if ((uint32_t)(cu[mid] >> 4) + 2u * (uint32_t)mid <= unit) lo = mid; else hi = mid - 1;
   }
   const int s = lo;
   const int q0 = cu[s], q_len = cu[s + 1] - q0;
   const int ctx = ctxs[s];
   const int off = ctx - q_len;
-  const int k = (int)(unit - (q0 >> 4) - 2 * (int64_t)s);
+  const int k = (int)(unit - (uint32_t)(q0 >> 4) - 2u * (uint32_t)s);
   if (q_len <= 0) return;
   if (off < 0 || q0 < 0 || q0 + q_len > p.total_q) {
     if (lane == 0) report_error(p.dev_error, HB_DEVERR_INDEX);
@@ -111,40 +121,78 @@ __global__ void __launch_bounds__(kA8Threads) kv8_append_kernel(const Append8Par
   const int lp = off / kPageSize + k;
   // (lp < ceil(ctx / 16), without adding to a length near 2^31)
   if (lp > (ctx - 1) / kPageSize) return;
-  int page = -1;
-  if (lp < p.max_pages_per_seq) page = __ldcg(&p.block_table[(size_t)s * p.max_pages_per_seq + lp]);
-  if ((unsigned)page >= (unsigned)p.num_pages) {
-    if (lane == 0) report_error(p.dev_error, HB_DEVERR_INDEX);
+  a.page = -1;
+  if (lp < p.max_pages_per_seq) a.page = __ldcg(&p.block_table[(size_t)s * p.max_pages_per_seq + lp]);
+  // slots s0 .. s1-1 of the page receive tokens tok0 ..
+  a.part = (int)(w - unit * per_unit);
+  a.s0 = max(0, off - lp * kPageSize);
+  a.s1 = min(kPageSize, ctx - lp * kPageSize);
+  const int tok0 = q0 + lp * kPageSize + a.s0 - off;
+  const bool is_v = a.part >= p.num_kv_heads;
+  const int head = is_v ? a.part - p.num_kv_heads : a.part;
+  const int sub = lane / P::kLanesPerRow, l = lane % P::kLanesPerRow;
+  const size_t row = (size_t)p.num_kv_heads * D;   // elements of one token
+  const uint16_t* src = (is_v ? p.v_new : p.k_new) + ((size_t)tok0 * p.num_kv_heads + head) * D + l * 8;
+#pragma unroll
+  for (int i = 0; i < P::kIters; ++i) {
+    const int slot = i * P::kRows + sub;
+    a.x[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (slot >= a.s0 && slot < a.s1) a.x[i] = ld_stream16(src + (size_t)(slot - a.s0) * row);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ int8_t* exponent_of(const Append8Params& p, const Piece<D>& a) {
+  const bool is_v = a.part >= p.num_kv_heads;
+  return (is_v ? p.v_exp : p.k_exp) + (size_t)a.page * p.num_kv_heads +
+         (is_v ? a.part - p.num_kv_heads : a.part);
+}
+
+// The page is known: checks it, and asks for the exponent that it has.
+template <int D>
+__device__ __forceinline__ void check_piece(const Append8Params& p, Piece<D>& a) {
+  if (a.part < 0) return;
+  if ((unsigned)a.page >= (unsigned)p.num_pages) {
+    if ((threadIdx.x & 31) == 0) report_error(p.dev_error, HB_DEVERR_INDEX);
+    a.part = -1;
     return;
   }
-  // slots s0 .. s1-1 of the page receive tokens tok0 ..
-  const int s0 = max(0, off - lp * kPageSize);
-  const int s1 = min(kPageSize, ctx - lp * kPageSize);
-  const int tok0 = q0 + lp * kPageSize + s0 - off;
-  const int sub = lane / kLanesPerRow, l = lane % kLanesPerRow;
-  const uint16_t* src = is_v ? p.v_new : p.k_new;
-  const size_t row = (size_t)p.num_kv_heads * D;   // elements of one token
-  src += ((size_t)tok0 * p.num_kv_heads + head) * D + l * 8;
-  uint4 x[kIters];
+  a.old = kKv8MinExp;
+  if (a.s0 > 0) a.old = ldcg_s8(exponent_of(p, a));
+}
+
+template <int D>
+__device__ __forceinline__ void finish_piece(const Append8Params& p, Piece<D>& a) {
+  using P = Piece<D>;
+  if (a.part < 0) return;
+  const int lane = threadIdx.x & 31;
+  const bool is_v = a.part >= p.num_kv_heads;
+  const int head = is_v ? a.part - p.num_kv_heads : a.part;
+  const int sub = lane / P::kLanesPerRow, l = lane % P::kLanesPerRow;
+  const size_t row = (size_t)p.num_kv_heads * D;
+  uint8_t* dst = (is_v ? p.v_cache : p.k_cache) +
+                 ((size_t)a.page * kPageSize * p.num_kv_heads + head) * D + l * 8;
+  const int old = kv8_exp((int8_t)a.old);
+  auto largest = [&](auto magnitude) -> uint32_t {
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < kIters; ++i) {
-    const int slot = i * kRows + sub;
-    x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (slot >= s0 && slot < s1) x[i] = ld_stream16(src + (size_t)(slot - s0) * row);
+    for (int i = 0; i < P::kIters; ++i)
+      m = max_u16x2(max_u16x2(m, max_u16x2(magnitude(a.x[i].x), magnitude(a.x[i].y))),
+                    max_u16x2(magnitude(a.x[i].z), magnitude(a.x[i].w)));
+    return __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+  };
+  uint32_t m = largest([](uint32_t v) { return v & 0x7fff7fffu; });
+  if (m >= kInf) {   // rare: taken over the finite ones instead
+    m = largest([](uint32_t v) { return finite_abs2(v); });
+#pragma unroll
+    for (int i = 0; i < P::kIters; ++i)
+      a.x[i] = make_uint4(infinite_to_nan2(a.x[i].x), infinite_to_nan2(a.x[i].y),
+                          infinite_to_nan2(a.x[i].z), infinite_to_nan2(a.x[i].w));
   }
-  int8_t* exps = (is_v ? p.v_exp : p.k_exp) + (size_t)page * p.num_kv_heads + head;
-  uint8_t* dst = (is_v ? p.v_cache : p.k_cache) + ((size_t)page * kPageSize * p.num_kv_heads + head) * D + l * 8;
-  const int old = s0 > 0 ? kv8_exp(ldcg_s8(exps)) : kKv8MinExp;
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < kIters; ++i)
-    m = max(max(m, max(finite_max2(x[i].x), finite_max2(x[i].y))),
-            max(finite_max2(x[i].z), finite_max2(x[i].w)));
-  m = __reduce_max_sync(0xffffffffu, m);
   const int e = max(old, kv8_need_exp(m));
-  if (s0 > 0 && e > old) {
+  if (e > old && a.s0 > 0) {
     const float down = pow2i(old - e);
-    for (int slot = sub; slot < s0; slot += kRows) {
+    for (int slot = sub; slot < a.s0; slot += P::kRows) {
       uint2 v = *reinterpret_cast<const uint2*>(dst + (size_t)slot * row);
       uint32_t* b = &v.x;
 #pragma unroll
@@ -158,27 +206,70 @@ __global__ void __launch_bounds__(kA8Threads) kv8_append_kernel(const Append8Par
   }
   const float mul = pow2i(-e);
 #pragma unroll
-  for (int i = 0; i < kIters; ++i) {
-    const int slot = i * kRows + sub;
-    if (slot >= s0 && slot < s1)
+  for (int i = 0; i < P::kIters; ++i) {
+    if (i * P::kRows >= a.s1 || (i + 1) * P::kRows <= a.s0) continue;   // (alike in the warp)
+    const int slot = i * P::kRows + sub;
+    if (slot >= a.s0 && slot < a.s1)
       *reinterpret_cast<uint2*>(dst + (size_t)slot * row) =
-          make_uint2(quantise2(x[i].x, mul) | quantise2(x[i].y, mul) << 16,
-                     quantise2(x[i].z, mul) | quantise2(x[i].w, mul) << 16);
+          make_uint2(quantise2(a.x[i].x, mul) | quantise2(a.x[i].y, mul) << 16,
+                     quantise2(a.x[i].z, mul) | quantise2(a.x[i].w, mul) << 16);
   }
   __syncwarp();   // every lane has read the old exponent
-  if (lane == 0) *exps = (int8_t)e;
+  if (lane == 0) *exponent_of(p, a) = (int8_t)e;
+}
+
+// kMany: each warp takes pieces w, w + warps, .. and starts the next one's
+// loads before it finishes the one at hand; else one piece per warp, in more
+// and smaller warps.
+template <int D, bool kMany>
+__global__ void __launch_bounds__(kA8Threads, kMany ? kA8CtasPerSm : 4)
+    kv8_append_kernel(const Append8Params p) {
+  extern __shared__ int32_t s_cu[];
+  griddep_wait();
+  griddep_launch_dependents();
+  const bool staged = p.num_seqs <= kA8SmemSeqs;
+  int32_t* s_ctx = s_cu + p.num_seqs + 1;
+  if (staged) {
+    for (int i = threadIdx.x; i <= p.num_seqs; i += kA8Threads) s_cu[i] = __ldcg(&p.cu_q_len[i]);
+    for (int i = threadIdx.x; i < p.num_seqs; i += kA8Threads) s_ctx[i] = __ldcg(&p.context_len[i]);
+  }
+  __syncthreads();
+  const int32_t* cu = staged ? s_cu : p.cu_q_len;
+  const int32_t* ctxs = staged ? s_ctx : p.context_len;
+  uint32_t w = blockIdx.x * kA8Warps + (threadIdx.x >> 5);
+  Piece<D> a;
+  start_piece<D>(p, cu, ctxs, w, a);
+  check_piece<D>(p, a);
+  if constexpr (!kMany) {
+    finish_piece<D>(p, a);
+  } else {
+    // (two pieces by name: a copy would wait for the loads)
+    const uint32_t step = gridDim.x * kA8Warps;
+    Piece<D> b;
+    for (; w < p.num_pieces; w += 2 * step) {
+      start_piece<D>(p, cu, ctxs, w + step, b);
+      finish_piece<D>(p, a);
+      check_piece<D>(p, b);
+      start_piece<D>(p, cu, ctxs, w + 2 * step, a);
+      finish_piece<D>(p, b);
+      check_piece<D>(p, a);
+    }
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_kv8_append(Append8Params p, int head_dim, cudaStream_t stream) {
-  p.num_units = p.total_q / kPageSize + 2LL * p.num_seqs;
-  const int64_t warps = p.num_units * 2 * p.num_kv_heads;
-  const int64_t blocks = (warps + kA8Warps - 1) / kA8Warps;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+cudaError_t launch_kv8_append(Append8Params p, int head_dim, int num_sms, cudaStream_t stream) {
+  const int64_t pieces = (p.total_q / kPageSize + 2LL * p.num_seqs) * 2 * p.num_kv_heads;
+  if (pieces > 0x7fffffffLL) return cudaErrorInvalidValue;   // (w + step stays within 32 bits)
+  p.num_pieces = (uint32_t)pieces;
+  int64_t blocks = (pieces + kA8Warps - 1) / kA8Warps;
+  const bool many = blocks > 4 * 2LL * num_sms;
+  if (many) blocks = (int64_t)kA8CtasPerSm * num_sms;
   const size_t smem = p.num_seqs <= kA8SmemSeqs ? (size_t)(2 * p.num_seqs + 1) * 4 : 0;
-  return launch_serialized(head_dim == 128 ? kv8_append_kernel<128> : kv8_append_kernel<64>,
-                           (unsigned)blocks, kA8Threads, smem, stream, p);
+  const auto kernel = head_dim == 128 ? (many ? kv8_append_kernel<128, true> : kv8_append_kernel<128, false>)
+                                      : (many ? kv8_append_kernel<64, true> : kv8_append_kernel<64, false>);
+  return launch_serialized(kernel, (unsigned)blocks, kA8Threads, smem, stream, p);
 }
 
 }  // namespace hb

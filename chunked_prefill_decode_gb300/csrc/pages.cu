@@ -40,6 +40,8 @@ void internal_note_other_launch(void* stream);
 namespace {
 
 constexpr int kPagesThreads = 512;
+constexpr int kRun = 4;                   // tokens per thread and pass (slots)
+constexpr int kSeg = 8;                   // released pages per thread and pass
 constexpr int kPagesMaxSeqs = 16384;      // three int32 per sequence in shared memory
 
 struct PagesParams {
@@ -64,14 +66,17 @@ struct Sums {
   int64_t tokens, pages;
 };
 
-__device__ int prefix_sums(const PagesParams& p, Sums& a) {
+__device__ int prefix_sums(const PagesParams& p, Sums& a, int64_t* s_state) {
   __shared__ int64_t w_q[kPagesThreads / 32], w_pg[kPagesThreads / 32];
   const int S = p.num_seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t room = (int64_t)p.max_pages_per_seq * kPageSize;
   int bad = 0;
+  // (the ring's state arrives with the lengths)
+  longlong2 state = make_longlong2(0, 0);
+  if (tid == 0) state = make_longlong2(__ldcg(p.state_in), __ldcg(p.state_in + 1));
   for (int s = tid; s < S; s += kPagesThreads) {
-    const int ctx = p.ctx[s];
-    const int q = p.q_len ? p.q_len[s] : ctx;
+    const int ctx = __ldcg(p.ctx + s);
+    const int q = p.q_len ? __ldcg(p.q_len + s) : ctx;
     if (q < 0 || ctx < q || ctx > room) {
       bad = 1;
       continue;
@@ -82,6 +87,12 @@ __device__ int prefix_sums(const PagesParams& p, Sums& a) {
     a.s_pg[s] = (int32_t)(((int64_t)ctx + kPageSize - 1) / kPageSize -
                           ((int64_t)off + kPageSize - 1) / kPageSize);
     a.s_off[s] = off;
+  }
+  if (tid == 0) {
+    s_state[0] = state.x;
+    s_state[1] = state.y;
+    // where the ring's next page to take, or to put in, stands
+    s_state[2] = (p.q_len ? state.x : state.y) % p.num_pages;
   }
   if (__syncthreads_or(bad)) return HB_DEVERR_LENGTHS;
   // each thread sums a run of sequences, the block scans the runs
@@ -147,15 +158,8 @@ __device__ __forceinline__ int owner(const int32_t* sums, int S, int x) {
   return lo;
 }
 
-// Head and tail as they were before the launch; every CTA then counts itself
-// in, and the last one writes them back moved by `dh` / `dt`.
-__device__ void read_state(const PagesParams& p, int64_t* s_state) {
-  if (threadIdx.x == 0) {
-    s_state[0] = __ldcg(p.state_in);
-    s_state[1] = __ldcg(p.state_in + 1);
-  }
-  __syncthreads();
-}
+// Head and tail as the launch found them (s_state) moved by `dh` / `dt`,
+// written by the last CTA to have read them.
 __device__ void write_state(const PagesParams& p, const int64_t* s_state, int64_t dh, int64_t dt) {
   if (threadIdx.x != 0) return;
   bool last = gridDim.x == 1;
@@ -174,13 +178,12 @@ __device__ void write_state(const PagesParams& p, const int64_t* s_state, int64_
 
 __global__ void __launch_bounds__(kPagesThreads) pages_assign_kernel(const PagesParams p) {
   extern __shared__ int32_t s_dyn[];
-  __shared__ int64_t s_state[2];
+  __shared__ int64_t s_state[3];
   griddep_wait();
   griddep_launch_dependents();
   const int S = p.num_seqs;
   Sums a{s_dyn, s_dyn + S + 1, s_dyn + 2 * (S + 1), 0, 0};
-  read_state(p, s_state);
-  int err = prefix_sums(p, a);
+  int err = prefix_sums(p, a, s_state);
   const int64_t head = s_state[0], tail = s_state[1];
   if (!err && (head < 0 || tail < head || tail - head > p.num_pages || a.tokens > p.max_tokens))
     err = HB_DEVERR_LENGTHS;
@@ -190,8 +193,10 @@ __global__ void __launch_bounds__(kPagesThreads) pages_assign_kernel(const Pages
   if (err && blockIdx.x == 0 && threadIdx.x == 0) report_error(p.dev_error, err);
   if (!lengths_ok) return;
 
+  const int lane = threadIdx.x & 31;
   const int64_t first_thread = (int64_t)blockIdx.x * kPagesThreads + threadIdx.x;
   const int64_t step = (int64_t)gridDim.x * kPagesThreads;
+  const int64_t first_warp = first_thread >> 5, warps = step / 32;
   for (int64_t s = first_thread; s <= S; s += step) p.cu_q_len[s] = S > 0 ? a.s_q[s] : 0;
   if (S == 0) return;
   const int32_t* cu = a.s_q;
@@ -200,7 +205,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_assign_kernel(const Pages
       for (int64_t t = first_thread; t < a.tokens; t += step) p.slot_map[t] = -1;
     return;
   }
-  const int64_t at0 = head % p.num_pages;
+  const int64_t at0 = s_state[2];
   // ring entry k past the head (k below the pages taken, so at most one wrap)
   auto fresh_page = [&](int64_t k) -> int {
     int64_t i = at0 + k;
@@ -217,54 +222,89 @@ __global__ void __launch_bounds__(kPagesThreads) pages_assign_kernel(const Pages
     p.block_table[(size_t)s * p.max_pages_per_seq + lp] = page;
   }
   if (!p.slot_map) return;
-  for (int64_t t = first_thread; t < a.tokens; t += step) {
-    const int s = owner(cu, S, (int)t);
-    const int off = a.s_off[s];
-    const int pos = off + (int)t - cu[s];
-    const int lp = pos / kPageSize, first = (off + kPageSize - 1) / kPageSize;
-    int page;
-    if (lp >= first) {
-      page = fresh_page((int64_t)a.s_pg[s] + lp - first);
-    } else {
-      page = p.block_table[(size_t)s * p.max_pages_per_seq + lp];
-      if ((unsigned)page >= (unsigned)p.num_pages) page = -1;
+  // slots: a warp takes 32 kRun consecutive tokens, 32 at a time so that what
+  // it reads and writes lies together; a lane searches again only where its
+  // next token has left the sequence.  Where each page id stands is found
+  // first, so that a lane's loads are in flight together.
+  const int32_t tokens = (int32_t)a.tokens, h0 = (int32_t)at0;
+  for (int64_t tt = first_warp * 32 * kRun + lane; tt < tokens; tt += warps * 32 * kRun) {
+    const int32_t* src[kRun];
+    int in_page[kRun], page[kRun];
+    int s = owner(cu, S, (int)tt);
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+      const int t = (int)min(tt + 32 * j, (int64_t)tokens - 1);
+      if (cu[s + 1] <= t) s = owner(cu, S, t);
+      const int off = a.s_off[s];
+      const int pos = off + t - cu[s];
+      const int lp = pos / kPageSize, first = (off + kPageSize - 1) / kPageSize;
+      int64_t k = (int64_t)h0 + a.s_pg[s] + lp - first;
+      if (k >= p.num_pages) k -= p.num_pages;
+      src[j] = lp >= first ? p.ring + k : p.block_table + (size_t)s * p.max_pages_per_seq + lp;
+      in_page[j] = pos % kPageSize;
     }
-    if (page < 0) report_error(p.dev_error, HB_DEVERR_INDEX);
-    p.slot_map[t] = page < 0 ? -1 : (int64_t)page * kPageSize + pos % kPageSize;
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) page[j] = __ldcg(src[j]);
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+      const bool in = (unsigned)page[j] < (unsigned)p.num_pages;
+      bad |= !in;
+      if (tt + 32 * j < tokens)
+        p.slot_map[tt + 32 * j] = in ? (int64_t)page[j] * kPageSize + in_page[j] : -1;
+    }
+    if (bad) report_error(p.dev_error, HB_DEVERR_INDEX);
   }
 }
 
 __global__ void __launch_bounds__(kPagesThreads) pages_release_kernel(const PagesParams p) {
   extern __shared__ int32_t s_dyn[];
-  __shared__ int64_t s_state[2];
+  __shared__ int64_t s_state[3];
   griddep_wait();
   griddep_launch_dependents();
   const int S = p.num_seqs;
   Sums a{s_dyn, s_dyn + S + 1, s_dyn + 2 * (S + 1), 0, 0};
-  read_state(p, s_state);
-  int err = prefix_sums(p, a);
+  int err = prefix_sums(p, a, s_state);
   const int64_t head = s_state[0], tail = s_state[1];
   if (!err && (head < 0 || tail < head || tail - head > p.num_pages ||
                a.pages > p.num_pages - (tail - head)))
     err = HB_DEVERR_LENGTHS;
-  write_state(p, s_state, 0, err ? 0 : a.pages);
   if (err) {
     if (blockIdx.x == 0 && threadIdx.x == 0) report_error(p.dev_error, err);
+    write_state(p, s_state, 0, 0);
     return;
   }
-  const int64_t at0 = tail % p.num_pages;
-  const int64_t step = (int64_t)gridDim.x * kPagesThreads;
-  for (int64_t k = (int64_t)blockIdx.x * kPagesThreads + threadIdx.x; k < a.pages; k += step) {
-    const int s = owner(a.s_pg, S, (int)k);
-    int page = p.block_table[(size_t)s * p.max_pages_per_seq + (int)k - a.s_pg[s]];
-    if ((unsigned)page >= (unsigned)p.num_pages) {
-      report_error(p.dev_error, HB_DEVERR_INDEX);
-      page = -1;   // found again by the call that would hand it out
+  const int64_t at0 = s_state[2];
+  // a warp takes up to 32 kSeg pages of one row at a time: what it reads and
+  // what it writes are runs, and its loads are in flight together
+  const int lane = threadIdx.x & 31;
+  const int segs = (p.max_pages_per_seq + 32 * kSeg - 1) / (32 * kSeg);
+  const int64_t tasks = (int64_t)S * segs;
+  const int64_t warps = (int64_t)gridDim.x * (kPagesThreads / 32);
+  for (int64_t t = ((int64_t)blockIdx.x * kPagesThreads + threadIdx.x) >> 5; t < tasks; t += warps) {
+    // (segment-major: rows of one length fill the warps evenly)
+    const int seg = (int)((uint64_t)t / (uint32_t)S), s = (int)(t - (int64_t)seg * S);
+    const int k0 = a.s_pg[s], n = a.s_pg[s + 1] - k0;
+    const int lp0 = seg * 32 * kSeg + lane;
+    if (seg * 32 * kSeg >= n) continue;
+    const int32_t* row = p.block_table + (size_t)s * p.max_pages_per_seq;
+    int page[kSeg];
+#pragma unroll
+    for (int j = 0; j < kSeg; ++j) page[j] = lp0 + 32 * j < n ? __ldcg(row + lp0 + 32 * j) : 0;
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < kSeg; ++j) {
+      if ((unsigned)page[j] >= (unsigned)p.num_pages) {
+        bad = true;
+        page[j] = -1;   // found again by the call that would hand it out
+      }
+      int64_t i = at0 + k0 + lp0 + 32 * j;
+      if (i >= p.num_pages) i -= p.num_pages;
+      if (lp0 + 32 * j < n) p.ring[i] = page[j];
     }
-    int64_t i = at0 + k;
-    if (i >= p.num_pages) i -= p.num_pages;
-    p.ring[i] = page;
+    if (bad) report_error(p.dev_error, HB_DEVERR_INDEX);
   }
+  write_state(p, s_state, 0, a.pages);
 }
 
 hb_status check_common(int32_t num_seqs, int32_t max_pages_per_seq, int32_t num_pages, int32_t page_size,
@@ -291,15 +331,17 @@ hb_status check_common(int32_t num_seqs, int32_t max_pages_per_seq, int32_t num_
 
 using Kernel = void (*)(const PagesParams);
 
-// One CTA per kPagesThreads * 4 elements, at most two per SM.
-hb_status launch(Kernel kernel, PagesParams& p, int64_t elements, void* stream, const char* what) {
+// One run per thread, at most two CTAs per SM.
+hb_status launch(Kernel kernel, PagesParams& p, int64_t runs, void* stream, const char* what) {
   int num_sms = 0;
   const hb_status s = internal_device(&p.dev_error, &num_sms);
   if (s != HB_OK) return s;
-  const int64_t want = (elements + 4 * kPagesThreads - 1) / (4 * kPagesThreads);
+  const int64_t want = (runs + kPagesThreads - 1) / kPagesThreads;
   const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(want, 2LL * num_sms));
   const size_t smem = 3 * ((size_t)p.num_seqs + 1) * sizeof(int32_t);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  cudaError_t e = cudaSuccess;
+  if (smem > 32 * 1024)   // (more than a launch gets unasked, next to the static part)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
   if (e == cudaSuccess)
     e = launch_serialized(kernel, grid, kPagesThreads, smem, static_cast<cudaStream_t>(stream), p);
   if (e != cudaSuccess) return internal_fail(HB_ERR_CUDA, what);
@@ -343,9 +385,9 @@ extern "C" hb_status hb_pages_assign(int32_t num_seqs, int32_t max_tokens, int32
     p.block_table = block_table;
     p.cu_q_len = cu_q_len;
     p.slot_map = slot_map;
-    // tokens for the slots, at least one page per 16 of them and sequence
-    const int64_t elements = (slot_map ? (int64_t)max_tokens : (int64_t)max_tokens / kPageSize) + num_seqs;
-    return launch(pages_assign_kernel, p, elements, stream, "pages_assign launch failed");
+    // the slots' runs, or one page per 16 tokens and sequence
+    const int64_t runs = (int64_t)max_tokens / (slot_map ? kRun : kPageSize) + num_seqs;
+    return launch(pages_assign_kernel, p, runs, stream, "pages_assign launch failed");
   } catch (...) {
     return internal_fail(HB_ERR_CUDA, "unexpected exception in hb_pages_assign");
   }
@@ -368,10 +410,9 @@ extern "C" hb_status hb_pages_release(int32_t num_seqs, int32_t max_pages_per_se
     p.state_out = state_out;
     p.ring = free_pages;
     p.block_table = const_cast<int32_t*>(block_table);
-    // the lengths are on the GPU: at most every page comes back
-    const int64_t elements =
-        std::min<int64_t>(num_pages, (int64_t)num_seqs * max_pages_per_seq) + num_seqs;
-    return launch(pages_release_kernel, p, elements, stream, "pages_release launch failed");
+    // one warp per segment of a row, as long as the table is wide
+    const int64_t runs = (int64_t)num_seqs * ((max_pages_per_seq + 32 * kSeg - 1) / (32 * kSeg)) * 32;
+    return launch(pages_release_kernel, p, runs, stream, "pages_release launch failed");
   } catch (...) {
     return internal_fail(HB_ERR_CUDA, "unexpected exception in hb_pages_release");
   }

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 import torch
@@ -346,28 +347,48 @@ def hb_attention_new_kv(batch, plan, q, k_new, v_new, k_cache, v_cache, scale, o
 
 
 # ---------------------------------------------------------------- 8-bit cache
-def _tensor(t, name, dtype, shape):
-    """Pointer of a contiguous tensor of the given dtype and shape (None in the
-    shape: any size) on the current CUDA device."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor")
-    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
-        raise ValueError(f"{name} must have shape {tuple('*' if w is None else w for w in shape)}, "
-                         f"got {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return _ptr(t)
+class _Args:
+    """Argument checks of one call: `ptr` gives a tensor's address after its
+    dtype, layout, shape and device are found right, `stream` the stream's.
+    (A step makes these calls once per layer, so the checks are kept to a few
+    hundred nanoseconds each.)"""
+
+    __slots__ = ("dev",)
+
+    def __init__(self):
+        self.dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+
+    def ptr(self, t, name, dtype, shape):
+        """`shape`: a tuple, or an int for a 1-D tensor of that or (-1) any size."""
+        if type(t) is not torch.Tensor and not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a tensor")
+        if t.dtype is not dtype or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor")
+        if not (t.shape == shape if type(shape) is tuple else t.dim() == 1 and shape in (-1, t.shape[0])):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                             f"{shape if type(shape) is tuple else '(*,)' if shape < 0 else (shape,)}")
+        d = t.get_device()
+        if d < 0:
+            raise ValueError(f"{name} must be on a CUDA device")
+        if d != self.dev:
+            if self.dev is None:      # a CUDA tensor exists, so CUDA is up
+                self.dev = torch.cuda.current_device()
+            if d != self.dev:
+                raise ValueError(f"{name} is on cuda:{d}, the current device is cuda:{self.dev}")
+        return t.data_ptr()
+
+    def stream(self, stream):
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.dev) if self.dev is not None else None
+        return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _kv8_args(batch, k_cache, v_cache, k_exp, v_exp):
-    pool = (batch.num_pages, batch.page_size, batch.num_kv_heads, batch.head_dim)
-    exps = (batch.num_pages, batch.num_kv_heads)
-    return (_tensor(k_cache, "k_cache", torch.float8_e4m3fn, pool),
-            _tensor(v_cache, "v_cache", torch.float8_e4m3fn, pool),
-            _tensor(k_exp, "k_exp", torch.int8, exps), _tensor(v_exp, "v_exp", torch.int8, exps))
+def _kv8_args(a, batch, k_cache, v_cache, k_exp, v_exp):
+    pages, hkv = batch.num_pages, batch.num_kv_heads
+    pool, exps = (pages, batch.page_size, hkv, batch.head_dim), (pages, hkv)
+    return (a.ptr(k_cache, "k_cache", torch.float8_e4m3fn, pool),
+            a.ptr(v_cache, "v_cache", torch.float8_e4m3fn, pool),
+            a.ptr(k_exp, "k_exp", torch.int8, exps), a.ptr(v_exp, "v_exp", torch.int8, exps))
 
 
 def kv8_cache(num_pages, num_kv_heads, head_dim, page_size=16, device="cuda"):
@@ -380,10 +401,13 @@ def kv8_cache(num_pages, num_kv_heads, head_dim, page_size=16, device="cuda"):
 
 def hb_kv8_append(batch, k_new, v_new, k_cache, v_cache, k_exp, v_exp, stream=None):
     """Quantise the batch's new K/V rows (bf16) into the 8-bit cache."""
+    a = _Args()
     new = (batch.total_q, batch.num_kv_heads, batch.head_dim)
-    _check(load().hb_kv8_append(ctypes.byref(batch), _tensor(k_new, "k_new", torch.bfloat16, new),
-                                _tensor(v_new, "v_new", torch.bfloat16, new),
-                                *_kv8_args(batch, k_cache, v_cache, k_exp, v_exp), _stream(stream)))
+    kn, vn = a.ptr(k_new, "k_new", torch.bfloat16, new), a.ptr(v_new, "v_new", torch.bfloat16, new)
+    cache = _kv8_args(a, batch, k_cache, v_cache, k_exp, v_exp)
+    st = (_lib or load()).hb_kv8_append(ctypes.byref(batch), kn, vn, *cache, a.stream(stream))
+    if st:
+        _check(st)
 
 
 def hb_kv8_plan(batch, q_len, context_len, num_sms, workspace=None, stream=None, plan=None,
@@ -392,18 +416,30 @@ def hb_kv8_plan(batch, q_len, context_len, num_sms, workspace=None, stream=None,
     return hb_plan(batch, q_len, context_len, num_sms, workspace, stream, plan, upload, kv8=True)
 
 
+_PLAN_WS_TOTAL = struct.Struct("<Q")     # plan_header()["ws_total"]
+_PLAN_WS_TOTAL_AT = 88 + 8 * 5
+
+
 def hb_kv8_attention(batch, plan, q, k_cache, v_cache, k_exp, v_exp, scale, out, workspace,
                      stream=None):
     """hb_attention over the 8-bit cache."""
+    a = _Args()
     rows = (batch.total_q, batch.num_q_heads, batch.head_dim)
-    need = plan_header(plan)["ws_total"]
-    if workspace is not None and workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"workspace has {workspace.numel()} bytes, the plan needs {need}")
-    _check(load().hb_kv8_attention(ctypes.byref(batch), _ptr(plan),
-                                   _tensor(q, "q", torch.bfloat16, rows),
-                                   *_kv8_args(batch, k_cache, v_cache, k_exp, v_exp),
-                                   ctypes.c_float(scale), _tensor(out, "out", torch.bfloat16, rows),
-                                   _ptr(workspace), _stream(stream)))
+    if not isinstance(plan, np.ndarray) or plan.dtype != np.uint8 or plan.nbytes < HEADER_BYTES:
+        raise ValueError("plan must be the uint8 array that hb_kv8_plan returned")
+    ws = None
+    if workspace is not None:
+        need = _PLAN_WS_TOTAL.unpack_from(plan, _PLAN_WS_TOTAL_AT)[0]
+        ws = a.ptr(workspace, "workspace", torch.uint8, -1)
+        if workspace.shape[0] < need:
+            raise ValueError(f"workspace has {workspace.shape[0]} bytes, the plan needs {need}")
+    qp = a.ptr(q, "q", torch.bfloat16, rows)
+    cache = _kv8_args(a, batch, k_cache, v_cache, k_exp, v_exp)
+    st = (_lib or load()).hb_kv8_attention(ctypes.byref(batch), plan.ctypes.data, qp, *cache, scale,
+                                           a.ptr(out, "out", torch.bfloat16, rows), ws,
+                                           a.stream(stream))
+    if st:
+        _check(st)
 
 
 # ---------------------------------------------------------------- pages on the GPU
@@ -421,33 +457,38 @@ def hb_pages_assign(q_len, context_len, free_pages, state_in, state_out, block_t
     """Block-table entries, prefix sums and (if given) slots of a step from its
     lengths on the GPU, with pages taken from the ring free_pages / state_in
     (state_out receives the ring's new state and may be state_in)."""
+    a = _Args()
     n = q_len.numel()
-    _check(load().hb_pages_assign(
-        n, slot_map.numel() if slot_map is not None else 0x7fffffff,
-        block_table.shape[1] if block_table.dim() == 2 else 0, free_pages.numel(), int(page_size),
-        _tensor(q_len, "q_len", torch.int32, (n,)),
-        _tensor(context_len, "context_len", torch.int32, (n,)),
-        _tensor(free_pages, "free_pages", torch.int32, (None,)),
-        _tensor(state_in, "state_in", torch.int64, (4,)),
-        _tensor(state_out, "state_out", torch.int64, (4,)),
-        _tensor(block_table, "block_table", torch.int32, (n, None)),
-        _tensor(cu_q_len, "cu_q_len", torch.int32, (n + 1,)),
-        _tensor(slot_map, "slot_map", torch.int64, (None,)) if slot_map is not None else None,
-        _stream(stream)))
+    max_pages = block_table.shape[1] if block_table.dim() == 2 else 0
+    st = (_lib or load()).hb_pages_assign(
+        n, slot_map.numel() if slot_map is not None else 0x7fffffff, max_pages, free_pages.numel(),
+        page_size, a.ptr(q_len, "q_len", torch.int32, n),
+        a.ptr(context_len, "context_len", torch.int32, n),
+        a.ptr(free_pages, "free_pages", torch.int32, -1),
+        a.ptr(state_in, "state_in", torch.int64, 4), a.ptr(state_out, "state_out", torch.int64, 4),
+        a.ptr(block_table, "block_table", torch.int32, (n, max_pages)),
+        a.ptr(cu_q_len, "cu_q_len", torch.int32, n + 1),
+        a.ptr(slot_map, "slot_map", torch.int64, -1) if slot_map is not None else None,
+        a.stream(stream))
+    if st:
+        _check(st)
 
 
 def hb_pages_release(lengths, free_pages, state_in, state_out, block_table, page_size=16,
                      stream=None):
     """The pages of the sequences with lengths > 0 (tokens in the cache) go back
     to the ring."""
+    a = _Args()
     n = lengths.numel()
-    _check(load().hb_pages_release(
-        n, block_table.shape[1] if block_table.dim() == 2 else 0, free_pages.numel(),
-        int(page_size), _tensor(lengths, "lengths", torch.int32, (n,)),
-        _tensor(block_table, "block_table", torch.int32, (n, None)),
-        _tensor(free_pages, "free_pages", torch.int32, (None,)),
-        _tensor(state_in, "state_in", torch.int64, (4,)),
-        _tensor(state_out, "state_out", torch.int64, (4,)), _stream(stream)))
+    max_pages = block_table.shape[1] if block_table.dim() == 2 else 0
+    st = (_lib or load()).hb_pages_release(
+        n, max_pages, free_pages.numel(), page_size, a.ptr(lengths, "lengths", torch.int32, n),
+        a.ptr(block_table, "block_table", torch.int32, (n, max_pages)),
+        a.ptr(free_pages, "free_pages", torch.int32, -1),
+        a.ptr(state_in, "state_in", torch.int64, 4), a.ptr(state_out, "state_out", torch.int64, 4),
+        a.stream(stream))
+    if st:
+        _check(st)
 
 
 def hb_decode_attention_noalloc(batch, q_len, context_len, q, k_cache, v_cache, scale,
