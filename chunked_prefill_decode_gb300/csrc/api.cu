@@ -664,8 +664,8 @@ hb_status hb::internal_plan(const hb_batch* batch, const int32_t* h_q_len,
     if (tq != batch->total_q)
       return fail(HB_ERR_SHAPE, "sum of q_len (%lld) != total_q (%d)", (long long)tq, batch->total_q);
 
-    const int kvhb = std::min(Hkv, kDecodeKvhBlock);
-    const int n_blocks = Hkv / kvhb;
+    int kvhb = std::min(Hkv, kDecodeKvhBlock);
+    int n_blocks = Hkv / kvhb;
     // all working arrays live in per-thread storage that keeps its capacity
     // from call to call: a plan of a batch shaped like the last one
     // allocates nothing
@@ -938,6 +938,20 @@ hb_status hb::internal_plan(const hb_batch* batch, const int32_t* h_q_len,
     // intervals claimed from a counter) is supported by partition_decode and
     // the kernel but measured slower on GB300 (Mistral 125 vs 110 us: the
     // extra pieces and merges cost more than the ragged tail), so it is off.
+    if (kv8) {
+      // Few rows on many CTAs leave many pieces per row, and one CTA merges
+      // them all: blocks of fewer kv heads spread that over more CTAs (and
+      // the consumer warps share a head instead, decode8_body.cuh).  Narrow
+      // boxes stream slower, so the blocks are halved only while the rows'
+      // blocks are fewer than a quarter of the CTAs.  GB300, kernel time with
+      // full blocks / this rule / blocks up to the CTAs: 1 row of 16384 tokens
+      // 54 / 26 / 26 us, 4 of 8192 32 / 29 / 29, 32 of about 7300 115 / 109 /
+      // 131, 64 of about 2100 68 / 68 / 70.
+      while (kvhb % 2 == 0 && n_dec_rows * n_blocks * 4 < decode_ctas) {
+        kvhb /= 2;
+        n_blocks *= 2;
+      }
+    }
     const int max_intervals = std::max(1, decode_ctas) * (1 + kDynamicPerCta) + 1;
     const int max_dec_items =
         (int)std::min<int64_t>(n_dec_rows * n_blocks + max_intervals + 1, 1 << 30);
@@ -1367,6 +1381,7 @@ hb_status hb_kv8_attention(const hb_batch* batch, const void* h_plan, const void
     ChunkParams cp{};
     cp.group = dp.group;
     bool early = follows_own_append(stream, batch, k_cache, v_cache);
+    Decode8Params d8{k_exp, v_exp, 1};
     if (h.num_chunk_items > 0) {
       WidenParams wp{};
       wp.items = reinterpret_cast<const WidenItem*>(ws + p8.ws_widen_items);
@@ -1400,12 +1415,13 @@ hb_status hb_kv8_attention(const hb_batch* batch, const void* h_plan, const void
       if (e != cudaSuccess) return cuda_fail(e, "kv8_widen launch");
       note_launch(stream, LastLaunch{});
       g_launches.fetch_add(1);
-      // the widening lets the next launch start once everything before it is
-      // complete, so only what reads its pages waits
+      // the widening waits for the append and lets the next launch start only
+      // then, so of that launch only what reads the widened pages waits
       early = true;
+      d8.wait_new = 0;
     }
     LaunchTimer t(1, st);
-    cudaError_t e = launch_attention8(dp, Decode8Params{k_exp, v_exp}, h.decode_grid, cp, D, dec_k, dec_v,
+    cudaError_t e = launch_attention8(dp, d8, h.decode_grid, cp, D, dec_k, dec_v,
                                       chunk_q, chunk_k, chunk_v, st, early, h.chunk_pairs_only);
     t.done();
     if (e != cudaSuccess) return cuda_fail(e, "attention launch (8-bit)");

@@ -25,8 +25,9 @@ struct Attn8Params {
   ChunkParams chk;
   int32_t decode_grid;
   // 1: the launch before this one let it start with everything complete but
-  // its own results: the append's (only the pages with new tokens and their
-  // exponents wait), or the widened pages (only the chunk CTAs wait)
+  // its own results: the append's (the decode CTAs wait before the pages with
+  // new tokens, dec8.wait_new), or the widened pages (only the chunk CTAs
+  // wait)
   int32_t early;
 };
 

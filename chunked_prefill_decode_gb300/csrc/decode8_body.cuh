@@ -107,6 +107,79 @@ inline __host__ Decode8Layout decode8_layout(int head_dim, int kvh_block, int gr
   return L;
 }
 
+// The last piece of a row (and block of kv heads) merges all of them: o = sum
+// 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  A warp takes kMh of the block's nh q
+// heads at a time and kUnroll pieces of each, their loads in flight together;
+// each lane owns D / 32 dims.  (A block of few heads has many pieces.)
+template <int D, int kMh, int kUnroll>
+__device__ __forceinline__ void merge_rows8(const DecodeParams& p, const DecodeItem& it, int nh,
+                                            int warp) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, Hq = p.num_q_heads;
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+  for (int h0 = warp; h0 < nh; h0 += kMh * kDec8Consumers) {
+    float mmax[kMh], lsum[kMh], acc[kMh][E];
+    size_t hh[kMh];
+#pragma unroll
+    for (int h = 0; h < kMh; ++h) {
+      // (past the block's heads: the first one again, not stored)
+      hh[h] = (size_t)(it.kvh0 * p.group + (h0 + h * kDec8Consumers < nh ? h0 + h * kDec8Consumers : h0));
+      mmax[h] = -INFINITY;
+      lsum[h] = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[h][e] = 0.f;
+    }
+    // the pieces' (m, l), 32 at a time, a lane each
+    for (int i2 = lane; i2 < it.n_splits; i2 += 32)
+#pragma unroll
+      for (int h = 0; h < kMh; ++h)
+        mmax[h] = fmaxf(mmax[h], __ldcg(&ml[(size_t)(it.slot + i2) * Hq + hh[h]]).x);
+#pragma unroll
+    for (int h = 0; h < kMh; ++h)
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1)
+        mmax[h] = fmaxf(mmax[h], __shfl_xor_sync(0xffffffffu, mmax[h], d));
+    for (int base = 0; base < it.n_splits; base += 32) {
+      float wgt[kMh];
+#pragma unroll
+      for (int h = 0; h < kMh; ++h) {
+        wgt[h] = 0.f;
+        if (base + lane < it.n_splits) {
+          const float2 st2 = __ldcg(&ml[(size_t)(it.slot + base + lane) * Hq + hh[h]]);
+          wgt[h] = fast_exp2(st2.x - mmax[h]);
+          lsum[h] += wgt[h] * st2.y;
+        }
+      }
+      const int m = min(32, it.n_splits - base);
+#pragma unroll kUnroll
+      for (int i2 = 0; i2 < m; ++i2)
+#pragma unroll
+        for (int h = 0; h < kMh; ++h) {
+          const float wi = __shfl_sync(0xffffffffu, wgt[h], i2);
+          const float* po = p.part_o + ((size_t)(it.slot + base + i2) * Hq + hh[h]) * D + lane * E;
+          if constexpr (E == 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(po));
+            acc[h][0] += wi * v.x; acc[h][1] += wi * v.y;
+            acc[h][2] += wi * v.z; acc[h][3] += wi * v.w;
+          } else {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(po));
+            acc[h][0] += wi * v.x; acc[h][1] += wi * v.y;
+          }
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < kMh; ++h) {
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) lsum[h] += __shfl_xor_sync(0xffffffffu, lsum[h], d);
+      if (h0 + h * kDec8Consumers >= nh) continue;
+      const float inv = 1.f / lsum[h];
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + ((size_t)it.tok * Hq + hh[h]) * D + lane * E);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[h][e] * inv, acc[h][e + 1] * inv);
+    }
+  }
+}
+
 // Body of one decode CTA (index `cta` among the decode CTAs); `smem` is the
 // 1024-byte-aligned dynamic shared memory.
 template <int D>
@@ -212,7 +285,7 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
           phys = p.num_pages;
         }
         // the append before this launch wrote the new token's page
-        if (!dep_done && lp + np > new_page) {
+        if (p8.wait_new && !dep_done && lp + np > new_page) {
           griddep_wait();
           fence_proxy_async_global();
           dep_done = true;
@@ -288,7 +361,7 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
         return (kv8_exp(ldcg_s8(p8.k_exp + at)) & 0xff) | (kv8_exp(ldcg_s8(p8.v_exp + at)) << 8);
       };
       // what the append wrote (the exponents of the last pages) is complete
-      griddep_wait();
+      if (p8.wait_new) griddep_wait();
 
       int st = 0;
       uint32_t ph = 0;
@@ -660,50 +733,8 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
           if (!(ok = all_here())) break;
           if (flags[1]) {
             __threadfence();
-            // one warp per q head of the block; each lane owns D / 32 dims
-            constexpr int E = D / 32;
-            const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-            for (int hl = warp; hl < kvhb * g; hl += kDec8Consumers) {
-              const int hh = it.kvh0 * g + hl;
-              // the pieces' (m, l), 32 at a time, a lane each
-              float mmax = -INFINITY;
-              for (int i2 = lane; i2 < it.n_splits; i2 += 32)
-                mmax = fmaxf(mmax, __ldcg(&ml[(size_t)(it.slot + i2) * Hq + hh]).x);
-#pragma unroll
-              for (int d = 16; d > 0; d >>= 1) mmax = fmaxf(mmax, __shfl_xor_sync(0xffffffffu, mmax, d));
-              float acc[E];
-#pragma unroll
-              for (int e = 0; e < E; ++e) acc[e] = 0.f;
-              float lsum = 0.f;
-              for (int base = 0; base < it.n_splits; base += 32) {
-                float wgt = 0.f;
-                if (base + lane < it.n_splits) {
-                  const float2 st2 = __ldcg(&ml[(size_t)(it.slot + base + lane) * Hq + hh]);
-                  wgt = fast_exp2(st2.x - mmax);
-                  lsum += wgt * st2.y;
-                }
-                const int m = min(32, it.n_splits - base);
-#pragma unroll 8
-                for (int i2 = 0; i2 < m; ++i2) {
-                  const float wi = __shfl_sync(0xffffffffu, wgt, i2);
-                  const float* po = p.part_o + ((size_t)(it.slot + base + i2) * Hq + hh) * D + lane * E;
-                  if constexpr (E == 4) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(po));
-                    acc[0] += wi * v.x; acc[1] += wi * v.y;
-                    acc[2] += wi * v.z; acc[3] += wi * v.w;
-                  } else {
-                    const float2 v = __ldcg(reinterpret_cast<const float2*>(po));
-                    acc[0] += wi * v.x; acc[1] += wi * v.y;
-                  }
-                }
-              }
-#pragma unroll
-              for (int d = 16; d > 0; d >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, d);
-              const float inv = 1.f / lsum;
-              uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + ((size_t)it.tok * Hq + hh) * D + lane * E);
-#pragma unroll
-              for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-            }
+            if (kvhb * g <= kDec8Consumers) merge_rows8<D, 1, 16>(p, it, kvhb * g, warp);
+            else merge_rows8<D, 4, 4>(p, it, kvhb * g, warp);
             if (threadIdx.x == 0) p.counters[kCounterMerge0 + it.merge_id] = 0;
           }
         }

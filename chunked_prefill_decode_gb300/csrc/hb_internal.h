@@ -228,6 +228,9 @@ struct Append8Params {
 struct Decode8Params {
   const int8_t* k_exp;    // [num_pages, Hkv]
   const int8_t* v_exp;
+  // 1: the launch before this one is the append (the pages with new tokens
+  // and their exponents wait for it); 0: the append is complete already
+  int32_t wait_new;
 };
 
 // What an 8-bit plan adds to a plan (hb_kv8_plan): its host copy holds this

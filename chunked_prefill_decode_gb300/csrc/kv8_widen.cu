@@ -46,9 +46,9 @@ __global__ void __launch_bounds__(kWidenThreads) kv8_widen_kernel(const WidenPar
   if (which == 0 && threadIdx.x == 0) p.ws_table[entry] = unit;
   const int vecs = kPageSize * p.num_kv_heads * p.head_dim / 16;   // 16 values each
   const int per_head = p.head_dim / 16;
-  const uint4* src = reinterpret_cast<const uint4*>(p.cache[which]) + (size_t)page * vecs;
-  uint4* dst = reinterpret_cast<uint4*>(p.wide[which]) + (size_t)unit * vecs * 2;
-  const int8_t* exps = p.exps[which] + (size_t)page * p.num_kv_heads;
+  const uint4* src = reinterpret_cast<const uint4*>((which ? p.cache[1] : p.cache[0])) + (size_t)page * vecs;
+  uint4* dst = reinterpret_cast<uint4*>((which ? p.wide[1] : p.wide[0])) + (size_t)unit * vecs * 2;
+  const int8_t* exps = (which ? p.exps[1] : p.exps[0]) + (size_t)page * p.num_kv_heads;
   for (int i = threadIdx.x; i < vecs; i += kWidenThreads) {
     const uint4 v = __ldcg(src + i);
     const float mul = pow2i(kv8_exp(ldcg_s8(exps + i / per_head % p.num_kv_heads)));
