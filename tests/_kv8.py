@@ -87,7 +87,11 @@ def bounds(layout, inp, cache, scale=None, tokens=None):
     of the weights may or may not hold the rounded ones: 2^-8 |o| more.  A
     score is a sum of D products in fp32 and three roundings more, and its
     exponential is good to 2^-22: (D + 3) 2^-24 (sum_d |q_d k_d|) scale +
-    2^-21 relative in each weight, taken twice (numerator and sum)."""
+    2^-21 relative in each weight, taken twice (numerator and sum).  In fp16 a
+    weight has no finer step than 2^-24, against a largest one of 2^7 or more
+    (P carries that factor): a key far below the row's maximum is off by up to
+    2^-25 / 2^7 = 2^-32 of the largest weight, hence of the sum, so the ctx
+    keys of a row by 2^-32 ctx max |v| at most."""
     sh = layout.shape
     scale = 1.0 / math.sqrt(sh.head_dim) if scale is None else scale
     args = (layout.q_len, layout.context_len, layout.block_table, sh.page_size, sh.num_q_heads,
@@ -100,7 +104,10 @@ def bounds(layout, inp, cache, scale=None, tokens=None):
     k = k[np.isfinite(k)].max() if np.isfinite(k).any() else 0.0
     qmax = np.abs(inp.q.double().numpy()).sum(-1).max()
     score = (sh.head_dim + 3) * 2.0 ** -24 * qmax * k * scale + 2.0 ** -21
-    return ref, HALF_BF16 * (2 * np.abs(ref) + a) + 2 * score * a + 1e-30
+    v = np.abs(kv8.values(cache[1], cache[3]))
+    v = v[np.isfinite(v)].max() if np.isfinite(v).any() else 0.0
+    far = np.repeat(np.asarray(layout.context_len, np.float64), layout.q_len)[:, None, None] * 2.0 ** -32 * v
+    return ref, HALF_BF16 * (2 * np.abs(ref) + a) + 2 * score * a + far
 
 
 def check_out(out, ref, tol, tokens=None):
