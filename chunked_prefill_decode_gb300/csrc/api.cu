@@ -1409,6 +1409,7 @@ hb_status hb_kv8_attention(const hb_batch* batch, const void* h_plan, const void
       fill_chunk(&cp, h, batch, ws, out, scale_log2, dev);
       cp.block_table = wp.ws_table;
       cp.num_pages = p8.widen_pages;
+      cp.wait_first = 1;
       LaunchTimer t(1, st);
       cudaError_t e = launch_kv8_widen(wp, st);
       t.done();

@@ -26,8 +26,8 @@ struct Attn8Params {
   int32_t decode_grid;
   // 1: the launch before this one let it start with everything complete but
   // its own results: the append's (the decode CTAs wait before the pages with
-  // new tokens, dec8.wait_new), or the widened pages (only the chunk CTAs
-  // wait)
+  // new tokens, dec8.wait_new), or the widened pages (the chunk CTAs wait
+  // before they read one, chk.wait_first)
   int32_t early;
 };
 
@@ -39,18 +39,15 @@ __global__ void __launch_bounds__(kAttn8Threads, 1)
                       const __grid_constant__ CUtensorMap chunk_k,
                       const __grid_constant__ CUtensorMap chunk_v) {
   extern __shared__ uint8_t smem_raw[];
-  const bool decode = (int)blockIdx.x < p.decode_grid;
-  if (!p.early || !decode) griddep_wait();
+  if (!p.early) griddep_wait();
   griddep_launch_dependents();
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
-  if (decode) {
+  if ((int)blockIdx.x < p.decode_grid)
     decode8_cta<D>(p.dec, p.dec8, p.dl, dec_k, dec_v, smem, blockIdx.x);
-  } else {
-    fence_proxy_async_global();   // the widened pages, read by TMA
+  else
     chunk_cta<D, kPairs, kFew>(p.chk, chunk_q, chunk_k, chunk_v, chunk_k, chunk_v, nullptr, nullptr,
                                smem, blockIdx.x - p.decode_grid);
-  }
 }
 
 // As launch_attention (attention.cu): decode_grid decode CTAs, then one CTA

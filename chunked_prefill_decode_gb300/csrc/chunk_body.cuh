@@ -383,6 +383,11 @@ __device__ __forceinline__ void chunk_cta(const ChunkParams& p, const CUtensorMa
         par = (par & ~(1u << bit)) | (ph << bit);
       }
     };
+    if (p.wait_first) {
+      griddep_wait();
+      fence_proxy_async_global();
+      dep_done = true;
+    }
     int bt_prev = kPastContext, bt_cur = load_batch(0), bt_next = load_batch(1);
     bool ok = true;
     for (int j = 0; ok && j <= n_all; ++j) {   // j: tile jb + j

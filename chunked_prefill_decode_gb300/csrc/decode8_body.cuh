@@ -23,12 +23,14 @@
 //  * the host plan gives each CTA an equal contiguous range of the decode
 //    rows' pages (decode_plan.h), cut into items at row boundaries;
 //  * a stage of the ring is as many pages as make sixteen (kv head, page)
-//    pairs, K and V: two pages of 8 heads, or 16 pages of one head, so a warp
-//    has the same work per stage whatever the head count.  One producer warp
-//    fills it with one TMA box per page and pool ([kv head][slot][D bytes],
+//    pairs, K and V, at D 128 and 32 at D 64: two (four) pages of 8 heads, or
+//    16 (32) pages of one head, so a warp has the same work per stage whatever
+//    the head count.  Four producer
+//    warps fill it with one TMA box per page and pool ([kv head][slot][D bytes],
 //    swizzled by the row width);
-//  * eight consumer warps, each with one head and two pages of the stage, so
-//    that two chains of products, softmax and products run side by side: a
+//  * eight consumer warps, each with one head and two pages of the stage (four
+//    at D 64), so that as many chains of products, softmax and products run
+//    side by side: a
 //    page alone is a chain of latencies (1390 cycles at D 128, hardly less at
 //    D 64, the same with the conversions left out), and filling a stage costs
 //    the producer about 750 cycles whatever it holds;
@@ -65,8 +67,10 @@
 
 namespace hb {
 
-constexpr int kDec8Consumers = 8;     // warps 0-7; warp 8 is the producer
-constexpr int kDec8Pages = 2;         // pages of a stage per consumer warp
+constexpr int kDec8Consumers = 8;     // warps 0-7
+constexpr int kDec8Producers = 4;     // warps 8-11
+// pages of a stage per consumer warp: 256 head dims' worth
+inline __host__ __device__ constexpr int decode8_pages(int head_dim) { return 256 / head_dim; }
 constexpr int kDec8MaxStages = 14;
 constexpr float kDec8RescaleThreshold = 8.0f;   // log2 units
 constexpr float kDec8PShift = 7.0f;             // P <= 2^(8 + 7) in fp16
@@ -95,7 +99,7 @@ inline __host__ Decode8Layout decode8_layout(int head_dim, int kvh_block, int gr
   Decode8Layout L{};
   L.parts = kDec8Consumers / kvh_block;   // 8, 4, 2, 2, 1 ..: a power of two
   L.half_bytes = kvh_block * kPageSize * head_dim;
-  L.stage_bytes = 2 * L.half_bytes * L.parts * kDec8Pages;
+  L.stage_bytes = 2 * L.half_bytes * L.parts * decode8_pages(head_dim);
   L.qslot_bytes = ((kvh_block * group * head_dim * 2) + 1023) / 1024 * 1024;
   L.merge_bytes = L.parts / 2 * kvh_block * decode8_state_floats(head_dim, group) * 4;
   const int fixed = 1024 /*align*/ + 2 * L.qslot_bytes + L.merge_bytes +
@@ -203,11 +207,12 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
   const int g = p.group;
   const int kvhb = p.kvh_block;
   const int parts = L.parts;
-  const int pps = parts * kDec8Pages;   // pages per stage; divides 32
+  constexpr int U = decode8_pages(D);
+  const int pps = parts * U;            // pages per stage; divides 32
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], kDec8Producers);
       mbar_init(&empty[s], kDec8Consumers);
     }
     for (int i = 0; i < 2; ++i) {
@@ -228,11 +233,13 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
   if (warp >= kDec8Consumers) {
     setmaxnreg_dec<kDec8LightRegs>();
     // ------------------------------------------------------------ producer
-    // The whole warp runs the loop: each lane holds one block-table entry of
-    // a 32-page window (fetched a window ahead), lane 0 works the barriers,
-    // lanes 2i and 2i + 1 issue K and V of the stage's page i.
-    const bool producer = warp == kDec8Consumers;
-    if (producer && lane == 0) {
+    // Four warps walk the stages side by side and issue every fourth box of
+    // each (K and V of page i are boxes 2i and 2i + 1): a box takes a warp
+    // about 110 cycles to issue, and a stage of 16 pages of one head has 32.
+    // In each warp a lane holds one block-table entry of a 32-page window
+    // (fetched a window ahead) and lane 0 works the barriers.
+    const int me = warp - kDec8Consumers;
+    if (lane == 0) {
       tma_prefetch_desc(&kmap);
       tma_prefetch_desc(&vmap);
     }
@@ -252,13 +259,13 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
     bool ok = true;
     DecodeItem it{}, nxt{};
     int win = 0, win_next = 0, nxt_win = 0;
-    if (producer && item0 < item1) {
+    if (item0 < item1) {
       it = p.items[item0];
       win = window(it, it.page_begin);
       win_next = window(it, it.page_begin + 32);
     }
-    for (int i = producer ? item0 : item1; ok && i < item1; ++i) {
-      if (lane == 0) {
+    for (int i = item0; ok && i < item1; ++i) {
+      if (me == 0 && lane == 0) {
         ok = mbar_wait(&qempty[qslot], qph[qslot] ^ 1u, abort_flag);
         if (ok) {
           mbar_arrive_expect_tx(&qfull[qslot], qbytes);
@@ -277,8 +284,9 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
           win_next = window(it, lp + 32);
         }
         const int np = min(pps, it.page_end - lp);
-        int phys = __shfl_sync(0xffffffffu, win, k + min(lane >> 1, pps - 1));
-        const bool issuer = lane < 2 * np;
+        const int box = 4 * lane + me;   // this lane's box of the stage, if there are so many
+        int phys = __shfl_sync(0xffffffffu, win, k + min(box >> 1, pps - 1));
+        const bool issuer = box < 2 * np;
         if (issuer && (unsigned)phys >= (unsigned)p.num_pages) {
           // out of range: reported, and fetched out of bounds (zeros)
           report_error(p.dev_error, HB_DEVERR_INDEX);
@@ -292,12 +300,13 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
         }
         if (lane == 0) {
           ok = mbar_wait(&empty[st], ph ^ 1u, abort_flag);
-          if (ok) mbar_arrive_expect_tx(&full[st], 2u * (uint32_t)(np * L.half_bytes));
+          // (the boxes of this warp)
+          if (ok) mbar_arrive_expect_tx(&full[st], (uint32_t)((2 * np - me + 3) / 4 * L.half_bytes));
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         if (ok) {
           if (issuer)
-            tma_load_4d(stages + st * L.stage_bytes + lane * L.half_bytes, (lane & 1) ? &vmap : &kmap,
+            tma_load_4d(stages + st * L.stage_bytes + box * L.half_bytes, (box & 1) ? &vmap : &kmap,
                         &full[st], 0, 0, it.kvh0, phys);
           issued_mask |= 1u << st;
           last_par_mask = (last_par_mask & ~(1u << st)) | (ph << st);
@@ -326,7 +335,6 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
     auto consume = [&](auto nq_const) {
       constexpr int NQ = decltype(nq_const)::value;   // 8-head column tiles
       constexpr int KC = D / 64;                      // 16-byte K chunks per lane and key
-      constexpr int U = kDec8Pages;
       const int w = warp % kvhb;                      // local kv head of this warp
       const int part = warp / kvhb;                   // its pages of a stage: part + u * parts
       const bool active = part < parts;
@@ -487,7 +495,7 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
               lo_valid[u] = p.window > 0 ? it.ctx - p.window - lp * kPageSize : 0;
             }
             // independent accumulators, so that the chains of MMAs are short
-            constexpr int kQk = NQ == 1 ? 2 : 1;
+            constexpr int kQk = NQ * U <= 2 ? 2 : 1;
             float s[U][kQk][NQ][4];
 #pragma unroll
             for (int u = 0; u < U; ++u)

@@ -166,6 +166,9 @@ struct ChunkParams {
   // inputs, [total_q, Hkv, D]): pages that hold only new tokens are read from
   // there, so the chunk does not wait for the append that writes them
   int32_t has_new;
+  // 1: the pages and the block table themselves come from the launch before
+  // this one, which is waited for before the first of either is read
+  int32_t wait_first;
 };
 
 // Linear layer y = x W^T (linear.cu).  epilogue: 0 store, 1 gated (W has

@@ -23,9 +23,8 @@ namespace {
 
 constexpr int kWidenThreads = 256;
 
+template <int D>
 __global__ void __launch_bounds__(kWidenThreads) kv8_widen_kernel(const WidenParams p) {
-  griddep_wait();
-  griddep_launch_dependents();
   const int unit = blockIdx.x >> 1, which = blockIdx.x & 1;
   int lo = 0, hi = p.num_items - 1;
   while (lo < hi) {
@@ -33,6 +32,9 @@ __global__ void __launch_bounds__(kWidenThreads) kv8_widen_kernel(const WidenPar
     if (__ldg(&p.items[mid].ws_page) <= unit) lo = mid; else hi = mid - 1;
   }
   const WidenItem it = p.items[lo];
+  // (the plan was there before the launch before this one began)
+  griddep_wait();
+  griddep_launch_dependents();
   const int lp = it.page_begin + unit - it.ws_page;
   const size_t entry = (size_t)it.seq * p.max_pages_per_seq + lp;
   const int page = lp < p.max_pages_per_seq ? __ldcg(&p.block_table[entry]) : -1;
@@ -44,14 +46,14 @@ __global__ void __launch_bounds__(kWidenThreads) kv8_widen_kernel(const WidenPar
     return;
   }
   if (which == 0 && threadIdx.x == 0) p.ws_table[entry] = unit;
-  const int vecs = kPageSize * p.num_kv_heads * p.head_dim / 16;   // 16 values each
-  const int per_head = p.head_dim / 16;
-  const uint4* src = reinterpret_cast<const uint4*>((which ? p.cache[1] : p.cache[0])) + (size_t)page * vecs;
-  uint4* dst = reinterpret_cast<uint4*>((which ? p.wide[1] : p.wide[0])) + (size_t)unit * vecs * 2;
+  constexpr int kPerHead = D / 16;   // vectors of 16 values
+  const int vecs = kPageSize * p.num_kv_heads * kPerHead;
+  const uint4* src = reinterpret_cast<const uint4*>(which ? p.cache[1] : p.cache[0]) + (size_t)page * vecs;
+  uint4* dst = reinterpret_cast<uint4*>(which ? p.wide[1] : p.wide[0]) + (size_t)unit * vecs * 2;
   const int8_t* exps = (which ? p.exps[1] : p.exps[0]) + (size_t)page * p.num_kv_heads;
   for (int i = threadIdx.x; i < vecs; i += kWidenThreads) {
     const uint4 v = __ldcg(src + i);
-    const float mul = pow2i(kv8_exp(ldcg_s8(exps + i / per_head % p.num_kv_heads)));
+    const float mul = pow2i(kv8_exp(ldcg_s8(exps + (uint32_t)(i / kPerHead) % (uint32_t)p.num_kv_heads)));
     const uint32_t in[4] = {v.x, v.y, v.z, v.w};
     uint32_t o[8];
 #pragma unroll
@@ -70,7 +72,7 @@ __global__ void __launch_bounds__(kWidenThreads) kv8_widen_kernel(const WidenPar
 
 cudaError_t launch_kv8_widen(const WidenParams& p, cudaStream_t stream) {
   if (p.num_units == 0) return cudaSuccess;
-  return launch_serialized(kv8_widen_kernel, 2u * (unsigned)p.num_units, kWidenThreads, 0, stream, p);
+  return launch_serialized(p.head_dim == 128 ? kv8_widen_kernel<128> : kv8_widen_kernel<64>, 2u * (unsigned)p.num_units, kWidenThreads, 0, stream, p);
 }
 
 }  // namespace hb
