@@ -33,7 +33,7 @@ cudaError_t launch_attention8(const DecodeParams& dec, const Decode8Params& dec8
                               const ChunkParams& chk, int head_dim, const CUtensorMap& dec_k,
                               const CUtensorMap& dec_v, const CUtensorMap& chunk_q,
                               const CUtensorMap& chunk_k, const CUtensorMap& chunk_v,
-                              cudaStream_t stream, bool early, int pairs_mode);
+                              cudaStream_t stream, bool early, int pairs_mode, int device);
 cudaError_t launch_linear(const LinearParams& p, const CUtensorMap& xmap, const CUtensorMap& wmap,
                           int num_sms, cudaStream_t stream);
 int linear_w_box_rows();
@@ -83,6 +83,7 @@ struct DevState {
   bool ready = false;
   int* err = nullptr;
   int num_sms = 0;
+  int index = 0;
 };
 std::mutex g_dev_mu;
 DevState g_dev[64];
@@ -101,6 +102,7 @@ hb_status device_state(DevState** out) {
     e = cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
     d.err = static_cast<int*>(p);
+    d.index = dev;
     d.ready = true;
   }
   *out = &d;
@@ -751,7 +753,12 @@ hb_status hb::internal_plan(const hb_batch* batch, const int32_t* h_q_len,
     // at 3 us (6: 1.311 / 0.814 / 0.586, 15: 1.298 / 0.824 / 0.585), the
     // batches with decode rows unchanged.
     constexpr double kHbmBytesPerUs = 7.0e6;      // whole-GPU HBM stream
-    constexpr double kSmBytesPerUs = 8.5e4;       // one SM's stream ceiling
+    // one SM's stream ceiling.  (8-bit: 61 GB/s measured.  There the estimate
+    // is flat over more of the range, and the decode CTAs' share of the time
+    // falls with their number, so a quarter into the range is taken: 64
+    // decodes + 448-token chunk 73.9 us, 32 long decodes + 2016-token chunk
+    // 387; the middle 75.7 and 395, with bf16's rate 75.7 and 388.)
+    const double kSmBytesPerUs = kv8 ? 6.2e4 : 8.5e4;
     constexpr double kPairTileUs = 2.0;           // 2-tile item x one key tile
     constexpr double kSingleTileUs = 1.25;        // 1-tile item x one key tile
     constexpr double kPieceUs = 10.0;             // extra cost of one split piece
@@ -798,7 +805,7 @@ hb_status hb::internal_plan(const hb_batch* batch, const int32_t* h_q_len,
         }
         hi = c;
       }
-      return (lo + hi) / 2;
+      return lo + (hi - lo) / (kv8 ? 4 : 2);
     };
     // pieces per item when each piece holds about L key tiles
     auto pieces_of = [&](int kv, int L) {
@@ -1423,7 +1430,7 @@ hb_status hb_kv8_attention(const hb_batch* batch, const void* h_plan, const void
     }
     LaunchTimer t(1, st);
     cudaError_t e = launch_attention8(dp, d8, h.decode_grid, cp, D, dec_k, dec_v,
-                                      chunk_q, chunk_k, chunk_v, st, early, h.chunk_pairs_only);
+                                      chunk_q, chunk_k, chunk_v, st, early, h.chunk_pairs_only, dev->index);
     t.done();
     if (e != cudaSuccess) return cuda_fail(e, "attention launch (8-bit)");
     note_launch(stream, LastLaunch{});

@@ -51,12 +51,13 @@ __global__ void __launch_bounds__(kAttn8Threads, 1)
 }
 
 // As launch_attention (attention.cu): decode_grid decode CTAs, then one CTA
-// per chunk item, either part possibly empty; pairs_mode as there.
+// per chunk item, either part possibly empty; pairs_mode as there; device:
+// the current one (below 64).
 cudaError_t launch_attention8(const DecodeParams& dec, const Decode8Params& dec8, int decode_grid,
                               const ChunkParams& chk, int head_dim, const CUtensorMap& dec_k,
                               const CUtensorMap& dec_v, const CUtensorMap& chunk_q,
                               const CUtensorMap& chunk_k, const CUtensorMap& chunk_v,
-                              cudaStream_t stream, bool early, int pairs_mode) {
+                              cudaStream_t stream, bool early, int pairs_mode, int device) {
   Attn8Params p{};
   p.early = early ? 1 : 0;
   p.dec = dec;
@@ -91,8 +92,15 @@ cudaError_t launch_attention8(const DecodeParams& dec, const Decode8Params& dec8
     regs[which].store(n, std::memory_order_relaxed);
   }
   if (n < kChunkLaunchRegs) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  // (the opt-in to the largest shared memory holds for a device once made)
+  static std::atomic<uint64_t> opted[8] = {};
+  const uint64_t bit = 1ull << device;
+  if (!(opted[which].load(std::memory_order_relaxed) & bit)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e != cudaSuccess) return e;
+    opted[which].fetch_or(bit, std::memory_order_relaxed);
+  }
   return launch_serialized(kernel, grid, kAttn8Threads, smem, stream, p, dec_k, dec_v, chunk_q, chunk_k,
                            chunk_v);
 }

@@ -133,8 +133,17 @@ __device__ __forceinline__ void merge_rows8(const DecodeParams& p, const DecodeI
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[h][e] = 0.f;
     }
-    // the pieces' (m, l), 32 at a time, a lane each
-    for (int i2 = lane; i2 < it.n_splits; i2 += 32)
+    // the pieces' (m, l), 32 at a time, a lane each; the first 32 (as good as
+    // always all) stay in registers
+    float2 st0[kMh];
+#pragma unroll
+    for (int h = 0; h < kMh; ++h) {
+      st0[h] = make_float2(-INFINITY, 0.f);
+      if (lane < it.n_splits) st0[h] = __ldcg(&ml[(size_t)(it.slot + lane) * Hq + hh[h]]);
+    }
+#pragma unroll
+    for (int h = 0; h < kMh; ++h) mmax[h] = st0[h].x;
+    for (int i2 = lane + 32; i2 < it.n_splits; i2 += 32)
 #pragma unroll
       for (int h = 0; h < kMh; ++h)
         mmax[h] = fmaxf(mmax[h], __ldcg(&ml[(size_t)(it.slot + i2) * Hq + hh[h]]).x);
@@ -147,12 +156,13 @@ __device__ __forceinline__ void merge_rows8(const DecodeParams& p, const DecodeI
       float wgt[kMh];
 #pragma unroll
       for (int h = 0; h < kMh; ++h) {
-        wgt[h] = 0.f;
-        if (base + lane < it.n_splits) {
-          const float2 st2 = __ldcg(&ml[(size_t)(it.slot + base + lane) * Hq + hh[h]]);
-          wgt[h] = fast_exp2(st2.x - mmax[h]);
-          lsum[h] += wgt[h] * st2.y;
+        float2 st2 = st0[h];
+        if (base > 0) {
+          st2 = make_float2(-INFINITY, 0.f);
+          if (base + lane < it.n_splits) st2 = __ldcg(&ml[(size_t)(it.slot + base + lane) * Hq + hh[h]]);
         }
+        wgt[h] = fast_exp2(st2.x - mmax[h]);   // 0 past the pieces
+        lsum[h] += wgt[h] * st2.y;
       }
       const int m = min(32, it.n_splits - base);
 #pragma unroll kUnroll
@@ -729,18 +739,16 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
             }
         }
         if (it.n_splits > 1) {
-          // publish this piece's state: the barrier orders every consumer's
-          // stores before thread 0's device-scope fence + atomic
+          // publish this piece's state: every consumer's stores come before
+          // its arrival, and those before thread 0's device-scope release
           if (!(ok = all_here())) break;
           if (threadIdx.x == 0) {
-            __threadfence();
-            const int old = atomicAdd(&p.counters[kCounterMerge0 + it.merge_id], 1);
-            __threadfence();  // acquire: the other pieces' states are visible
+            // release this piece's state, acquire the others'
+            const int old = atom_add_acq_rel(&p.counters[kCounterMerge0 + it.merge_id], 1);
             flags[1] = (old == it.n_splits - 1) ? 1 : 0;
           }
           if (!(ok = all_here())) break;
           if (flags[1]) {
-            __threadfence();
             if (kvhb * g <= kDec8Consumers) merge_rows8<D, 1, 16>(p, it, kvhb * g, warp);
             else merge_rows8<D, 4, 4>(p, it, kvhb * g, warp);
             if (threadIdx.x == 0) p.counters[kCounterMerge0 + it.merge_id] = 0;

@@ -81,6 +81,14 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return v;
 }
 
+// *p += v at device scope, as a release of everything ordered before it and
+// an acquire of what the others released there.
+__device__ __forceinline__ int atom_add_acq_rel(int32_t* p, int v) {
+  int old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
+}
+
 // A byte through L2 (another kernel may have written it since this SM's L1
 // last saw its line).
 __device__ __forceinline__ int8_t ldcg_s8(const int8_t* p) {
