@@ -1305,6 +1305,9 @@ hb_status hb_kv8_append(const hb_batch* batch, const void* k_new, const void* v_
     if ((s = check_ptr(k_new, "k_new")) != HB_OK) return s;
     if ((s = check_ptr(v_new, "v_new")) != HB_OK) return s;
     if ((s = check_kv8(k_cache, v_cache, k_exp, v_exp)) != HB_OK) return s;
+    if (kv8_append_pieces(batch->total_q, batch->num_seqs, batch->num_kv_heads) > 0x7fffffffLL)
+      return fail(HB_ERR_UNSUPPORTED, "%d tokens of %d sequences and %d kv heads are too many at once",
+                  batch->total_q, batch->num_seqs, batch->num_kv_heads);
     DevState* dev = nullptr;
     if ((s = device_state(&dev)) != HB_OK) return s;
     Append8Params p{};

@@ -328,7 +328,10 @@ __device__ __forceinline__ void chunk_cta(const ChunkParams& p, const CUtensorMa
     auto load_batch = [&](int b) -> int {
       const int lp = (jb + b * kTilesPerBatch) * kPagesPerTile + lane;
       if (lp >= n_pages || (lp + 1) * kPageSize <= lowest_key) return kPastContext;
-      return lp < p.max_pages_per_seq ? __ldg(&bt_row[lp]) : -1;
+      if (lp >= p.max_pages_per_seq) return -1;
+      // (a table that the launch before writes: not through a path that may
+      // hold what was there before)
+      return p.wait_first ? __ldcg(&bt_row[lp]) : __ldg(&bt_row[lp]);
     };
     auto phys_of = [&](int raw) -> int {
       if (raw == kPastContext) return p.num_pages;

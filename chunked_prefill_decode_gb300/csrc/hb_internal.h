@@ -227,6 +227,12 @@ struct Append8Params {
   int* dev_error;
 };
 
+// Its pieces (page unit, head, K or V): at least one unit per page that a
+// batch's tokens touch (kv8_append.cu).
+inline int64_t kv8_append_pieces(int32_t total_q, int32_t num_seqs, int32_t num_kv_heads) {
+  return (total_q / kPageSize + 2LL * num_seqs) * 2 * num_kv_heads;
+}
+
 // What the decode rows of the 8-bit cache need besides DecodeParams.
 struct Decode8Params {
   const int8_t* k_exp;    // [num_pages, Hkv]

@@ -114,7 +114,7 @@ __device__ __forceinline__ void start_piece(const Append8Params& p, const int32_
   const int off = ctx - q_len;
   const int k = (int)(unit - (uint32_t)(q0 >> 4) - 2u * (uint32_t)s);
   if (q_len <= 0) return;
-  if (off < 0 || q0 < 0 || q0 + q_len > p.total_q) {
+  if (off < 0 || q0 < 0 || (int64_t)q0 + q_len > p.total_q) {
     if (lane == 0) report_error(p.dev_error, HB_DEVERR_INDEX);
     return;
   }
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kA8Threads, kMany ? kA8CtasPerSm : 4)
 }  // namespace
 
 cudaError_t launch_kv8_append(Append8Params p, int head_dim, int num_sms, cudaStream_t stream) {
-  const int64_t pieces = (p.total_q / kPageSize + 2LL * p.num_seqs) * 2 * p.num_kv_heads;
+  const int64_t pieces = kv8_append_pieces(p.total_q, p.num_seqs, p.num_kv_heads);
   if (pieces > 0x7fffffffLL) return cudaErrorInvalidValue;   // (w + step stays within 32 bits)
   p.num_pieces = (uint32_t)pieces;
   int64_t blocks = (pieces + kA8Warps - 1) / kA8Warps;

@@ -273,7 +273,8 @@ hb_status hb_decode_attention_noalloc(const hb_batch* batch,
  * one sequence's new tokens only (a prefix may be shared between sequences
  * in whole pages that no batch row appends to).
  *   k_new, v_new     device, [total_q, Hkv, D] bf16, 16-byte aligned
- * Errors as hb_kv_append; HB_ERR_INVALID_ARG for NULL exponents.
+ * Errors as hb_kv_append; HB_ERR_INVALID_ARG for NULL exponents,
+ * HB_ERR_UNSUPPORTED for a batch of over 2^31 (page, head) pieces.
  */
 hb_status hb_kv8_append(const hb_batch* batch, const void* k_new, const void* v_new,
                         void* k_cache, void* v_cache, int8_t* k_exp, int8_t* v_exp,
@@ -291,7 +292,11 @@ hb_status hb_kv8_plan(const hb_batch* batch, const int32_t* h_q_len,
 /* hb_attention over the 8-bit cache: the same result, of the elements' values,
  * with the same masks, precision and errors; HB_ERR_INVALID_ARG for a
  * softmax_scale that is not positive and finite.  What unwritten slots of a
- * page hold (NaN included) never shows. */
+ * page hold (NaN included) never shows, nor for a decode row what stands
+ * below its window; a NaN stored as a value (V) of a chunk's own token may
+ * reach the chunk's earlier rows too, as in hb_attention.  Work: decode rows
+ * stream the 8-bit pages as they are; chunk rows' pages are spelt out as bf16
+ * in the workspace by a launch before, and attended to as by hb_attention. */
 hb_status hb_kv8_attention(const hb_batch* batch, const void* h_plan, const void* q,
                            const void* k_cache, const void* v_cache, const int8_t* k_exp,
                            const int8_t* v_exp, float softmax_scale, void* out,

@@ -215,6 +215,74 @@ def test_constant_v_returns_it():
     assert (out.float() - 0.75).abs().max() <= 0.75 * 2 * 2.0 ** -8
 
 
+@pytest.mark.parametrize("geom", [(3, 3, 128), (6, 3, 64), (48, 3, 128), (5, 5, 64), (12, 6, 128), (14, 7, 64),
+                                  (64, 4, 128), (32, 2, 128), (16, 1, 64), (128, 8, 128), (64, 32, 64)])
+def test_any_number_of_kv_heads(geom):
+    """Heads that do not divide the eight consumer warps, and groups of more
+    than 8 q heads, alone and shared by several pages of a stage."""
+    full_check(layout_from_rows(Shape(*geom), [(1, 1), (1, 17), (1, 530), (1, 1600), (33, 200)], 51), seed=52)
+
+
+@pytest.mark.parametrize("geom", [(32, 8, 128), (8, 2, 64), (16, 1, 128)])
+@pytest.mark.parametrize("rows", [1, 2, 3, 5, 9, 40, 150])
+def test_few_and_many_decode_rows(geom, rows):
+    """The plan gives few rows blocks of fewer kv heads, cut into many pieces."""
+    full_check(layout_from_rows(Shape(*geom), [(1, 900 + 37 * i % 400) for i in range(rows)], 53), seed=rows)
+
+
+def test_what_a_row_may_not_see_may_be_nan():
+    """NaN values below a decode row's window, and q rows of NaN and infinity:
+    no other row, head or sequence changes."""
+    sh = Shape(8, 2, 128, sliding_window=40)
+    layout = layout_from_rows(sh, [(1, 100), (1, 70), (20, 64)], 54)
+    inp = Inputs(layout, 55)
+    cache = list(inp.oracle_append(layout))
+    inp.cache, inp.exps = cache[:2], cache[2:]
+    ref, tol = bounds(layout, inp, cache)
+    for s, low in ((0, 60), (1, 30)):
+        for pos in range(low):
+            cache[0][layout.block_table[s, pos // 16], pos % 16] = 0x7F
+            cache[1][layout.block_table[s, pos // 16], pos % 16] = 0xFF
+    inp.cache = cache[:2]
+    _, out = step(layout, inp, append=False)
+    check_out(out, ref, tol)
+    inp.q[0, 3], inp.q[5, 1, 7] = float("nan"), float("inf")
+    _, out = step(layout, inp, append=False)
+    hit = np.zeros(out.shape[:2], bool)
+    hit[0, 3] = hit[5, 1] = True
+    got = out.float().cpu().numpy()
+    assert np.isnan(got[0, 3]).all() and not np.isfinite(got[5, 1]).any()
+    check_out(torch.from_numpy(np.where(hit[:, :, None], 0.0, got)), np.where(hit[:, :, None], 0.0, ref), tol)
+
+
+def test_one_workspace_for_batches_in_turn():
+    """A workspace sized for the larger of two batches, planned for each in
+    turn: nothing of one batch's plan, counters or pages stays for the other."""
+    hb = lib()
+    work, ws = [], None
+    for s, rows in ((56, [(1, 1500), (90, 700), (1, 33), (40, 40)]), (57, [(200, 1000), (1, 2000), (1, 5), (1, 900)])):
+        layout = layout_from_rows(Shape(32, 8, 128), rows, s)
+        inp = Inputs(layout, s)
+        work.append((layout, inp, from_layout(layout, "cuda:0"), inp.device(), inp.q.cuda(), inp.k_new.cuda(),
+                     inp.v_new.cuda(), []))
+    for layout, _, db, *_ in work:
+        need = hb.hb_plan_sizes(db.batch, db.q_len, db.context_len, sms(), kv8=True)[1]
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda") if ws is None or ws.numel() < need else ws
+    for _ in range(15):
+        for _, _, db, cache, q, kn, vn, outs in work:
+            out = torch.empty_like(q)
+            plan, w = hb.hb_kv8_plan(db.batch, db.q_len, db.context_len, sms(), workspace=ws)
+            assert w is ws
+            hb.hb_kv8_append(db.batch, kn, vn, *cache)
+            hb.hb_kv8_attention(db.batch, plan, q, *cache, 1.0 / math.sqrt(128), out, ws)
+            outs.append(out)
+    hb.hb_check()
+    for layout, inp, _, cache, _, _, _, outs in work:
+        ref, tol = bounds(layout, inp, check_append(layout, inp, cache))
+        for out in outs:
+            check_out(out, ref, tol)
+
+
 def test_plan_is_reused_and_results_repeat():
     layout = layout_from_rows(Shape(32, 8, 128), [(1, 3000), (100, 700), (1, 40)], 36)
     inp = Inputs(layout, 37)

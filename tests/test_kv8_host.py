@@ -133,6 +133,13 @@ def test_bad_pointers_are_refused():
     assert L.hb_kv8_attention(ctypes.byref(b), None, *[FAKE] * 5, 1.0, FAKE, FAKE, None) == 1
 
 
+def test_append_of_too_many_pieces_is_refused():
+    hb = lib()
+    b, _, _ = batch(hb)
+    b.num_seqs = b.total_q = 2 ** 30
+    assert hb.load().hb_kv8_append(ctypes.byref(b), *[FAKE] * 6, None) == 3
+
+
 def test_plans_of_the_two_caches_are_told_apart():
     hb = lib()
     L = hb.load()
