@@ -217,7 +217,8 @@ struct Append8Params {
   const int32_t* context_len;
   const int32_t* block_table;
   int32_t num_seqs, total_q, max_pages_per_seq, num_pages, num_kv_heads;
-  uint32_t num_pieces;    // (page unit, head, K or V) of the batch, set by the launcher
+  uint32_t num_pieces;    // (unit, head, K or V) of the batch, set by the launcher
+  int32_t by_token;       // a unit is a token, not a page
   const uint16_t* k_new;
   const uint16_t* v_new;
   uint8_t* k_cache;
@@ -227,10 +228,17 @@ struct Append8Params {
   int* dev_error;
 };
 
-// Its pieces (page unit, head, K or V): at least one unit per page that a
-// batch's tokens touch (kv8_append.cu).
+// Its pieces (unit, head, K or V): at least one unit per page that a batch's
+// tokens touch, or one per token where that is less (kv8_append.cu).
+inline int64_t kv8_append_page_units(int32_t total_q, int32_t num_seqs) {
+  return total_q / kPageSize + 2LL * num_seqs;
+}
+inline bool kv8_append_by_token(int32_t total_q, int32_t num_seqs) {
+  return total_q < kv8_append_page_units(total_q, num_seqs);
+}
 inline int64_t kv8_append_pieces(int32_t total_q, int32_t num_seqs, int32_t num_kv_heads) {
-  return (total_q / kPageSize + 2LL * num_seqs) * 2 * num_kv_heads;
+  const int64_t units = kv8_append_page_units(total_q, num_seqs);
+  return (total_q < units ? total_q : units) * 2 * num_kv_heads;
 }
 
 // What the decode rows of the 8-bit cache need besides DecodeParams.

@@ -22,6 +22,13 @@
 // warp that draws a unit past them has nothing to do.  So the grid is known
 // on the host (total_q / 16 + 2 num_seqs units) and the device needs no
 // prefix sum over pages, only the search in cu_q_len that every append makes.
+// Where the tokens are fewer than that (decode rows), each token is a unit,
+// and those that do not open their page for the batch have nothing to do.
+//
+// What bounds it: small batches the chain of loads (lengths, table entry, old
+// exponent), large ones HBM.  Batches of more pieces than fit the GPU at four
+// CTAs per SM take the form with two pieces in flight per warp.  GB300, device
+// time per call: @APPEND@.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -106,19 +113,26 @@ __device__ __forceinline__ void start_piece(const Append8Params& p, const int32_
   int lo = 0, hi = p.num_seqs - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if ((uint32_t)(cu[mid] >> 4) + 2u * (uint32_t)mid <= unit) lo = mid; else hi = mid - 1;
+    const uint32_t first = p.by_token ? (uint32_t)cu[mid] : (uint32_t)(cu[mid] >> 4) + 2u * (uint32_t)mid;
+    if (first <= unit) lo = mid; else hi = mid - 1;
   }
   const int s = lo;
   const int q0 = cu[s], q_len = cu[s + 1] - q0;
   const int ctx = ctxs[s];
   const int off = ctx - q_len;
-  const int k = (int)(unit - (uint32_t)(q0 >> 4) - 2u * (uint32_t)s);
   if (q_len <= 0) return;
   if (off < 0 || q0 < 0 || (int64_t)q0 + q_len > p.total_q) {
     if (lane == 0) report_error(p.dev_error, HB_DEVERR_INDEX);
     return;
   }
-  const int lp = off / kPageSize + k;
+  int lp;
+  if (p.by_token) {
+    const int t = (int)unit - q0;
+    lp = (off + t) / kPageSize;
+    if (t > 0 && (off + t) % kPageSize) return;
+  } else {
+    lp = off / kPageSize + (int)(unit - (uint32_t)(q0 >> 4) - 2u * (uint32_t)s);
+  }
   // (lp < ceil(ctx / 16), without adding to a length near 2^31)
   if (lp > (ctx - 1) / kPageSize) return;
   a.page = -1;
@@ -263,6 +277,7 @@ cudaError_t launch_kv8_append(Append8Params p, int head_dim, int num_sms, cudaSt
   const int64_t pieces = kv8_append_pieces(p.total_q, p.num_seqs, p.num_kv_heads);
   if (pieces > 0x7fffffffLL) return cudaErrorInvalidValue;   // (w + step stays within 32 bits)
   p.num_pieces = (uint32_t)pieces;
+  p.by_token = kv8_append_by_token(p.total_q, p.num_seqs);
   int64_t blocks = (pieces + kA8Warps - 1) / kA8Warps;
   const bool many = blocks > 4 * 2LL * num_sms;
   if (many) blocks = (int64_t)kA8CtasPerSm * num_sms;

@@ -40,7 +40,6 @@ void internal_note_other_launch(void* stream);
 namespace {
 
 constexpr int kPagesThreads = 512;
-constexpr int kRun = 4;                   // tokens per thread and pass (slots)
 constexpr int kSeg = 8;                   // released pages per thread and pass
 constexpr int kPagesMaxSeqs = 16384;      // three int32 per sequence in shared memory
 
@@ -176,6 +175,10 @@ __device__ void write_state(const PagesParams& p, const int64_t* s_state, int64_
   }
 }
 
+// kRun: tokens per thread and pass (slots).  One where a thread per token is
+// at hand (256 decodes: 4.3 us, with four 5.6), four for more (129053 tokens
+// of 1053 rows: 8.0 us, with one 8.3).
+template <int kRun>
 __global__ void __launch_bounds__(kPagesThreads) pages_assign_kernel(const PagesParams p) {
   extern __shared__ int32_t s_dyn[];
   __shared__ int64_t s_state[3];
@@ -332,10 +335,8 @@ hb_status check_common(int32_t num_seqs, int32_t max_pages_per_seq, int32_t num_
 using Kernel = void (*)(const PagesParams);
 
 // One run per thread, at most two CTAs per SM.
-hb_status launch(Kernel kernel, PagesParams& p, int64_t runs, void* stream, const char* what) {
-  int num_sms = 0;
-  const hb_status s = internal_device(&p.dev_error, &num_sms);
-  if (s != HB_OK) return s;
+hb_status launch(Kernel kernel, const PagesParams& p, int64_t runs, int num_sms, void* stream,
+                 const char* what) {
   const int64_t want = (runs + kPagesThreads - 1) / kPagesThreads;
   const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(want, 2LL * num_sms));
   const size_t smem = 3 * ((size_t)p.num_seqs + 1) * sizeof(int32_t);
@@ -386,8 +387,11 @@ extern "C" hb_status hb_pages_assign(int32_t num_seqs, int32_t max_tokens, int32
     p.cu_q_len = cu_q_len;
     p.slot_map = slot_map;
     // the slots' runs, or one page per 16 tokens and sequence
-    const int64_t runs = (int64_t)max_tokens / (slot_map ? kRun : kPageSize) + num_seqs;
-    return launch(pages_assign_kernel, p, runs, stream, "pages_assign launch failed");
+    int num_sms = 0;
+    if ((s = internal_device(&p.dev_error, &num_sms)) != HB_OK) return s;
+    const bool few = max_tokens <= kPagesThreads * num_sms;
+    const int64_t runs = (int64_t)max_tokens / (slot_map ? (few ? 1 : 4) : kPageSize) + num_seqs;
+    return launch(few ? pages_assign_kernel<1> : pages_assign_kernel<4>, p, runs, num_sms, stream, "pages_assign launch failed");
   } catch (...) {
     return internal_fail(HB_ERR_CUDA, "unexpected exception in hb_pages_assign");
   }
@@ -412,7 +416,9 @@ extern "C" hb_status hb_pages_release(int32_t num_seqs, int32_t max_pages_per_se
     p.block_table = const_cast<int32_t*>(block_table);
     // one warp per segment of a row, as long as the table is wide
     const int64_t runs = (int64_t)num_seqs * ((max_pages_per_seq + 32 * kSeg - 1) / (32 * kSeg)) * 32;
-    return launch(pages_release_kernel, p, runs, stream, "pages_release launch failed");
+    int num_sms = 0;
+    if ((s = internal_device(&p.dev_error, &num_sms)) != HB_OK) return s;
+    return launch(pages_release_kernel, p, runs, num_sms, stream, "pages_release launch failed");
   } catch (...) {
     return internal_fail(HB_ERR_CUDA, "unexpected exception in hb_pages_release");
   }

@@ -348,38 +348,35 @@ def hb_attention_new_kv(batch, plan, q, k_new, v_new, k_cache, v_cache, scale, o
 
 # ---------------------------------------------------------------- 8-bit cache
 class _Args:
-    """Argument checks of one call: `ptr` gives a tensor's address after its
-    dtype, layout, shape and device are found right, `stream` the stream's.
-    (A step makes these calls once per layer, so the checks are kept to a few
-    hundred nanoseconds each.)"""
+    """Argument checks of one call: `ptr` gives a tensor's address once its
+    dtype, shape, layout and device are found right (a step makes these calls
+    once per layer: about 0.4 us each), `stream` the stream's handle."""
 
     __slots__ = ("dev",)
 
-    def __init__(self):
-        self.dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    def __init__(self, first):
+        # a CPU tensor is refused by ptr; without one on a GPU, CUDA may not be up
+        self.dev = torch.cuda.current_device() if getattr(first, "is_cuda", False) else None
 
     def ptr(self, t, name, dtype, shape):
-        """`shape`: a tuple, or an int for a 1-D tensor of that or (-1) any size."""
-        if type(t) is not torch.Tensor and not isinstance(t, torch.Tensor):
-            raise ValueError(f"{name} must be a tensor")
-        if t.dtype is not dtype or not t.is_contiguous():
+        try:
+            if (t.dtype is dtype and t.shape == shape and t.get_device() == self.dev
+                    and t.is_contiguous()):
+                return t.data_ptr()
+        except AttributeError:
+            pass
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor")
-        if not (t.shape == shape if type(shape) is tuple else t.dim() == 1 and shape in (-1, t.shape[0])):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
-                             f"{shape if type(shape) is tuple else '(*,)' if shape < 0 else (shape,)}")
-        d = t.get_device()
-        if d < 0:
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if not t.is_cuda:
             raise ValueError(f"{name} must be on a CUDA device")
-        if d != self.dev:
-            if self.dev is None:      # a CUDA tensor exists, so CUDA is up
-                self.dev = torch.cuda.current_device()
-            if d != self.dev:
-                raise ValueError(f"{name} is on cuda:{d}, the current device is cuda:{self.dev}")
-        return t.data_ptr()
+        raise ValueError(f"{name} is on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
 
     def stream(self, stream):
         if stream is None:
-            return torch._C._cuda_getCurrentRawStream(self.dev) if self.dev is not None else None
+            return torch._C._cuda_getCurrentRawStream(self.dev)
         return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
@@ -401,7 +398,7 @@ def kv8_cache(num_pages, num_kv_heads, head_dim, page_size=16, device="cuda"):
 
 def hb_kv8_append(batch, k_new, v_new, k_cache, v_cache, k_exp, v_exp, stream=None):
     """Quantise the batch's new K/V rows (bf16) into the 8-bit cache."""
-    a = _Args()
+    a = _Args(k_new)
     new = (batch.total_q, batch.num_kv_heads, batch.head_dim)
     kn, vn = a.ptr(k_new, "k_new", torch.bfloat16, new), a.ptr(v_new, "v_new", torch.bfloat16, new)
     cache = _kv8_args(a, batch, k_cache, v_cache, k_exp, v_exp)
@@ -423,16 +420,17 @@ _PLAN_WS_TOTAL_AT = 88 + 8 * 5
 def hb_kv8_attention(batch, plan, q, k_cache, v_cache, k_exp, v_exp, scale, out, workspace,
                      stream=None):
     """hb_attention over the 8-bit cache."""
-    a = _Args()
+    a = _Args(q)
     rows = (batch.total_q, batch.num_q_heads, batch.head_dim)
     if not isinstance(plan, np.ndarray) or plan.dtype != np.uint8 or plan.nbytes < HEADER_BYTES:
         raise ValueError("plan must be the uint8 array that hb_kv8_plan returned")
     ws = None
     if workspace is not None:
         need = _PLAN_WS_TOTAL.unpack_from(plan, _PLAN_WS_TOTAL_AT)[0]
-        ws = a.ptr(workspace, "workspace", torch.uint8, -1)
-        if workspace.shape[0] < need:
-            raise ValueError(f"workspace has {workspace.shape[0]} bytes, the plan needs {need}")
+        have = workspace.numel()
+        if have < need:
+            raise ValueError(f"workspace has {have} bytes, the plan needs {need}")
+        ws = a.ptr(workspace, "workspace", torch.uint8, (have,))
     qp = a.ptr(q, "q", torch.bfloat16, rows)
     cache = _kv8_args(a, batch, k_cache, v_cache, k_exp, v_exp)
     st = (_lib or load()).hb_kv8_attention(ctypes.byref(batch), plan.ctypes.data, qp, *cache, scale,
@@ -457,19 +455,24 @@ def hb_pages_assign(q_len, context_len, free_pages, state_in, state_out, block_t
     """Block-table entries, prefix sums and (if given) slots of a step from its
     lengths on the GPU, with pages taken from the ring free_pages / state_in
     (state_out receives the ring's new state and may be state_in)."""
-    a = _Args()
-    n = q_len.numel()
+    a = _Args(q_len)
+    n, pages = q_len.numel(), free_pages.numel()
     max_pages = block_table.shape[1] if block_table.dim() == 2 else 0
+    rows, state = (n,), (4,)
+    if slot_map is None:
+        slots, slots_ptr = 0x7fffffff, None
+    else:
+        slots = slot_map.numel()
+        slots_ptr = a.ptr(slot_map, "slot_map", torch.int64, (slots,))
+    i32 = torch.int32
     st = (_lib or load()).hb_pages_assign(
-        n, slot_map.numel() if slot_map is not None else 0x7fffffff, max_pages, free_pages.numel(),
-        page_size, a.ptr(q_len, "q_len", torch.int32, n),
-        a.ptr(context_len, "context_len", torch.int32, n),
-        a.ptr(free_pages, "free_pages", torch.int32, -1),
-        a.ptr(state_in, "state_in", torch.int64, 4), a.ptr(state_out, "state_out", torch.int64, 4),
-        a.ptr(block_table, "block_table", torch.int32, (n, max_pages)),
-        a.ptr(cu_q_len, "cu_q_len", torch.int32, n + 1),
-        a.ptr(slot_map, "slot_map", torch.int64, -1) if slot_map is not None else None,
-        a.stream(stream))
+        n, slots, max_pages, pages, page_size, a.ptr(q_len, "q_len", i32, rows),
+        a.ptr(context_len, "context_len", i32, rows),
+        a.ptr(free_pages, "free_pages", i32, (pages,)),
+        a.ptr(state_in, "state_in", torch.int64, state),
+        a.ptr(state_out, "state_out", torch.int64, state),
+        a.ptr(block_table, "block_table", i32, (n, max_pages)),
+        a.ptr(cu_q_len, "cu_q_len", i32, (n + 1,)), slots_ptr, a.stream(stream))
     if st:
         _check(st)
 
@@ -478,15 +481,16 @@ def hb_pages_release(lengths, free_pages, state_in, state_out, block_table, page
                      stream=None):
     """The pages of the sequences with lengths > 0 (tokens in the cache) go back
     to the ring."""
-    a = _Args()
-    n = lengths.numel()
+    a = _Args(lengths)
+    n, pages = lengths.numel(), free_pages.numel()
     max_pages = block_table.shape[1] if block_table.dim() == 2 else 0
+    i32, state = torch.int32, (4,)
     st = (_lib or load()).hb_pages_release(
-        n, max_pages, free_pages.numel(), page_size, a.ptr(lengths, "lengths", torch.int32, n),
-        a.ptr(block_table, "block_table", torch.int32, (n, max_pages)),
-        a.ptr(free_pages, "free_pages", torch.int32, -1),
-        a.ptr(state_in, "state_in", torch.int64, 4), a.ptr(state_out, "state_out", torch.int64, 4),
-        a.stream(stream))
+        n, max_pages, pages, page_size, a.ptr(lengths, "lengths", i32, (n,)),
+        a.ptr(block_table, "block_table", i32, (n, max_pages)),
+        a.ptr(free_pages, "free_pages", i32, (pages,)),
+        a.ptr(state_in, "state_in", torch.int64, state),
+        a.ptr(state_out, "state_out", torch.int64, state), a.stream(stream))
     if st:
         _check(st)
 
