@@ -347,45 +347,36 @@ def hb_attention_new_kv(batch, plan, q, k_new, v_new, k_cache, v_cache, scale, o
 
 
 # ---------------------------------------------------------------- 8-bit cache
-class _Args:
-    """Argument checks of one call: `ptr` gives a tensor's address once its
-    dtype, shape, layout and device are found right (a step makes these calls
-    once per layer: about 0.4 us each), `stream` the stream's handle."""
+# A step makes these calls once per layer, so their checks are one expression
+# over everything (about 0.3 us a tensor); only where it fails does _refuse
+# look for what to say.
+_BF16, _E4M3, _I8, _I32, _I64 = (torch.bfloat16, torch.float8_e4m3fn, torch.int8, torch.int32,
+                                 torch.int64)
 
-    __slots__ = ("dev",)
 
-    def __init__(self, first):
-        # a CPU tensor is refused by ptr; without one on a GPU, CUDA may not be up
-        self.dev = torch.cuda.current_device() if getattr(first, "is_cuda", False) else None
-
-    def ptr(self, t, name, dtype, shape):
-        try:
-            if (t.dtype is dtype and t.shape == shape and t.get_device() == self.dev
-                    and t.is_contiguous()):
-                return t.data_ptr()
-        except AttributeError:
-            pass
+def _refuse(*specs):
+    """Raises for the first (name, tensor, dtype, shape) that does not fit."""
+    for name, t, dtype, shape in specs:
         if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor")
-        if t.shape != shape:
+        if tuple(t.shape) != tuple(shape):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if not t.is_cuda:
             raise ValueError(f"{name} must be on a CUDA device")
-        raise ValueError(f"{name} is on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-
-    def stream(self, stream):
-        if stream is None:
-            return torch._C._cuda_getCurrentRawStream(self.dev)
-        return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+    raise ValueError("arguments on different devices")
 
 
-def _kv8_args(a, batch, k_cache, v_cache, k_exp, v_exp):
-    pages, hkv = batch.num_pages, batch.num_kv_heads
-    pool, exps = (pages, batch.page_size, hkv, batch.head_dim), (pages, hkv)
-    return (a.ptr(k_cache, "k_cache", torch.float8_e4m3fn, pool),
-            a.ptr(v_cache, "v_cache", torch.float8_e4m3fn, pool),
-            a.ptr(k_exp, "k_exp", torch.int8, exps), a.ptr(v_exp, "v_exp", torch.int8, exps))
+def _current_device():
+    return torch._C._cuda_getDevice()     # (only once a CUDA tensor is at hand)
+
+
+def _raw_stream(stream, dev):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def kv8_cache(num_pages, num_kv_heads, head_dim, page_size=16, device="cuda"):
@@ -398,11 +389,28 @@ def kv8_cache(num_pages, num_kv_heads, head_dim, page_size=16, device="cuda"):
 
 def hb_kv8_append(batch, k_new, v_new, k_cache, v_cache, k_exp, v_exp, stream=None):
     """Quantise the batch's new K/V rows (bf16) into the 8-bit cache."""
-    a = _Args(k_new)
-    new = (batch.total_q, batch.num_kv_heads, batch.head_dim)
-    kn, vn = a.ptr(k_new, "k_new", torch.bfloat16, new), a.ptr(v_new, "v_new", torch.bfloat16, new)
-    cache = _kv8_args(a, batch, k_cache, v_cache, k_exp, v_exp)
-    st = (_lib or load()).hb_kv8_append(ctypes.byref(batch), kn, vn, *cache, a.stream(stream))
+    pages, hkv, d = batch.num_pages, batch.num_kv_heads, batch.head_dim
+    new, pool, exps = (batch.total_q, hkv, d), (pages, batch.page_size, hkv, d), (pages, hkv)
+    try:
+        dev = k_new.get_device()
+        ok = (k_new.dtype is _BF16 and k_new.shape == new and k_new.is_contiguous()
+              and v_new.dtype is _BF16 and v_new.shape == new and v_new.is_contiguous()
+              and k_cache.dtype is _E4M3 and k_cache.shape == pool and k_cache.is_contiguous()
+              and v_cache.dtype is _E4M3 and v_cache.shape == pool and v_cache.is_contiguous()
+              and k_exp.dtype is _I8 and k_exp.shape == exps and k_exp.is_contiguous()
+              and v_exp.dtype is _I8 and v_exp.shape == exps and v_exp.is_contiguous()
+              and dev >= 0 and dev == v_new.get_device() == k_cache.get_device()
+              == v_cache.get_device() == k_exp.get_device() == v_exp.get_device()
+              and dev == _current_device())
+    except AttributeError:
+        ok = False
+    if not ok:
+        _refuse(("k_new", k_new, _BF16, new), ("v_new", v_new, _BF16, new),
+                ("k_cache", k_cache, _E4M3, pool), ("v_cache", v_cache, _E4M3, pool),
+                ("k_exp", k_exp, _I8, exps), ("v_exp", v_exp, _I8, exps))
+    st = (_lib or load()).hb_kv8_append(
+        ctypes.byref(batch), k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), _raw_stream(stream, dev))
     if st:
         _check(st)
 
@@ -420,22 +428,41 @@ _PLAN_WS_TOTAL_AT = 88 + 8 * 5
 def hb_kv8_attention(batch, plan, q, k_cache, v_cache, k_exp, v_exp, scale, out, workspace,
                      stream=None):
     """hb_attention over the 8-bit cache."""
-    a = _Args(q)
-    rows = (batch.total_q, batch.num_q_heads, batch.head_dim)
+    pages, hkv, d = batch.num_pages, batch.num_kv_heads, batch.head_dim
+    rows, pool, exps = (batch.total_q, batch.num_q_heads, d), (pages, batch.page_size, hkv, d), (pages, hkv)
     if not isinstance(plan, np.ndarray) or plan.dtype != np.uint8 or plan.nbytes < HEADER_BYTES:
         raise ValueError("plan must be the uint8 array that hb_kv8_plan returned")
-    ws = None
-    if workspace is not None:
-        need = _PLAN_WS_TOTAL.unpack_from(plan, _PLAN_WS_TOTAL_AT)[0]
-        have = workspace.numel()
-        if have < need:
-            raise ValueError(f"workspace has {have} bytes, the plan needs {need}")
-        ws = a.ptr(workspace, "workspace", torch.uint8, (have,))
-    qp = a.ptr(q, "q", torch.bfloat16, rows)
-    cache = _kv8_args(a, batch, k_cache, v_cache, k_exp, v_exp)
-    st = (_lib or load()).hb_kv8_attention(ctypes.byref(batch), plan.ctypes.data, qp, *cache, scale,
-                                           a.ptr(out, "out", torch.bfloat16, rows), ws,
-                                           a.stream(stream))
+    need = _PLAN_WS_TOTAL.unpack_from(plan, _PLAN_WS_TOTAL_AT)[0]
+    have = workspace.numel() if workspace is not None else need
+    if have < need:
+        raise ValueError(f"workspace has {have} bytes, the plan needs {need}")
+    try:
+        dev = q.get_device()
+        ok = (q.dtype is _BF16 and q.shape == rows and q.is_contiguous()
+              and out.dtype is _BF16 and out.shape == rows and out.is_contiguous()
+              and k_cache.dtype is _E4M3 and k_cache.shape == pool and k_cache.is_contiguous()
+              and v_cache.dtype is _E4M3 and v_cache.shape == pool and v_cache.is_contiguous()
+              and k_exp.dtype is _I8 and k_exp.shape == exps and k_exp.is_contiguous()
+              and v_exp.dtype is _I8 and v_exp.shape == exps and v_exp.is_contiguous()
+              and dev >= 0 and dev == out.get_device() == k_cache.get_device()
+              == v_cache.get_device() == k_exp.get_device() == v_exp.get_device()
+              and dev == _current_device()
+              and (workspace is None or (workspace.dtype is torch.uint8 and workspace.dim() == 1
+                                         and workspace.is_contiguous()
+                                         and workspace.get_device() == dev)))
+    except AttributeError:
+        ok = False
+    if not ok:
+        specs = [("q", q, _BF16, rows), ("k_cache", k_cache, _E4M3, pool),
+                 ("v_cache", v_cache, _E4M3, pool), ("k_exp", k_exp, _I8, exps),
+                 ("v_exp", v_exp, _I8, exps), ("out", out, _BF16, rows)]
+        if workspace is not None:
+            specs.append(("workspace", workspace, torch.uint8, (have,)))
+        _refuse(*specs)
+    st = (_lib or load()).hb_kv8_attention(
+        ctypes.byref(batch), plan.ctypes.data, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        k_exp.data_ptr(), v_exp.data_ptr(), scale, out.data_ptr(),
+        workspace.data_ptr() if workspace is not None else None, _raw_stream(stream, dev))
     if st:
         _check(st)
 
@@ -455,24 +482,41 @@ def hb_pages_assign(q_len, context_len, free_pages, state_in, state_out, block_t
     """Block-table entries, prefix sums and (if given) slots of a step from its
     lengths on the GPU, with pages taken from the ring free_pages / state_in
     (state_out receives the ring's new state and may be state_in)."""
-    a = _Args(q_len)
     n, pages = q_len.numel(), free_pages.numel()
     max_pages = block_table.shape[1] if block_table.dim() == 2 else 0
-    rows, state = (n,), (4,)
-    if slot_map is None:
-        slots, slots_ptr = 0x7fffffff, None
-    else:
-        slots = slot_map.numel()
-        slots_ptr = a.ptr(slot_map, "slot_map", torch.int64, (slots,))
-    i32 = torch.int32
+    slots = slot_map.numel() if slot_map is not None else 0x7fffffff
+    rows, table, state = (n,), (n, max_pages), (4,)
+    try:
+        dev = q_len.get_device()
+        ok = (q_len.dtype is _I32 and q_len.shape == rows and q_len.is_contiguous()
+              and context_len.dtype is _I32 and context_len.shape == rows and context_len.is_contiguous()
+              and free_pages.dtype is _I32 and free_pages.dim() == 1 and free_pages.is_contiguous()
+              and state_in.dtype is _I64 and state_in.shape == state and state_in.is_contiguous()
+              and state_out.dtype is _I64 and state_out.shape == state and state_out.is_contiguous()
+              and block_table.dtype is _I32 and block_table.shape == table
+              and block_table.is_contiguous()
+              and cu_q_len.dtype is _I32 and cu_q_len.shape == (n + 1,) and cu_q_len.is_contiguous()
+              and dev >= 0 and dev == context_len.get_device() == free_pages.get_device()
+              == state_in.get_device() == state_out.get_device() == block_table.get_device()
+              == cu_q_len.get_device() and dev == _current_device()
+              and (slot_map is None or (slot_map.dtype is _I64 and slot_map.dim() == 1
+                                        and slot_map.is_contiguous()
+                                        and slot_map.get_device() == dev)))
+    except AttributeError:
+        ok = False
+    if not ok:
+        specs = [("q_len", q_len, _I32, rows), ("context_len", context_len, _I32, rows),
+                 ("free_pages", free_pages, _I32, (pages,)), ("state_in", state_in, _I64, state),
+                 ("state_out", state_out, _I64, state), ("block_table", block_table, _I32, table),
+                 ("cu_q_len", cu_q_len, _I32, (n + 1,))]
+        if slot_map is not None:
+            specs.append(("slot_map", slot_map, _I64, (slots,)))
+        _refuse(*specs)
     st = (_lib or load()).hb_pages_assign(
-        n, slots, max_pages, pages, page_size, a.ptr(q_len, "q_len", i32, rows),
-        a.ptr(context_len, "context_len", i32, rows),
-        a.ptr(free_pages, "free_pages", i32, (pages,)),
-        a.ptr(state_in, "state_in", torch.int64, state),
-        a.ptr(state_out, "state_out", torch.int64, state),
-        a.ptr(block_table, "block_table", i32, (n, max_pages)),
-        a.ptr(cu_q_len, "cu_q_len", i32, (n + 1,)), slots_ptr, a.stream(stream))
+        n, slots, max_pages, pages, page_size, q_len.data_ptr(), context_len.data_ptr(),
+        free_pages.data_ptr(), state_in.data_ptr(), state_out.data_ptr(), block_table.data_ptr(),
+        cu_q_len.data_ptr(), slot_map.data_ptr() if slot_map is not None else None,
+        _raw_stream(stream, dev))
     if st:
         _check(st)
 
@@ -481,16 +525,28 @@ def hb_pages_release(lengths, free_pages, state_in, state_out, block_table, page
                      stream=None):
     """The pages of the sequences with lengths > 0 (tokens in the cache) go back
     to the ring."""
-    a = _Args(lengths)
     n, pages = lengths.numel(), free_pages.numel()
     max_pages = block_table.shape[1] if block_table.dim() == 2 else 0
-    i32, state = torch.int32, (4,)
+    rows, table, state = (n,), (n, max_pages), (4,)
+    try:
+        dev = lengths.get_device()
+        ok = (lengths.dtype is _I32 and lengths.shape == rows and lengths.is_contiguous()
+              and block_table.dtype is _I32 and block_table.shape == table
+              and block_table.is_contiguous()
+              and free_pages.dtype is _I32 and free_pages.dim() == 1 and free_pages.is_contiguous()
+              and state_in.dtype is _I64 and state_in.shape == state and state_in.is_contiguous()
+              and state_out.dtype is _I64 and state_out.shape == state and state_out.is_contiguous()
+              and dev >= 0 and dev == block_table.get_device() == free_pages.get_device()
+              == state_in.get_device() == state_out.get_device() and dev == _current_device())
+    except AttributeError:
+        ok = False
+    if not ok:
+        _refuse(("lengths", lengths, _I32, rows), ("block_table", block_table, _I32, table),
+                ("free_pages", free_pages, _I32, (pages,)), ("state_in", state_in, _I64, state),
+                ("state_out", state_out, _I64, state))
     st = (_lib or load()).hb_pages_release(
-        n, max_pages, pages, page_size, a.ptr(lengths, "lengths", i32, (n,)),
-        a.ptr(block_table, "block_table", i32, (n, max_pages)),
-        a.ptr(free_pages, "free_pages", i32, (pages,)),
-        a.ptr(state_in, "state_in", torch.int64, state),
-        a.ptr(state_out, "state_out", torch.int64, state), a.stream(stream))
+        n, max_pages, pages, page_size, lengths.data_ptr(), block_table.data_ptr(),
+        free_pages.data_ptr(), state_in.data_ptr(), state_out.data_ptr(), _raw_stream(stream, dev))
     if st:
         _check(st)
 
