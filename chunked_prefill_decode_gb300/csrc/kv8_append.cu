@@ -131,11 +131,14 @@ __device__ __forceinline__ void start_piece(const Append8Params& p, const int32_
   }
   int lp;
   if (p.by_token) {
-    const int t = (int)unit - q0;
-    lp = (off + t) / kPageSize;
-    if (t > 0 && (off + t) % kPageSize) return;
+    const uint32_t t = unit - (uint32_t)q0;
+    if (t >= (uint32_t)q_len) return;   // a token of no sequence
+    lp = (off + (int)t) / kPageSize;
+    if (t > 0 && (off + (int)t) % kPageSize) return;
   } else {
-    lp = off / kPageSize + (int)(unit - (uint32_t)(q0 >> 4) - 2u * (uint32_t)s);
+    const int k = (int)(unit - (uint32_t)(q0 >> 4) - 2u * (uint32_t)s);
+    if (k < 0) return;                  // (before the first sequence's tokens)
+    lp = off / kPageSize + k;
   }
   // (lp < ceil(ctx / 16), without adding to a length near 2^31)
   if (lp > (ctx - 1) / kPageSize) return;

@@ -460,3 +460,23 @@ def test_full_size_workloads(name):
         tok = None if n == 1 else np.unique(np.concatenate([[0, n - 1], rng.choice(n, 12)]))
         ref, tol = bounds(sub, inp, small, tokens=tok)
         check_out(out[cu[s]:cu[s] + n], ref, tol, tokens=tok)
+
+
+@pytest.mark.parametrize("rows", [[(1, 20), (1, 33), (1, 16)], [(1, 3 + i) for i in range(40)],
+                                  [(30, 40), (5, 5), (17, 100)]])
+def test_append_with_tokens_of_no_sequence(rows):
+    """New rows before the first sequence's and behind the last one's: not read,
+    whatever they hold, and written nowhere."""
+    layout = layout_from_rows(Shape(8, 4, 64), rows, 61)
+    inp = Inputs(layout, 62)
+    hb = lib()
+    db = from_layout(layout, "cuda:0")
+    cache = inp.device()
+    first, behind = 20, 9
+    new = [torch.cat([torch.full((first, 4, 64), float("inf")), x.float(), torch.full((behind, 4, 64), 1e30)])
+           .to(torch.bfloat16).cuda() for x in (inp.k_new, inp.v_new)]
+    db.cu_q_len.add_(first)
+    db.batch.total_q = layout.total_q + first + behind
+    hb.hb_kv8_append(db.batch, *new, *cache)
+    hb.hb_check()
+    check_append(layout, inp, cache)
