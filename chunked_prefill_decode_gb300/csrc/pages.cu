@@ -19,7 +19,8 @@
 // grid-wide wait) and then writes its share of the tokens and of the pages.
 //
 // The ring's head and tail may be read and written in place: every CTA reads
-// them first, then counts itself in; the last one to do so writes them back.
+// them first, then counts itself in (in the state's third entry); the last one
+// to do so writes them back.  Into another array the first CTA writes them.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -158,11 +159,11 @@ __device__ __forceinline__ int owner(const int32_t* sums, int S, int x) {
 }
 
 // Head and tail as the launch found them (s_state) moved by `dh` / `dt`,
-// written by the last CTA to have read them.
+// written by the last CTA to have read them, or to another array by the first.
 __device__ void write_state(const PagesParams& p, const int64_t* s_state, int64_t dh, int64_t dt) {
   if (threadIdx.x != 0) return;
-  bool last = gridDim.x == 1;
-  if (!last) {
+  bool last = blockIdx.x == 0;
+  if (gridDim.x > 1 && p.state_out == p.state_in) {
     __threadfence();
     last = atomicAdd(reinterpret_cast<unsigned long long*>(p.state_out + 2), 1ull) + 1ull == gridDim.x;
     __threadfence();
@@ -329,6 +330,9 @@ hb_status check_common(int32_t num_seqs, int32_t max_pages_per_seq, int32_t num_
     return internal_fail(HB_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
   if ((reinterpret_cast<uintptr_t>(state_in) | reinterpret_cast<uintptr_t>(state_out)) & 7u)
     return internal_fail(HB_ERR_INVALID_ARG, "state_in and state_out must be 8-byte aligned");
+  const uintptr_t a = reinterpret_cast<uintptr_t>(state_in), b = reinterpret_cast<uintptr_t>(state_out);
+  if (a != b && a < b + 32 && b < a + 32)
+    return internal_fail(HB_ERR_INVALID_ARG, "state_in and state_out overlap without being one");
   return HB_OK;
 }
 

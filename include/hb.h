@@ -312,10 +312,11 @@ hb_status hb_kv8_attention(const hb_batch* batch, const void* h_plan, const void
  * and a state of four int64: state[0] pages taken so far (head), state[1]
  * pages put in so far (tail), 0 <= head <= tail <= head + num_pages;
  * the free pages are free_pages[i % num_pages] for head <= i < tail, taken in
- * that order.  state[2] and state[3] must be zero before the first call and
- * are left zero (a full pool starts as free_pages = 0 .. num_pages-1, state =
- * {0, num_pages, 0, 0}).  state_in is read and state_out written (its four
- * entries); both may be the same array.  Calls on one ring must be ordered.
+ * that order.  state[2] and state[3] are zero (a full pool starts as
+ * free_pages = 0 .. num_pages-1, state = {0, num_pages, 0, 0}).  state_in is
+ * read and state_out written (its four entries, whatever they held); both may
+ * be the same array, and must not overlap otherwise (HB_ERR_INVALID_ARG).
+ * Calls on one ring must be ordered.
  *
  * Lengths are read on the device, so mistakes in them are found there: the
  * call then changes nothing but the error word (state_out = state_in), and

@@ -261,3 +261,20 @@ def test_a_run_of_steps(geom, window):
         inp = Inp()
         inp.q = qt
         check_out(out, *bounds(layout, inp, o_cache))
+
+
+def test_state_out_may_hold_anything():
+    """Many CTAs; the state written to an array of its own, whatever that held."""
+    hb = lib()
+    n, pages_, maxp = 700, 9000, 12
+    ring, state = hb.pages_ring(pages_)
+    q = torch.full((n,), 150, dtype=torch.int32, device="cuda")
+    table = torch.full((n, maxp), -1, dtype=torch.int32, device="cuda")
+    cu = torch.empty(n + 1, dtype=torch.int32, device="cuda")
+    slots = torch.empty(n * 150, dtype=torch.int64, device="cuda")
+    after, back = (torch.full((4,), 77, dtype=torch.int64, device="cuda") for _ in range(2))
+    hb.hb_pages_assign(q, q, ring, state, after, table, cu, slots)
+    hb.hb_pages_release(q, ring, after, back, table)
+    hb.hb_check()
+    assert state.tolist() == [0, pages_, 0, 0]
+    assert after.tolist() == [7000, pages_, 0, 0] and back.tolist() == [7000, pages_ + 7000, 0, 0]

@@ -232,3 +232,10 @@ def test_binding_refuses_tensors_that_do_not_fit():
         hb.hb_pages_release(i32, i32, st, st, i32.view(2, 1))
     with pytest.raises(ValueError, match="every page"):
         hb.pages_ring(4, [0, 1], device="cpu")
+
+
+def test_a_ring_state_that_overlaps_the_other_is_refused():
+    L = lib().load()
+    for d in (-24, -8, 8, 24):
+        assert L.hb_pages_assign(*assign_args(state_out=FAKE + d)) == 1
+        assert L.hb_pages_release(2, 4, 16, 16, FAKE, FAKE, FAKE, FAKE, FAKE + d, None) == 1
