@@ -15,7 +15,11 @@
 // the scales, and a page whose values are tiny next to another's weighs as
 // little in o as it should, so P fits fp16 (11 significant bits, against
 // bf16's 8) for any spread of scales.  P carries a factor 2^7 that cancels in
-// o, which puts fp16's smallest step at 2^-31 of the largest weight.
+// o, which puts fp16's smallest step at 2^-31 of the largest weight.  In l the
+// factor 2^-ve brings such a page back, so P is formed with 2^48 more before
+// it is rounded (256 decodes 349 us with and without it; with exponentials that
+// keep results below 2^-126 instead 352), and merges take their weights from
+// such exponentials: of pages 2^128 apart each weight in l is good to 2^-14.
 // q is scaled by a power of two per head so that its largest element is near
 // 2^12 and every element keeps its bits in fp16; e4m3 is exact in fp16.
 //
@@ -74,6 +78,7 @@ inline __host__ __device__ constexpr int decode8_pages(int head_dim) { return 25
 constexpr int kDec8MaxStages = 14;
 constexpr float kDec8RescaleThreshold = 8.0f;   // log2 units
 constexpr float kDec8PShift = 7.0f;             // P <= 2^(8 + 7) in fp16
+constexpr int kDec8LShift = 48;                 // of P before it is rounded, see above
 constexpr int kDec8Regs = 224;        // per thread, warps 0-7
 constexpr int kDec8LightRegs = 56;    // per thread, warps 8-11
 static_assert(256 * kDec8Regs + 128 * kDec8LightRegs <= 384 * 168,
@@ -161,7 +166,7 @@ __device__ __forceinline__ void merge_rows8(const DecodeParams& p, const DecodeI
           st2 = make_float2(-INFINITY, 0.f);
           if (base + lane < it.n_splits) st2 = __ldcg(&ml[(size_t)(it.slot + base + lane) * Hq + hh[h]]);
         }
-        wgt[h] = fast_exp2(st2.x - mmax[h]);   // 0 past the pieces
+        wgt[h] = exp2_approx(st2.x - mmax[h]);   // 0 past the pieces
         lsum[h] += wgt[h] * st2.y;
       }
       const int m = min(32, it.n_splits - base);
@@ -497,7 +502,7 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
               const int ke = (int)(int8_t)(ex & 0xff), ve = ex >> 8;
               fk[u] = pow2i(ke);
               fv[u] = (float)ve;
-              inv_v[u] = pow2i(-ve);
+              inv_v[u] = pow2i(-ve - kDec8LShift);
               const int lp = lp0 + u * parts;
               // (a page past the item's end: the stage holds none, no key is seen)
               valid[u] = lp < it.page_end ? min(kPageSize, it.ctx - lp * kPageSize) : 0;
@@ -576,7 +581,7 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
                   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                   if (mx > m_run[nq][e] + kDec8RescaleThreshold) {
-                    alpha[nq][e] = fast_exp2(m_run[nq][e] - mx);
+                    alpha[nq][e] = exp2_approx(m_run[nq][e] - mx);
                     m_run[nq][e] = mx;
                   }
                 }
@@ -594,15 +599,19 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
               for (int e = 0; e < 2; ++e) l_part[nq][e] *= alpha[nq][e];
 #pragma unroll
               for (int u = 0; u < U; ++u) {
-                float p0[2], p1[2];
+                float p0[2], p1[2];   // P 2^kDec8LShift
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   // no key seen yet: every x is -inf and so is P's exponent
-                  const float mu = (m_run[nq][e] == -INFINITY ? 0.f : m_run[nq][e]) - kDec8PShift;
+                  const float mu =
+                      (m_run[nq][e] == -INFINITY ? 0.f : m_run[nq][e]) - (kDec8PShift + kDec8LShift);
                   p0[e] = fast_exp2(x0[u][nq][e] - mu);
                   p1[e] = fast_exp2(x1[u][nq][e] - mu);
                   l_part[nq][e] = fmaf(p0[e] + p1[e], inv_v[u], l_part[nq][e]);
                 }
+                const uint64_t down = pack_f32x2(pow2i(-kDec8LShift), pow2i(-kDec8LShift));
+                unpack_f32x2(mul_f32x2(pack_f32x2(p0[0], p0[1]), down), p0[0], p0[1]);
+                unpack_f32x2(mul_f32x2(pack_f32x2(p1[0], p1[1]), down), p1[0], p1[1]);
                 pb[u][nq][0] = movmatrix_trans(pack_f16x2(p0[0], p0[1]));   // B: keys 2c, 2c + 1 of head r
                 pb[u][nq][1] = movmatrix_trans(pack_f16x2(p1[0], p1[1]));   // keys 8 + 2c ..
               }
@@ -695,8 +704,8 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
               for (int e = 0; e < 2; ++e) {
                 const float m2 = src[32 * k++], l2 = src[32 * k++];
                 const float mm = fmaxf(m_run[nq][e], m2);
-                wa[nq][e] = m_run[nq][e] == -INFINITY ? 0.f : fast_exp2(m_run[nq][e] - mm);
-                wb[nq][e] = m2 == -INFINITY ? 0.f : fast_exp2(m2 - mm);
+                wa[nq][e] = m_run[nq][e] == -INFINITY ? 0.f : exp2_approx(m_run[nq][e] - mm);
+                wb[nq][e] = m2 == -INFINITY ? 0.f : exp2_approx(m2 - mm);
                 m_run[nq][e] = mm;
                 l_tot[nq][e] = l_tot[nq][e] * wa[nq][e] + l2 * wb[nq][e];
               }

@@ -462,6 +462,22 @@ def test_full_size_workloads(name):
         check_out(out[cu[s]:cu[s] + n], ref, tol, tokens=tok)
 
 
+@pytest.mark.parametrize("geom", [(16, 4, 128), (8, 1, 64)])
+def test_scales_at_both_ends_of_the_range(geom):
+    """Pages whose V scales are 2^64 and 2^-64: the values of the latter vanish
+    beside the former's, their weights do not.  (Those come as 2^(x - M) down to
+    2^-136, 13 bits of a number below 2^-126, so they are good to 2^-14, which
+    lies inside the 2^-8 - 2^-11 that `bounds` grants fp16 weights too much.)"""
+    layout = layout_from_rows(Shape(*geom), [(1, 400), (1, 33), (30, 200), (1, 3000), (1, 1200)], 58)
+    inp = Inputs(layout, 59)
+    cache = list(inp.oracle_append(layout))
+    g = np.random.default_rng(60)
+    cache[3] = g.choice([-64, 64], cache[3].shape).astype(np.int8)
+    inp.cache, inp.exps = cache[:2], cache[2:]
+    _, out = step(layout, inp, append=False)
+    check_out(out, *bounds(layout, inp, cache))
+
+
 @pytest.mark.parametrize("rows", [[(1, 20), (1, 33), (1, 16)], [(1, 3 + i) for i in range(40)],
                                   [(30, 40), (5, 5), (17, 100)]])
 def test_append_with_tokens_of_no_sequence(rows):
