@@ -32,7 +32,8 @@ __global__ void __launch_bounds__(kWidenThreads) kv8_widen_kernel(const WidenPar
     if (__ldg(&p.items[mid].ws_page) <= unit) lo = mid; else hi = mid - 1;
   }
   const WidenItem it = p.items[lo];
-  // (the plan was there before the launch before this one began)
+  // (hb_kv8_plan writes the items with a copy, which no launch overtakes: they
+  // may be read before the wait)
   griddep_wait();
   griddep_launch_dependents();
   const int lp = it.page_begin + unit - it.ws_page;
@@ -72,7 +73,8 @@ __global__ void __launch_bounds__(kWidenThreads) kv8_widen_kernel(const WidenPar
 
 cudaError_t launch_kv8_widen(const WidenParams& p, cudaStream_t stream) {
   if (p.num_units == 0) return cudaSuccess;
-  return launch_serialized(p.head_dim == 128 ? kv8_widen_kernel<128> : kv8_widen_kernel<64>, 2u * (unsigned)p.num_units, kWidenThreads, 0, stream, p);
+  return launch_serialized(p.head_dim == 128 ? kv8_widen_kernel<128> : kv8_widen_kernel<64>,
+                           2u * (unsigned)p.num_units, kWidenThreads, 0, stream, p);
 }
 
 }  // namespace hb
