@@ -27,10 +27,12 @@
 //
 // What bounds it: small batches the chain of loads (lengths, table entry, old
 // exponent), large ones HBM.  Batches of more pieces than fit the GPU at four
-// CTAs per SM take the form with two pieces in flight per warp.  GB300, device
-// time per call: 68 tokens (8 heads of 64) 2.5 us; 256 decodes (8 heads of 128)
-// 4.9, with page units 7.2; 16201 tokens 20.4 (4.9 TB/s), with one piece per
-// warp 39.6.
+// CTAs per SM take the form where a warp keeps K and V of a page in flight and
+// finds the place of both at once (with a place for each, 661 instructions a
+// piece and half the issue slots).  GB300, device time per call: 68 tokens (8
+// heads of 64) 2.6 us; 256 decodes (8 heads of 128) 4.8, with page units 7.2;
+// 16201 tokens from HBM 20.8 (4.8 TB/s), from L2 15.2, with a place for each
+// 23.9 and 20.5, with one piece per warp 39.6 from L2.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -87,32 +89,29 @@ __device__ __forceinline__ uint32_t finite_abs2(uint32_t v) {
   return lo | hi << 16;
 }
 
-// One warp's share of the work: the new tokens of one page, one head and one
-// of K and V, with their rows on the way to registers.  D bf16 of one token
-// and head are D / 8 lanes' 16 bytes, so a warp access covers 256 / D tokens
-// and a page takes D / 16 of them.
+// The new tokens of one page and one head, K or V or both.  D bf16 of one
+// token and head are D / 8 lanes' 16 bytes, so a warp access covers 256 / D
+// tokens and a page takes D / 16 of them (kIters).
 template <int D>
-struct Piece {
+struct Rows {
   static constexpr int kLanesPerRow = D / 8;
   static constexpr int kRows = 32 / kLanesPerRow;
   static constexpr int kIters = kPageSize / kRows;
-  uint4 x[kIters];
-  int page;        // block-table entry, checked where it is used
-  int part;        // head, or Hkv + head for V; -1: nothing to do
-  int old;         // the page's exponent, where it holds older tokens
-  int s0, s1;      // slots of the page that receive tokens
 };
 
-// Finds the piece and starts its loads (the rows' addresses need no page).
-template <int D>
-__device__ __forceinline__ void start_piece(const Append8Params& p, const int32_t* cu,
-                                            const int32_t* ctxs, uint32_t w, Piece<D>& a) {
-  using P = Piece<D>;
-  const int lane = threadIdx.x & 31;
-  const uint32_t per_unit = 2u * (uint32_t)p.num_kv_heads;
-  const uint32_t unit = w / per_unit;
-  a.part = -1;
-  if (w >= p.num_pieces) return;
+struct Place {
+  int page;        // block-table entry, checked where it is used
+  int head;        // -1: nothing to do
+  int s0, s1;      // slots of the page that receive tokens
+  int tok;         // the token that slot 0 holds, or would (below 0 at worst by 15)
+};
+
+// Finds the place of unit `unit`; the table entry may still be on its way.
+__device__ __forceinline__ Place find_place(const Append8Params& p, const int32_t* cu,
+                                            const int32_t* ctxs, uint32_t unit, int head) {
+  Place a;
+  a.page = a.head = -1;
+  a.s0 = a.s1 = a.tok = 0;
   // the sequence whose units hold this one
   int lo = 0, hi = p.num_seqs - 1;
   while (lo < hi) {
@@ -124,98 +123,94 @@ __device__ __forceinline__ void start_piece(const Append8Params& p, const int32_
   const int q0 = cu[s], q_len = cu[s + 1] - q0;
   const int ctx = ctxs[s];
   const int off = ctx - q_len;
-  if (q_len <= 0) return;
+  if (q_len <= 0) return a;
   if (off < 0 || q0 < 0 || (int64_t)q0 + q_len > p.total_q) {
-    if (lane == 0) report_error(p.dev_error, HB_DEVERR_INDEX);
-    return;
+    if ((threadIdx.x & 31) == 0) report_error(p.dev_error, HB_DEVERR_INDEX);
+    return a;
   }
   int lp;
   if (p.by_token) {
     const uint32_t t = unit - (uint32_t)q0;
-    if (t >= (uint32_t)q_len) return;   // a token of no sequence
+    if (t >= (uint32_t)q_len) return a;   // a token of no sequence
     lp = (off + (int)t) / kPageSize;
-    if (t > 0 && (off + (int)t) % kPageSize) return;
+    if (t > 0 && (off + (int)t) % kPageSize) return a;
   } else {
     const int k = (int)(unit - (uint32_t)(q0 >> 4) - 2u * (uint32_t)s);
-    if (k < 0) return;                  // (before the first sequence's tokens)
+    if (k < 0) return a;                  // (before the first sequence's tokens)
     lp = off / kPageSize + k;
   }
   // (lp < ceil(ctx / 16), without adding to a length near 2^31)
-  if (lp > (ctx - 1) / kPageSize) return;
-  a.page = -1;
+  if (lp > (ctx - 1) / kPageSize) return a;
   if (lp < p.max_pages_per_seq) a.page = __ldcg(&p.block_table[(size_t)s * p.max_pages_per_seq + lp]);
-  // slots s0 .. s1-1 of the page receive tokens tok0 ..
-  a.part = (int)(w - unit * per_unit);
+  a.head = head;
   a.s0 = max(0, off - lp * kPageSize);
   a.s1 = min(kPageSize, ctx - lp * kPageSize);
-  const int tok0 = q0 + lp * kPageSize + a.s0 - off;
-  const bool is_v = a.part >= p.num_kv_heads;
-  const int head = is_v ? a.part - p.num_kv_heads : a.part;
-  const int sub = lane / P::kLanesPerRow, l = lane % P::kLanesPerRow;
+  a.tok = q0 + (lp * kPageSize - off);
+  return a;
+}
+
+// Starts the loads of its rows of `src` (k_new or v_new; no page is needed).
+template <int D>
+__device__ __forceinline__ void load_rows(const Append8Params& p, const Place& a, const uint16_t* src,
+                                          uint4* x) {
+  using R = Rows<D>;
+  if (a.head < 0) return;
+  const int lane = threadIdx.x & 31, sub = lane / R::kLanesPerRow, l = lane % R::kLanesPerRow;
   const size_t row = (size_t)p.num_kv_heads * D;   // elements of one token
-  // (where slot `sub` would be; only the slots that receive tokens are read)
-  const uint16_t* src = (is_v ? p.v_new : p.k_new) + (int64_t)head * D + l * 8 +
-                        ((int64_t)tok0 + sub - a.s0) * (int64_t)row;
+  // (only the slots that receive tokens are read)
+  const uint16_t* at = src + (int64_t)a.head * D + l * 8 + ((int64_t)a.tok + sub) * (int64_t)row;
+  if (a.s1 - a.s0 == kPageSize) {
 #pragma unroll
-  for (int i = 0; i < P::kIters; ++i) {
-    const uint32_t from = (uint32_t)(i * P::kRows + sub - a.s0);
-    a.x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (from < (uint32_t)(a.s1 - a.s0)) a.x[i] = ld_stream16(src + (size_t)(i * P::kRows) * row);
+    for (int i = 0; i < R::kIters; ++i) x[i] = ld_stream16(at + (size_t)(i * R::kRows) * row);
+  } else {
+#pragma unroll
+    for (int i = 0; i < R::kIters; ++i) {
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      if ((uint32_t)(i * R::kRows + sub - a.s0) < (uint32_t)(a.s1 - a.s0))
+        x[i] = ld_stream16(at + (size_t)(i * R::kRows) * row);
+    }
   }
 }
 
-template <int D>
-__device__ __forceinline__ int8_t* exponent_of(const Append8Params& p, const Piece<D>& a) {
-  const bool is_v = a.part >= p.num_kv_heads;
-  return (is_v ? p.v_exp : p.k_exp) + (size_t)a.page * p.num_kv_heads +
-         (is_v ? a.part - p.num_kv_heads : a.part);
+// The page is known: false (and reported) if it is none.
+__device__ __forceinline__ bool check_page(const Append8Params& p, const Place& a) {
+  if (a.head < 0) return false;
+  if ((unsigned)a.page < (unsigned)p.num_pages) return true;
+  if ((threadIdx.x & 31) == 0) report_error(p.dev_error, HB_DEVERR_INDEX);
+  return false;
 }
 
-// The page is known: checks it, and asks for the exponent that it has.
+// Quantises the rows into `cache` (k_cache or v_cache), with `exps` its
+// exponents.
 template <int D>
-__device__ __forceinline__ void check_piece(const Append8Params& p, Piece<D>& a) {
-  if (a.part < 0) return;
-  if ((unsigned)a.page >= (unsigned)p.num_pages) {
-    if ((threadIdx.x & 31) == 0) report_error(p.dev_error, HB_DEVERR_INDEX);
-    a.part = -1;
-    return;
-  }
-  a.old = kKv8MinExp;
-  if (a.s0 > 0) a.old = ldcg_s8(exponent_of(p, a));
-}
-
-template <int D>
-__device__ __forceinline__ void finish_piece(const Append8Params& p, Piece<D>& a) {
-  using P = Piece<D>;
-  if (a.part < 0) return;
-  const int lane = threadIdx.x & 31;
-  const bool is_v = a.part >= p.num_kv_heads;
-  const int head = is_v ? a.part - p.num_kv_heads : a.part;
-  const int sub = lane / P::kLanesPerRow, l = lane % P::kLanesPerRow;
+__device__ __forceinline__ void finish_rows(const Append8Params& p, const Place& a, uint8_t* cache,
+                                            int8_t* exps, uint4* x) {
+  using R = Rows<D>;
+  const int lane = threadIdx.x & 31, sub = lane / R::kLanesPerRow, l = lane % R::kLanesPerRow;
   const size_t row = (size_t)p.num_kv_heads * D;
-  uint8_t* dst = (is_v ? p.v_cache : p.k_cache) +
-                 ((size_t)a.page * kPageSize * p.num_kv_heads + head) * D + l * 8;
-  const int old = kv8_exp((int8_t)a.old);
+  uint8_t* dst = cache + ((size_t)a.page * kPageSize * p.num_kv_heads + a.head) * D + l * 8;
+  int8_t* exp_at = exps + (size_t)a.page * p.num_kv_heads + a.head;
+  const int old = a.s0 > 0 ? kv8_exp(ldcg_s8(exp_at)) : kKv8MinExp;
   auto largest = [&](auto magnitude) -> uint32_t {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < P::kIters; ++i)
-      m = max_u16x2(max_u16x2(m, max_u16x2(magnitude(a.x[i].x), magnitude(a.x[i].y))),
-                    max_u16x2(magnitude(a.x[i].z), magnitude(a.x[i].w)));
+    for (int i = 0; i < R::kIters; ++i)
+      m = max_u16x2(max_u16x2(m, max_u16x2(magnitude(x[i].x), magnitude(x[i].y))),
+                    max_u16x2(magnitude(x[i].z), magnitude(x[i].w)));
     return __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
   };
   uint32_t m = largest([](uint32_t v) { return v & 0x7fff7fffu; });
   if (m >= kInf) {   // rare: taken over the finite ones instead
     m = largest([](uint32_t v) { return finite_abs2(v); });
 #pragma unroll
-    for (int i = 0; i < P::kIters; ++i)
-      a.x[i] = make_uint4(infinite_to_nan2(a.x[i].x), infinite_to_nan2(a.x[i].y),
-                          infinite_to_nan2(a.x[i].z), infinite_to_nan2(a.x[i].w));
+    for (int i = 0; i < R::kIters; ++i)
+      x[i] = make_uint4(infinite_to_nan2(x[i].x), infinite_to_nan2(x[i].y), infinite_to_nan2(x[i].z),
+                        infinite_to_nan2(x[i].w));
   }
   const int e = max(old, kv8_need_exp(m));
   if (e > old && a.s0 > 0) {
     const float down = pow2i(old - e);
-    for (int slot = sub; slot < a.s0; slot += P::kRows) {
+    for (int slot = sub; slot < a.s0; slot += R::kRows) {
       uint2 v = *reinterpret_cast<const uint2*>(dst + (size_t)slot * row);
       uint32_t* b = &v.x;
 #pragma unroll
@@ -229,21 +224,30 @@ __device__ __forceinline__ void finish_piece(const Append8Params& p, Piece<D>& a
   }
   const float mul = pow2i(-e);
   uint8_t* dst_sub = dst + (size_t)sub * row;
+  auto quantised = [&](const uint4& v) {
+    return make_uint2(quantise2(v.x, mul) | quantise2(v.y, mul) << 16,
+                      quantise2(v.z, mul) | quantise2(v.w, mul) << 16);
+  };
+  if (a.s1 - a.s0 == kPageSize) {
 #pragma unroll
-  for (int i = 0; i < P::kIters; ++i) {
-    if (i * P::kRows >= a.s1 || (i + 1) * P::kRows <= a.s0) continue;   // (alike in the warp)
-    if ((uint32_t)(i * P::kRows + sub - a.s0) < (uint32_t)(a.s1 - a.s0))
-      *reinterpret_cast<uint2*>(dst_sub + (size_t)(i * P::kRows) * row) =
-          make_uint2(quantise2(a.x[i].x, mul) | quantise2(a.x[i].y, mul) << 16,
-                     quantise2(a.x[i].z, mul) | quantise2(a.x[i].w, mul) << 16);
+    for (int i = 0; i < R::kIters; ++i)
+      *reinterpret_cast<uint2*>(dst_sub + (size_t)(i * R::kRows) * row) = quantised(x[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < R::kIters; ++i) {
+      if (i * R::kRows >= a.s1 || (i + 1) * R::kRows <= a.s0) continue;   // (alike in the warp)
+      if ((uint32_t)(i * R::kRows + sub - a.s0) < (uint32_t)(a.s1 - a.s0))
+        *reinterpret_cast<uint2*>(dst_sub + (size_t)(i * R::kRows) * row) = quantised(x[i]);
+    }
   }
   __syncwarp();   // every lane has read the old exponent
-  if (lane == 0) *exponent_of(p, a) = (int8_t)e;
+  if (lane == 0) *exp_at = (int8_t)e;
 }
 
-// kMany: each warp takes pieces w, w + warps, .. and starts the next one's
-// loads before it finishes the one at hand; else one piece per warp, in more
-// and smaller warps.
+// kMany: a warp takes K and V of a page and head at once (their places, rows
+// and checks are alike), w, w + warps, .., and starts the next ones' loads as
+// it finishes those at hand; else K or V, one per warp, in more and smaller
+// warps.
 template <int D, bool kMany>
 __global__ void __launch_bounds__(kA8Threads, kMany ? kA8CtasPerSm : 4)
     kv8_append_kernel(const Append8Params p) {
@@ -259,23 +263,35 @@ __global__ void __launch_bounds__(kA8Threads, kMany ? kA8CtasPerSm : 4)
   __syncthreads();
   const int32_t* cu = staged ? s_cu : p.cu_q_len;
   const int32_t* ctxs = staged ? s_ctx : p.context_len;
+  const uint32_t heads = (uint32_t)p.num_kv_heads;
   uint32_t w = blockIdx.x * kA8Warps + (threadIdx.x >> 5);
-  Piece<D> a;
-  start_piece<D>(p, cu, ctxs, w, a);
-  check_piece<D>(p, a);
   if constexpr (!kMany) {
-    finish_piece<D>(p, a);
+    if (w >= p.num_pieces) return;
+    const uint32_t unit = w / (2u * heads), part = w - unit * 2u * heads;
+    const bool is_v = part >= heads;
+    const Place a = find_place(p, cu, ctxs, unit, (int)(is_v ? part - heads : part));
+    uint4 x[Rows<D>::kIters];
+    load_rows<D>(p, a, is_v ? p.v_new : p.k_new, x);
+    if (check_page(p, a)) finish_rows<D>(p, a, is_v ? p.v_cache : p.k_cache, is_v ? p.v_exp : p.k_exp, x);
   } else {
-    // (two pieces by name: a copy would wait for the loads)
-    const uint32_t step = gridDim.x * kA8Warps;
-    Piece<D> b;
-    for (; w < p.num_pieces; w += 2 * step) {
-      start_piece<D>(p, cu, ctxs, w + step, b);
-      finish_piece<D>(p, a);
-      check_piece<D>(p, b);
-      start_piece<D>(p, cu, ctxs, w + 2 * step, a);
-      finish_piece<D>(p, b);
-      check_piece<D>(p, a);
+    const uint32_t step = gridDim.x * kA8Warps, pairs = p.num_pieces / 2u;
+    uint4 xk[Rows<D>::kIters], xv[Rows<D>::kIters];
+    auto place = [&](uint32_t i) -> Place {
+      const uint32_t unit = i / heads;
+      if (i < pairs) return find_place(p, cu, ctxs, unit, (int)(i - unit * heads));
+      return Place{-1, -1, 0, 0, 0};
+    };
+    Place a = place(w);
+    load_rows<D>(p, a, p.k_new, xk);
+    load_rows<D>(p, a, p.v_new, xv);
+    for (; w < pairs; w += step) {
+      const Place b = place(w + step);
+      const bool ok = check_page(p, a);
+      if (ok) finish_rows<D>(p, a, p.k_cache, p.k_exp, xk);
+      load_rows<D>(p, b, p.k_new, xk);
+      if (ok) finish_rows<D>(p, a, p.v_cache, p.v_exp, xv);
+      load_rows<D>(p, b, p.v_new, xv);
+      a = b;
     }
   }
 }
@@ -289,7 +305,7 @@ cudaError_t launch_kv8_append(Append8Params p, int head_dim, int num_sms, cudaSt
   p.by_token = kv8_append_by_token(p.total_q, p.num_seqs);
   int64_t blocks = (pieces + kA8Warps - 1) / kA8Warps;
   const bool many = blocks > 4 * 2LL * num_sms;
-  if (many) blocks = (int64_t)kA8CtasPerSm * num_sms;
+  if (many) blocks = std::min<int64_t>((blocks + 1) / 2, (int64_t)kA8CtasPerSm * num_sms);
   const size_t smem = p.num_seqs <= kA8SmemSeqs ? (size_t)(2 * p.num_seqs + 1) * 4 : 0;
   const auto kernel = head_dim == 128 ? (many ? kv8_append_kernel<128, true> : kv8_append_kernel<128, false>)
                                       : (many ? kv8_append_kernel<64, true> : kv8_append_kernel<64, false>);
