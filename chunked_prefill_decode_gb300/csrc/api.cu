@@ -950,10 +950,11 @@ hb_status hb::internal_plan(const hb_batch* batch, const int32_t* h_q_len,
       // them all: blocks of fewer kv heads spread that over more CTAs (and
       // the consumer warps share a head instead, decode8_body.cuh).  Narrow
       // boxes stream slower, so the blocks are halved only while the rows'
-      // blocks are fewer than a quarter of the CTAs.  GB300, kernel time with
-      // full blocks / this rule / blocks up to the CTAs: 1 row of 16384 tokens
-      // 54 / 26 / 26 us, 4 of 8192 32 / 29 / 29, 32 of about 7300 115 / 109 /
-      // 131, 64 of about 2100 68 / 68 / 70.
+      // blocks are fewer than a quarter of the CTAs.  GB300, device time with
+      // the blocks halved up to half / a quarter / an eighth of them: 20 rows
+      // of 100 to 900 tokens 10.0 / 11.3 / 12.5 us, 30 of 50 to 4000 (4 heads)
+      // 29.7 / 15.6 / 16.5, 16 of 2048 to 8192 41.0 / 37.2 / 38.1, 24 of 4000
+      // to 16000 91 / 94 / 95.
       while (kvhb % 2 == 0 && n_dec_rows * n_blocks * 4 < decode_ctas) {
         kvhb /= 2;
         n_blocks *= 2;
@@ -966,7 +967,20 @@ hb_status hb::internal_plan(const hb_batch* batch, const int32_t* h_q_len,
     ps.cta_off.resize(max_intervals + 1);
     ps.cta_off[0] = 0;
     DecodePartition part;
-    if (!partition_decode(S, h_q_len, h_context_len, n_blocks, kvhb, std::max(1, decode_ctas), 4,
+    // Few rows are cut each by itself.  GB300, device time of the equal shares /
+    // of this: 5 rows of 16 to 512 tokens 14.1 / 5.5 us, 20 of 100 to 900 16.0 /
+    // 11.3, 1 of 16384 16.4 / 12.6, 4 of 8192 20.1 / 16.0, 40 of 100 to 3000
+    // 32.9 / 31.0, 16 of 2048 to 8192 38.3 / 37.3.  A row within four stages
+    // of a piece is not cut (two: 40 rows 33.1; eight: 3 rows of 500 to 2500
+    // 10.2 -> 13.0).  (A stage holds kv8_stage pages, decode8_body.cuh.)
+    constexpr int kRowStages = 4;
+    const int kv8_stage = std::max(1, 8 / kvhb) * (256 / D);
+    const bool by_rows =
+        kv8 && partition_decode_rows(S, h_q_len, h_context_len, n_blocks, kvhb, std::max(1, decode_ctas),
+                                     kv8_stage, kRowStages * kv8_stage, ps.dec.data(),
+                                     ps.cta_off.data(), &part, W);
+    if (!by_rows &&
+        !partition_decode(S, h_q_len, h_context_len, n_blocks, kvhb, std::max(1, decode_ctas), 4,
                           ps.dec.data(), (int)ps.dec.size(), ps.cta_off.data(), max_intervals,
                           &part, W, /*dynamic_tail=*/false))
       return fail(HB_ERR_WORKSPACE, "decode partition overflow");

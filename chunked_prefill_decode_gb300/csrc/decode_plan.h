@@ -136,4 +136,77 @@ inline bool partition_decode(int S, const int32_t* q_len, const int32_t* ctx, in
   return true;
 }
 
+// The other way, for few rows: each row (and kv-head block) is cut by itself
+// into equal pieces, a CTA each, so that no CTA has the ends of two rows to
+// finish, and a short row is not cut at all.  The piece length is the smallest
+// that needs no more than `ctas` CTAs, not below `min_pages`; no row is cut
+// if the longest one is within `row_pages` of that (a cut row's pieces
+// meet through memory, which takes about as long as streaming so many pages).
+// Not taken (false, nothing written) if the rows are more than the CTAs or
+// the longest piece is over `row_pages` above the equal share of a CTA.
+inline bool partition_decode_rows(int S, const int32_t* q_len, const int32_t* ctx, int n_blocks,
+                                  int kvhb, int ctas, int min_pages, int row_pages, DecodeItem* items,
+                                  int32_t* offsets, DecodePartition* out, int window) {
+  int64_t total = 0, rows = 0;
+  int longest = 0;
+  const auto pages_of = [&](int i) {
+    return (ctx[i] + kPageSize - 1) / kPageSize - decode_first_page(ctx[i], window);
+  };
+  for (int i = 0; i < S; ++i)
+    if (q_len[i] == 1) {
+      longest = std::max(longest, pages_of(i));
+      total += (int64_t)pages_of(i) * n_blocks;
+      ++rows;
+    }
+  if (rows == 0 || rows * n_blocks > ctas) return false;
+  int lo = std::min(min_pages, longest), hi = longest;
+  while (lo < hi) {
+    const int mid = lo + (hi - lo) / 2;
+    int64_t pieces = 0;
+    for (int i = 0; i < S; ++i)
+      if (q_len[i] == 1) pieces += (int64_t)((pages_of(i) + mid - 1) / mid) * n_blocks;
+    if (pieces <= ctas) hi = mid; else lo = mid + 1;
+  }
+  const int len = longest - lo <= row_pages ? longest : lo;
+  if (len - (total + ctas - 1) / ctas > row_pages) return false;
+  DecodePartition r;
+  int32_t tok = 0;
+  int k = 0;
+  for (int i = 0; i < S; ++i) {
+    const int32_t this_tok = tok;
+    tok += q_len[i];
+    if (q_len[i] != 1) continue;
+    const int first = decode_first_page(ctx[i], window), np = pages_of(i);
+    const int pieces = (np + len - 1) / len;
+    for (int blk = 0; blk < n_blocks; ++blk) {
+      const int slot = pieces > 1 ? r.n_slots : 0, merge_id = pieces > 1 ? r.n_merge : 0;
+      if (pieces > 1) {
+        r.n_slots += pieces;
+        r.n_merge += 1;
+      }
+      for (int c = 0; c < pieces; ++c) {
+        DecodeItem it{};
+        it.seq = i;
+        it.kvh0 = blk * kvhb;
+        it.page_begin = first + (int32_t)((int64_t)np * c / pieces);
+        it.page_end = first + (int32_t)((int64_t)np * (c + 1) / pieces);
+        it.split = c;
+        it.n_splits = pieces;
+        it.slot = slot;
+        it.merge_id = merge_id;
+        it.ctx = ctx[i];
+        it.tok = this_tok;
+        items[k] = it;
+        offsets[k] = k;
+        ++k;
+      }
+    }
+  }
+  offsets[k] = k;
+  r.n_items = r.grid = k;
+  r.pages_per_cta = len;
+  *out = r;
+  return true;
+}
+
 }  // namespace hb

@@ -239,3 +239,62 @@ def test_a_ring_state_that_overlaps_the_other_is_refused():
     for d in (-24, -8, 8, 24):
         assert L.hb_pages_assign(*assign_args(state_out=FAKE + d)) == 1
         assert L.hb_pages_release(2, 4, 16, 16, FAKE, FAKE, FAKE, FAKE, FAKE + d, None) == 1
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_the_decode_rows_of_a_plan_are_covered_once(seed):
+    """Every page of a row and head in one item, the pieces of a row numbered,
+    their slots and counters their own, no more CTAs than SMs."""
+    hb = lib()
+    rng = np.random.default_rng(900 + seed)
+    hq, hkv, d = [(8, 8, 64), (32, 8, 128), (56, 8, 128), (16, 2, 64), (16, 1, 128), (12, 6, 128), (64, 16, 128)][seed % 7]
+    window = int(rng.choice([0, 0, 40, 1000]))
+    sms = int(rng.choice([1, 7, 152]))
+    n = int(rng.choice([1, 2, 5, 17, 40, 200]))
+    rows = [(1, int(2 ** rng.uniform(0, 13))) for _ in range(n)] + [(int(rng.integers(2, 200)), 300)] * int(rng.integers(0, 2))
+    rng.shuffle(rows)
+    b, ql, cl = host_batch(hb, [tuple(int(x) for x in r) for r in rows], hq=hq, hkv=hkv, d=d, window=window)
+    plan, _ = hb.hb_kv8_plan(b, ql, cl, sms, upload=False)
+    h = hb.plan_header(plan)
+    dec, _, offs = hb.plan_items(plan)
+    kvhb, grid = h["decode_kvh_block"], h["decode_grid"]
+    assert hkv % kvhb == 0 and 1 <= grid <= sms and h["num_decode_dynamic"] == 0
+    assert offs[0] == 0 and offs[-1] == len(dec) and (np.diff(offs) >= 1).all()
+    cu = np.concatenate([[0], np.cumsum(ql)])
+    got = {}
+    for seq, kvh0, pb, pe, split, ns, slot, mid, ctx, tok, _, _ in dec:
+        assert ql[seq] == 1 and ctx == cl[seq] and tok == cu[seq] and kvh0 % kvhb == 0 and 0 <= kvh0 < hkv
+        got.setdefault((seq, kvh0), []).append((pb, pe, split, ns, slot, mid))
+    assert len(got) == int((ql == 1).sum()) * (hkv // kvhb)
+    slots, mids = set(), set()
+    for (seq, _), items in got.items():
+        items.sort()
+        first = (cl[seq] - window) // 16 if 0 < window < cl[seq] else 0
+        assert items[0][0] == first and items[-1][1] == -(-cl[seq] // 16)
+        assert all(a[1] == c[0] for a, c in zip(items, items[1:])) and all(a[0] < a[1] for a in items)
+        assert [a[2] for a in items] == list(range(len(items))) and all(a[3] == len(items) for a in items)
+        if len(items) > 1:
+            assert len({a[4:] for a in items}) == 1
+            mine = set(range(items[0][4], items[0][4] + len(items)))
+            assert not mine & slots and items[0][5] not in mids
+            slots |= mine
+            mids.add(items[0][5])
+    assert len(slots) == h["num_partial_slots"] and len(mids) == h["num_merge_counters"]
+    assert not slots or max(slots) == len(slots) - 1
+
+
+@pytest.mark.parametrize("geom,ctxs,pieces", [
+    ((8, 8, 64), [16, 100, 300, 512, 40], [1, 1, 1, 1, 1]),        # short rows are not cut
+    ((32, 8, 128), [16384], [19]),                                 # 8 blocks of one head on 152 CTAs
+    ((32, 8, 128), [2000, 2000, 100], [8, 8, 1])])                 # 125 pages in stages of 16
+def test_few_decode_rows_are_cut_each_by_itself(geom, ctxs, pieces):
+    hb = lib()
+    b, ql, cl = host_batch(hb, [(1, c) for c in ctxs], hq=geom[0], hkv=geom[1], d=geom[2])
+    plan, _ = hb.hb_kv8_plan(b, ql, cl, 152, upload=False)
+    dec, _, offs = hb.plan_items(plan)
+    assert (np.diff(offs) == 1).all()
+    for s, n in enumerate(pieces):
+        mine = [d for d in dec if d[0] == s and d[1] == 0]
+        assert [d[5] for d in mine] == [n] * n
+        lens = [d[3] - d[2] for d in mine]
+        assert max(lens) - min(lens) <= 1
