@@ -496,3 +496,19 @@ def test_append_with_tokens_of_no_sequence(rows):
     hb.hb_kv8_append(db.batch, *new, *cache)
     hb.hb_check()
     check_append(layout, inp, cache)
+
+
+def test_a_plan_that_is_read_only():
+    hb = lib()
+    layout = layout_from_rows(Shape(8, 8, 64), [(1, 40), (20, 60)], 63)
+    inp = Inputs(layout, 64)
+    cache = inp.oracle_append(layout)
+    inp.cache, inp.exps = list(cache[:2]), list(cache[2:])
+    db = from_layout(layout, "cuda:0")
+    plan, ws = hb.hb_kv8_plan(db.batch, db.q_len, db.context_len, sms())
+    plan.flags.writeable = False
+    ref, tol = bounds(layout, inp, cache)
+    out = torch.full_like(inp.q, float("nan"), device="cuda")
+    hb.hb_kv8_attention(db.batch, plan, inp.q.cuda(), *inp.device(), 1.0 / math.sqrt(64), out, ws)
+    hb.hb_check()
+    check_out(out, ref, tol)
