@@ -25,7 +25,8 @@
 //
 // Layout of the work, and why:
 //  * the host plan gives each CTA an equal contiguous range of the decode
-//    rows' pages (decode_plan.h), cut into items at row boundaries;
+//    rows' pages, cut into items at row boundaries, or, where rows are few, a
+//    piece of one row (decode_plan.h);
 //  * a stage of the ring is as many pages as make sixteen (kv head, page)
 //    pairs, K and V, at D 128 and 32 at D 64: two (four) pages of 8 heads, or
 //    16 (32) pages of one head, so a warp has the same work per stage whatever
