@@ -47,7 +47,10 @@ namespace hb {
 namespace {
 
 constexpr int kA8Threads = 256;
-constexpr int kA8CtasPerSm = 2;     // 128 registers a thread: two pieces' rows of 32
+// CTAs per SM of the form for large batches: K's and V's rows of a page take 64
+// registers a thread at D 128, 32 at D 64 (16 x 2021 tokens of 8 heads: 20.3
+// us, with three CTAs 20.8, with two 23.6).
+constexpr int a8_ctas_per_sm(int head_dim) { return head_dim == 128 ? 2 : 4; }
 constexpr int kA8Warps = kA8Threads / 32;
 constexpr int kA8SmemSeqs = 6143;   // cu_q_len and context_len in shared memory up to here (48 KB)
 
@@ -249,7 +252,7 @@ __device__ __forceinline__ void finish_rows(const Append8Params& p, const Place&
 // it finishes those at hand; else K or V, one per warp, in more and smaller
 // warps.
 template <int D, bool kMany>
-__global__ void __launch_bounds__(kA8Threads, kMany ? kA8CtasPerSm : 4)
+__global__ void __launch_bounds__(kA8Threads, kMany ? a8_ctas_per_sm(D) : 4)
     kv8_append_kernel(const Append8Params p) {
   extern __shared__ int32_t s_cu[];
   griddep_wait();
@@ -305,7 +308,7 @@ cudaError_t launch_kv8_append(Append8Params p, int head_dim, int num_sms, cudaSt
   p.by_token = kv8_append_by_token(p.total_q, p.num_seqs);
   int64_t blocks = (pieces + kA8Warps - 1) / kA8Warps;
   const bool many = blocks > 4 * 2LL * num_sms;
-  if (many) blocks = std::min<int64_t>((blocks + 1) / 2, (int64_t)kA8CtasPerSm * num_sms);
+  if (many) blocks = std::min<int64_t>((blocks + 1) / 2, (int64_t)a8_ctas_per_sm(head_dim) * num_sms);
   const size_t smem = p.num_seqs <= kA8SmemSeqs ? (size_t)(2 * p.num_seqs + 1) * 4 : 0;
   const auto kernel = head_dim == 128 ? (many ? kv8_append_kernel<128, true> : kv8_append_kernel<128, false>)
                                       : (many ? kv8_append_kernel<64, true> : kv8_append_kernel<64, false>);
