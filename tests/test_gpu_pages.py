@@ -278,3 +278,22 @@ def test_state_out_may_hold_anything():
     hb.hb_check()
     assert state.tolist() == [0, pages_, 0, 0]
     assert after.tolist() == [7000, pages_, 0, 0] and back.tolist() == [7000, pages_ + 7000, 0, 0]
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("rows,maxp", [(16384, 3), (15000, 2), (1, 9000), (2, 70000), (455, 300), (457, 300)])
+def test_release_of_many_rows_and_of_wide_ones(rows, maxp, in_place):
+    """More rows in a CTA than a warp has lanes; several CTAs for one row."""
+    hb = lib()
+    rng = np.random.default_rng(rows)
+    lengths = np.where(rng.random(rows) < 0.2, 0, rng.integers(1, maxp * 16 + 1, rows)).astype(np.int32)
+    lengths[0] = maxp * 16
+    n = int((-(-lengths // 16)).sum())
+    ring = Ring(n + 100, head=3 * n, taken=n, seed=rows)
+    table = rng.integers(0, n + 100, (rows, maxp)).astype(np.int32)
+    want, w_tail = pages.release(lengths, ring.order, ring.head, ring.tail, table)
+    out = ring.state if in_place else torch.full((4,), 5, dtype=torch.int64, device="cuda")
+    hb.hb_pages_release(dev(lengths), ring.pages, ring.state, out, dev(table))
+    hb.hb_check()
+    assert np.array_equal(ring.pages.cpu().numpy(), want)
+    assert out.tolist() == [ring.head, w_tail, 0, 0]
