@@ -1471,12 +1471,15 @@ hb_status hb_check(void* stream) {
     if (v == 0) return ok();
     const int zero = 0;
     cudaMemcpy(dev->err, &zero, sizeof(int), cudaMemcpyHostToDevice);
-    if (v & HB_DEVERR_INDEX)
-      return fail(HB_ERR_DEVICE_INDEX, "a kernel met a page index outside [0, num_pages) (word %d)", v);
-    if (v & HB_DEVERR_TIMEOUT) return fail(HB_ERR_TIMEOUT, "a kernel wait gave up (word %d)", v);
+    // (what hb_pages_* found first: the calls after them meet the page indexes
+    // that it left out, and report those too)
+    if (v & HB_DEVERR_LENGTHS)
+      return fail(HB_ERR_SHAPE, "hb_pages_* met lengths or a ring state that break their rules (word %d)", v);
     if (v & HB_DEVERR_PAGES)
       return fail(HB_ERR_OUT_OF_PAGES, "hb_pages_assign found too few free pages (word %d)", v);
-    return fail(HB_ERR_SHAPE, "hb_pages_* met lengths or a ring state that break their rules (word %d)", v);
+    if (v & HB_DEVERR_INDEX)
+      return fail(HB_ERR_DEVICE_INDEX, "a kernel met a page index outside [0, num_pages) (word %d)", v);
+    return fail(HB_ERR_TIMEOUT, "a kernel wait gave up (word %d)", v);
   } catch (...) {
     return fail(HB_ERR_CUDA, "unexpected exception in hb_check");
   }

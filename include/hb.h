@@ -439,8 +439,9 @@ hb_status hb_step(const hb_batch* shape, const int32_t* h_q_len,
 /*
  * Synchronise `stream`, then read and clear the device error word of the
  * current device: HB_OK, HB_ERR_DEVICE_INDEX or HB_ERR_TIMEOUT, after
- * hb_pages_* also HB_ERR_OUT_OF_PAGES or HB_ERR_SHAPE (or HB_ERR_CUDA if the
- * stream itself failed).  Blocking.
+ * hb_pages_* also HB_ERR_OUT_OF_PAGES or HB_ERR_SHAPE, which come before what
+ * later calls reported because of them (or HB_ERR_CUDA if the stream itself
+ * failed).  Blocking.
  */
 hb_status hb_check(void* stream);
 

@@ -1,0 +1,59 @@
+"""After a page assignment that failed, the calls that follow it in the same
+stream: no page of another sequence is written, and the error that hb_check
+gives is the assignment's."""
+import numpy as np
+import pytest
+import torch
+
+from _hbutil import lib
+from test_gpu_pages import Ring, dev
+
+pytestmark = pytest.mark.gpu
+
+HKV, D, PAGES = 2, 64, 16
+
+
+class Caches:
+    """A bf16 and an 8-bit cache that hold known bytes everywhere."""
+
+    def __init__(self, seed):
+        g = torch.Generator("cuda").manual_seed(seed)
+        shape = (PAGES, 16, HKV, D)
+        self.bf16 = [torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2)]
+        self.kv8 = [(torch.randn(shape, generator=g, device="cuda") * 100).to(torch.float8_e4m3fn) for _ in range(2)]
+        self.kv8 += [torch.full((PAGES, HKV), -8, dtype=torch.int8, device="cuda") for _ in range(2)]
+
+    def append(self, batch, total):
+        hb = lib()
+        g = torch.Generator("cuda").manual_seed(total)
+        kn, vn = ((9 * torch.randn(total, HKV, D, generator=g, device="cuda")).to(torch.bfloat16) for _ in range(2))
+        hb.hb_kv_append(batch, kn, vn, *self.bf16)
+        hb.hb_kv8_append(batch, kn, vn, *self.kv8)
+
+    def pages(self):
+        """Each page's bytes, all caches together: [PAGES, n] uint8."""
+        torch.cuda.synchronize()
+        return torch.cat([c.reshape(PAGES, -1).view(torch.uint8) for c in self.bf16 + self.kv8], 1).cpu().numpy()
+
+
+def changed(a, b):
+    return np.flatnonzero((a != b).any(1)).tolist()
+
+
+def stale_table(rows, maxp, live):
+    """Rows of the live sequence's page ids, as finished requests leave them."""
+    return np.resize(np.asarray(live, np.int32), (rows, maxp)).copy()
+
+
+def test_the_assignments_error_comes_before_what_follows_from_it():
+    hb = lib()
+    for q, ctx, status in (([1], [17], 8), ([3], [2], 2)):
+        ring = Ring(PAGES, taken=PAGES)
+        d_table, cu, d_ctx = dev([[-1, -1]]), dev([0, 1]), dev(ctx)
+        hb.hb_pages_assign(dev(q), d_ctx, ring.pages, ring.state, ring.state, d_table, cu)
+        cu, d_ctx = dev([0, 1]), dev([17])
+        Caches(4).append(hb.make_batch(1, 1, 2, PAGES, HKV, HKV, D, cu, d_ctx, d_table), 1)   # reports a page index
+        with pytest.raises(hb.HbError) as e:
+            hb.hb_check()
+        assert e.value.status == status
+        hb.hb_check()
