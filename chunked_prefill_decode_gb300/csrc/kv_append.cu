@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(32 * kAppendMaxWarps, 2) kv_append_kernel(Appe
   const int s = lo;
   const int q0 = cu[s];
   const int q_len = cu[s + 1] - q0;
+  if ((unsigned)(tok - q0) >= (unsigned)max(q_len, 0)) return;   // a token of no sequence
   const int pos = ctx[s] - q_len + (tok - q0);
   const int lp = pos / kPageSize;
   int page = -1;

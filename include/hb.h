@@ -118,7 +118,8 @@ typedef struct hb_batch {
  * KV append (scatter).  For every new token j of sequence s, copy row
  * cu_q_len[s]+j of k_new / v_new ([num_kv_heads*head_dim] contiguous bf16)
  * to its page slot in k_cache / v_cache (see the layout above).  The copy is
- * bit-exact; no other slot is written.  Cited passage: the first page,
+ * bit-exact; no other slot is written, and rows of k_new / v_new outside
+ * every sequence's are written nowhere.  Cited passage: the first page,
  * §GPU / 系统数据路径 ⑤ ("a prefill chunk appends new KV").
  *   k_new, v_new     device, [total_q, Hkv, D] bf16, 16-byte aligned
  *   k_cache, v_cache device, [num_pages, 16, Hkv, D] bf16, 16-byte aligned

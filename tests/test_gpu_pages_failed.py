@@ -57,3 +57,31 @@ def test_the_assignments_error_comes_before_what_follows_from_it():
             hb.hb_check()
         assert e.value.status == status
         hb.hb_check()
+
+
+@pytest.mark.parametrize("rows", [[(1, 20), (1, 33), (1, 16)], [(1, 3 + i % 40) for i in range(300)],
+                                  [(30, 40), (5, 5), (17, 100)]])
+def test_bf16_append_with_tokens_of_no_sequence(rows):
+    """New rows before the first sequence's and behind the last one's are
+    written nowhere, as by hb_kv8_append."""
+    from _gpu import bits
+    from chunked_prefill_decode_gb300 import workloads
+    from chunked_prefill_decode_gb300.device import from_layout
+    from oracle import paged_attention as pa
+    hb = lib()
+    layout = workloads.layout_from_rows(workloads.Shape(4, 4, 64), rows, 61)
+    g = torch.Generator().manual_seed(62)
+    first, behind, T = 20, 9, layout.total_q
+    kc, vc = (torch.randn(layout.num_pages, 16, 4, 64, generator=g).to(torch.bfloat16) for _ in range(2))
+    kn, vn = (torch.randn(first + T + behind, 4, 64, generator=g).to(torch.bfloat16) for _ in range(2))
+    db = from_layout(layout, "cuda:0")
+    # the rows may still grow: their tables name pages past the context too
+    db.block_table.copy_(torch.where(db.block_table < 0, 0, db.block_table))
+    db.cu_q_len.add_(first)
+    db.batch.total_q = first + T + behind
+    dk, dv = kc.cuda(), vc.cuda()
+    hb.hb_kv_append(db.batch, kn.cuda(), vn.cuda(), dk, dv)
+    hb.hb_check()
+    wk, wv = pa.kv_append(bits(kc), bits(vc), bits(kn[first:first + T]), bits(vn[first:first + T]), layout.q_len,
+                          layout.context_len, layout.block_table, 16)
+    assert np.array_equal(bits(dk.cpu()), wk) and np.array_equal(bits(dv.cpu()), wv)
