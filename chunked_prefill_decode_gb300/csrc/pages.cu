@@ -204,7 +204,20 @@ __global__ void __launch_bounds__(kPagesThreads) pages_assign_kernel(const Pages
   for (int64_t s = first_thread; s <= S; s += step) p.cu_q_len[s] = S > 0 ? a.s_q[s] : 0;
   if (S == 0) return;
   const int32_t* cu = a.s_q;
-  if (err) {   // too few pages: no table entry changes, and no token has a slot
+  // the entry of the k-th page to take
+  auto entry = [&](int64_t k) -> int32_t* {
+    const int s = owner(a.s_pg, S, (int)k);
+    const int lp = (a.s_off[s] + kPageSize - 1) / kPageSize + (int)k - a.s_pg[s];
+    return p.block_table + (size_t)s * p.max_pages_per_seq + lp;
+  };
+  if (err) {
+    // too few pages: no token has a slot, and no entry that was to be filled
+    // may name a page -- what a finished request left there can be another
+    // sequence's by now, and an append behind this call would write to it
+    for (int64_t k = first_thread; k < a.pages; k += step) {
+      int32_t* at = entry(k);
+      if ((unsigned)__ldcg(at) < (unsigned)p.num_pages) *at = -1;
+    }
     if (p.slot_map)
       for (int64_t t = first_thread; t < a.tokens; t += step) p.slot_map[t] = -1;
     return;
@@ -219,11 +232,9 @@ __global__ void __launch_bounds__(kPagesThreads) pages_assign_kernel(const Pages
   };
   // table entries of the pages taken
   for (int64_t k = first_thread; k < a.pages; k += step) {
-    const int s = owner(a.s_pg, S, (int)k);
-    const int lp = (a.s_off[s] + kPageSize - 1) / kPageSize + (int)k - a.s_pg[s];
     const int page = fresh_page(k);
     if (page < 0) report_error(p.dev_error, HB_DEVERR_INDEX);
-    p.block_table[(size_t)s * p.max_pages_per_seq + lp] = page;
+    *entry(k) = page;
   }
   if (!p.slot_map) return;
   // slots: a warp takes 32 kRun consecutive tokens, 32 at a time so that what

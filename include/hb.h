@@ -320,9 +320,10 @@ hb_status hb_kv8_attention(const hb_batch* batch, const void* h_plan, const void
  * Calls on one ring must be ordered.
  *
  * Lengths are read on the device, so mistakes in them are found there: the
- * call then changes nothing but the error word (state_out = state_in), and
- * hb_check() gives HB_ERR_SHAPE, or HB_ERR_OUT_OF_PAGES where only the free
- * pages were too few.  num_seqs is at most 16384 (HB_ERR_UNSUPPORTED).
+ * call then takes and returns no page (state_out = state_in), and hb_check()
+ * gives HB_ERR_SHAPE, or HB_ERR_OUT_OF_PAGES where only the free pages were
+ * too few; what it leaves for the calls behind it, see below.  num_seqs is at
+ * most 16384 (HB_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------- */
 
 /*
@@ -339,8 +340,13 @@ hb_status hb_kv8_attention(const hb_batch* batch, const void* h_plan, const void
  *                of the t-th new token of the batch; entries behind the last
  *                token stay as they are
  * The sum of q_len must not exceed max_tokens.  With too few free pages
- * cu_q_len is written, block_table and the ring are not, and the tokens'
- * slots are -1.  A ring entry (or, for a token on an older page, a table
+ * cu_q_len is written and the ring is not, the tokens' slots are -1, and the
+ * entries that were to receive pages name none: one in [0, num_pages) becomes
+ * -1, the others stay.  An append behind the call then writes no page but
+ * those that the rows hold already, there past their earlier tokens (it
+ * reports the others, and the 8-bit scale of such a page may grow); the same
+ * call again, with pages in the ring, fills the table as if it had been the
+ * first.  A ring entry (or, for a token on an older page, a table
  * entry) outside [0, num_pages) becomes -1 and is reported by hb_check() as
  * HB_ERR_DEVICE_INDEX.
  */

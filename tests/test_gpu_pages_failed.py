@@ -45,6 +45,64 @@ def stale_table(rows, maxp, live):
     return np.resize(np.asarray(live, np.int32), (rows, maxp)).copy()
 
 
+@pytest.mark.parametrize("free", [0, 1, 2])
+def test_too_few_pages_and_an_append_behind_it(free):
+    """Row 0 stands still on pages 0 and 1; row 1 is new, row 2 goes on to its
+    next page, and the entries that they would fill still name row 0's pages."""
+    hb = lib()
+    ring = Ring(PAGES, head=5, taken=PAGES - free)
+    table = stale_table(3, 4, [0, 1])
+    table[0, :2], table[2, 0] = [0, 1], 7
+    q, ctx = [0, 40, 1], [32, 40, 17]
+    d_table, cu, d_ctx = dev(table), dev([0, 0, 1, 2]), dev(ctx)
+    slots = torch.zeros(41, dtype=torch.int64, device="cuda")
+    hb.hb_pages_assign(dev(q), d_ctx, ring.pages, ring.state, ring.state, d_table, cu, slots)
+    caches = Caches(1)
+    before = caches.pages()
+    batch = hb.make_batch(3, 41, 4, PAGES, HKV, HKV, D, cu, d_ctx, d_table)
+    caches.append(batch, 41)
+    assert changed(before, caches.pages()) == []
+    with pytest.raises(hb.HbError):
+        hb.hb_check()
+    hb.hb_check()
+    # rows that ask for no page keep theirs, and no entry to be opened names a page
+    got = d_table.cpu().numpy()
+    assert got[0].tolist() == table[0].tolist() and got[2, 0] == 7
+    assert not ((got[1, :3] >= 0) & (got[1, :3] < PAGES)).any() and not 0 <= got[2, 1] < PAGES
+    assert got[1, 3] == table[1, 3] and got[2, 2:].tolist() == table[2, 2:].tolist()
+    assert ring.state.tolist() == [5, 5 + free, 0, 0] and (slots == -1).all()
+    # with pages back in the ring the same call gives what it would have given
+    hb.hb_pages_release(dev([64]), ring.pages, ring.state, ring.state, dev([[9, 10, 11, 12]]))
+    want = [int(x) for x in torch.roll(ring.pages, -5).tolist()[:4]]
+    hb.hb_pages_assign(dev(q), d_ctx, ring.pages, ring.state, ring.state, d_table, cu, slots)
+    hb.hb_check()
+    got = d_table.cpu().numpy()
+    assert got[1, :3].tolist() == want[:3] and got[2].tolist() == [7, want[3], table[2, 2], table[2, 3]]
+
+
+def test_too_few_pages_for_many_rows():
+    """More pages to open than a CTA has threads; only entries that name a page
+    are cleared."""
+    hb = lib()
+    n, maxp = 900, 5
+    ring = Ring(3000, head=1, taken=1000)
+    rng = np.random.default_rng(2)
+    q = rng.integers(0, 80, n)
+    ctx = q + rng.integers(0, 80 - q + 1)
+    table = rng.integers(-5, 3010, (n, maxp)).astype(np.int32)
+    d_table, cu = dev(table), dev(np.zeros(n + 1))
+    hb.hb_pages_assign(dev(q), dev(ctx), ring.pages, ring.state, ring.state, d_table, cu)
+    with pytest.raises(hb.HbError) as e:
+        hb.hb_check()
+    assert e.value.status == 8
+    lp = np.arange(maxp)[None, :]
+    opened = (lp >= -(-(ctx - q) // 16)[:, None]) & (lp < -(-ctx // 16)[:, None])
+    assert opened.sum() > 2000
+    want = np.where(opened & (table >= 0) & (table < 3000), -1, table)
+    assert np.array_equal(d_table.cpu().numpy(), want)
+    assert cu.cpu().tolist() == [0] + np.cumsum(q).tolist()
+
+
 def test_the_assignments_error_comes_before_what_follows_from_it():
     hb = lib()
     for q, ctx, status in (([1], [17], 8), ([3], [2], 2)):
