@@ -195,11 +195,21 @@ __global__ void __launch_bounds__(kPagesThreads) pages_assign_kernel(const Pages
   if (!err && a.pages > tail - head) err = HB_DEVERR_PAGES;
   if (threadIdx.x == 0) write_state(p, s_state, err ? 0 : a.pages, 0);
   if (err && blockIdx.x == 0 && threadIdx.x == 0) report_error(p.dev_error, err);
-  if (!lengths_ok) return;
 
   const int lane = threadIdx.x & 31;
   const int64_t first_thread = (int64_t)blockIdx.x * kPagesThreads + threadIdx.x;
   const int64_t step = (int64_t)gridDim.x * kPagesThreads;
+  if (!lengths_ok) {
+    // a batch without tokens: the sums and slots of the step before, with this
+    // step's lengths, would send an append behind this call to other places
+    // (entry 0 is only read, so the CTAs need not agree on when)
+    const int c0 = __ldcg(p.cu_q_len);
+    for (int64_t s = first_thread + 1; s <= S; s += step) p.cu_q_len[s] = c0;
+    if (p.slot_map)
+      for (int64_t t = first_thread; t < p.max_tokens; t += step)
+        if (__ldcg(p.slot_map + t) >= 0) p.slot_map[t] = -1;
+    return;
+  }
   const int64_t first_warp = first_thread >> 5, warps = step / 32;
   for (int64_t s = first_thread; s <= S; s += step) p.cu_q_len[s] = S > 0 ? a.s_q[s] : 0;
   if (S == 0) return;

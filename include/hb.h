@@ -339,16 +339,19 @@ hb_status hb_kv8_attention(const hb_batch* batch, const void* h_plan, const void
  *   slot_map     [max_tokens] int64 or NULL: entry t receives page * 16 + slot
  *                of the t-th new token of the batch; entries behind the last
  *                token stay as they are
- * The sum of q_len must not exceed max_tokens.  With too few free pages
- * cu_q_len is written and the ring is not, the tokens' slots are -1, and the
- * entries that were to receive pages name none: one in [0, num_pages) becomes
- * -1, the others stay.  An append behind the call then writes no page but
- * those that the rows hold already, there past their earlier tokens (it
- * reports the others, and the 8-bit scale of such a page may grow); the same
- * call again, with pages in the ring, fills the table as if it had been the
- * first.  A ring entry (or, for a token on an older page, a table
- * entry) outside [0, num_pages) becomes -1 and is reported by hb_check() as
- * HB_ERR_DEVICE_INDEX.
+ * The sum of q_len must not exceed max_tokens.  A ring entry (or, for a token
+ * on an older page, a table entry) outside [0, num_pages) becomes -1 and is
+ * reported by hb_check() as HB_ERR_DEVICE_INDEX.
+ * Behind a call that failed, calls already queued stay safe to run:
+ *   - HB_ERR_SHAPE: no row has tokens by cu_q_len (all its entries equal the
+ *     first, which stays) and no entry of slot_map is a slot (those >= 0 become
+ *     -1), so an append writes nothing;
+ *   - HB_ERR_OUT_OF_PAGES: cu_q_len is written, the tokens' slots are -1, and
+ *     the table entries that were to receive pages name none (one in
+ *     [0, num_pages) becomes -1, the others stay).  An append writes only to
+ *     pages that the rows hold already, past their earlier tokens (there the
+ *     8-bit scale may grow), and reports the others.  The same call again,
+ *     with pages in the ring, fills the table as if it had been the first.
  */
 hb_status hb_pages_assign(int32_t num_seqs, int32_t max_tokens, int32_t max_pages_per_seq,
                           int32_t num_pages, int32_t page_size, const int32_t* q_len,

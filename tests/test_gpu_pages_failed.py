@@ -103,6 +103,27 @@ def test_too_few_pages_for_many_rows():
     assert cu.cpu().tolist() == [0] + np.cumsum(q).tolist()
 
 
+@pytest.mark.parametrize("q,ctx", [([1, 3], [17, 2]), ([17, -1], [33, 5]), ([1, 1], [17, 65])])
+def test_bad_lengths_and_an_append_behind_it(q, ctx):
+    """The step before had one token per row; the entries beyond name another
+    sequence's pages: nothing is written anywhere."""
+    hb = lib()
+    ring = Ring(PAGES)
+    d_table, cu, d_ctx = dev(stale_table(2, 4, [3, 4, 5])), dev([0, 1, 2]), dev(ctx)
+    slots = dev([48, 0, -9, 7], torch.int64)
+    hb.hb_pages_assign(dev(q), d_ctx, ring.pages, ring.state, ring.state, d_table, cu, slots)
+    caches = Caches(3)
+    before = caches.pages()
+    caches.append(hb.make_batch(2, 2, 4, PAGES, HKV, HKV, D, cu, d_ctx, d_table), 2)
+    assert changed(before, caches.pages()) == []
+    with pytest.raises(hb.HbError) as e:
+        hb.hb_check()
+    assert e.value.status == 2
+    assert len(set(cu.tolist())) == 1          # a batch without tokens
+    assert slots.tolist() == [-1, -1, -9, -1]
+    assert np.array_equal(d_table.cpu().numpy(), stale_table(2, 4, [3, 4, 5]))
+
+
 def test_the_assignments_error_comes_before_what_follows_from_it():
     hb = lib()
     for q, ctx, status in (([1], [17], 8), ([3], [2], 2)):
