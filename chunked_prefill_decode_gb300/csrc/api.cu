@@ -654,10 +654,11 @@ hb_status hb::internal_plan(const hb_batch* batch, const int32_t* h_q_len,
     const int W = batch->sliding_window;
     const int64_t max_ctx = (int64_t)batch->max_pages_per_seq * kPageSize;
     int64_t tq = 0;
+    const int min_q = kv8 ? 0 : 1;   // 0: a row that stands still (hb_pages_assign), no work below
     for (int i = 0; i < S; ++i) {
-      if (h_q_len[i] < 1 || h_q_len[i] > h_context_len[i])
-        return fail(HB_ERR_SHAPE, "row %d: q_len %d, context_len %d (need 1 <= q_len <= context_len)",
-                    i, h_q_len[i], h_context_len[i]);
+      if (h_q_len[i] < min_q || h_q_len[i] > h_context_len[i])
+        return fail(HB_ERR_SHAPE, "row %d: q_len %d, context_len %d (need %d <= q_len <= context_len)",
+                    i, h_q_len[i], h_context_len[i], min_q);
       if (h_context_len[i] > max_ctx)
         return fail(HB_ERR_SHAPE, "row %d: context_len %d exceeds max_pages_per_seq * 16", i,
                     h_context_len[i]);
@@ -994,7 +995,7 @@ hb_status hb::internal_plan(const hb_batch* batch, const int32_t* h_q_len,
     int64_t widen_pages = 0;
     if (kv8) {
       for (int i = 0; i < S; ++i) {
-        if (h_q_len[i] == 1) continue;   // decode rows read the 8-bit pages
+        if (h_q_len[i] <= 1) continue;   // decode rows read the 8-bit pages
         const int first = W > 0 ? std::max(0, h_context_len[i] - h_q_len[i] - W + 1) / kPageSize : 0;
         ps.widen.push_back(WidenItem{i, first, (int32_t)widen_pages, 0});
         widen_pages += (h_context_len[i] + kPageSize - 1) / kPageSize - first;

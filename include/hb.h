@@ -56,7 +56,9 @@
  *    absolute position).  Query head h reads kv head h / (Hq/Hkv).
  *
  * Supported shapes: page_size 16, head_dim 64 or 128, Hq a multiple of Hkv
- * with group size Hq/Hkv <= 16, 1 <= q_len <= context_len per sequence.
+ * with group size Hq/Hkv <= 16, 1 <= q_len <= context_len per sequence (in the
+ * 8-bit cache's calls and hb_pages_assign also q_len 0, a row that stands
+ * still).
  */
 #ifndef HB_H_
 #define HB_H_
@@ -281,8 +283,9 @@ hb_status hb_kv8_append(const hb_batch* batch, const void* k_new, const void* v_
                         void* k_cache, void* v_cache, int8_t* k_exp, int8_t* v_exp,
                         void* stream);
 
-/* hb_plan for hb_kv8_attention (same arguments, rules and errors).  A plan
- * serves one of the two: hb_attention refuses this one, hb_kv8_attention
+/* hb_plan for hb_kv8_attention (same arguments, rules and errors, but that a
+ * row may also stand still: q_len 0 with any context_len, no row of q or out).
+ * A plan serves one of the two: hb_attention refuses this one, hb_kv8_attention
  * refuses hb_plan's (HB_ERR_WORKSPACE).  The workspace also holds the chunk
  * rows' pages as bf16 (4 * Hkv * D bytes per visible token of theirs). */
 hb_status hb_kv8_plan(const hb_batch* batch, const int32_t* h_q_len,

@@ -1,0 +1,52 @@
+"""The 8-bit and page calls of the binding on the host (no GPU): arguments that
+are not what they should be, plans that are cut short, rows that stand still."""
+import numpy as np
+import pytest
+import torch
+
+from _hbutil import host_batch, lib
+
+
+def plan_of(hb, rows, **kw):
+    b, ql, cl = host_batch(hb, rows, **kw)
+    plan, _ = hb.hb_kv8_plan(b, ql, cl, 152, upload=False)
+    return plan, hb.hb_plan_sizes(b, ql, cl, 152, kv8=True)
+
+
+@pytest.mark.parametrize("window", [0, 50])
+def test_rows_that_stand_still_cost_nothing(window):
+    """Rows without new tokens (waiting, finished, empty) add no work to a plan:
+    it is the plan without them, at the rows' places."""
+    hb = lib()
+    rows = [(1, 700), (30, 200), (1, 33), (130, 130), (1, 5)]
+    at = [1, 2, 4, 5, 7]
+    still = [(0, 40), None, None, (0, 0), None, None, (0, 900), None, (0, 1)]
+    both = list(still)
+    for i, r in zip(at, rows):
+        both[i] = r
+    a, sizes_a = plan_of(hb, rows, max_pages=60, window=window)
+    b, sizes_b = plan_of(hb, both, max_pages=60, window=window)
+    for x, y, tok in zip(hb.plan_items(a)[:2], hb.plan_items(b)[:2], (9, 5)):
+        want = x.copy()
+        want[:, 0] = np.array(at)[x[:, 0]]
+        assert np.array_equal(y, want)
+    assert np.array_equal(hb.plan_items(a)[2], hb.plan_items(b)[2])
+    assert sizes_a[0] == sizes_b[0]                  # as many items to upload
+
+
+def test_a_step_in_which_every_row_stands_still():
+    hb = lib()
+    plan, _ = plan_of(hb, [(0, 5), (0, 0)])
+    dec, chk, _ = hb.plan_items(plan)
+    assert len(dec) == 0 and len(chk) == 0
+
+
+@pytest.mark.parametrize("row", [(-1, 5), (6, 5), (0, -1), (0, 4000)])
+def test_rows_that_break_the_rules_are_refused(row):
+    hb = lib()
+    b, ql, cl = host_batch(hb, [(1, 5), (1, 5)], max_pages=4)
+    ql[1], cl[1] = row
+    b.total_q = int(ql.sum())
+    with pytest.raises(hb.HbError) as e:
+        hb.hb_plan_sizes(b, ql, cl, 152, kv8=True)
+    assert e.value.status == 2
