@@ -9,17 +9,24 @@
 //
 // The mathematics, for one q head over keys t whose page has the exponents
 // ke, ve (values k, v):
-//     x_t = (q . k_t) scale log2(e) 2^ke + ve        M = max x_t
-//     P_t = 2^(x_t - M)      l = sum P_t 2^-ve       o = sum P_t v_t / l
-// The V scale goes through the exponent, not onto P or v: P_t <= 1 whatever
-// the scales, and a page whose values are tiny next to another's weighs as
-// little in o as it should, so P fits fp16 (11 significant bits, against
-// bf16's 8) for any spread of scales.  P carries a factor 2^7 that cancels in
-// o, which puts fp16's smallest step at 2^-31 of the largest weight.  In l the
-// factor 2^-ve brings such a page back, so P is formed with 2^48 more before
-// it is rounded (256 decodes 349 us with and without it; with exponentials that
-// keep results below 2^-126 instead 352), and merges take their weights from
-// such exponentials: of pages 2^128 apart each weight in l is good to 2^-14.
+//     x_t = (q . k_t) scale log2(e) 2^ke             M = max x_t
+//     P_t = 2^(x_t - M)      l = sum P_t      o = sum P_t 2^ve v_t / l
+// P goes to the products in fp16 (11 significant bits, against bf16's 8), times
+// 2^kDec8PShift and the page's 2^(ve - R).  R is a reference exponent of the
+// warp, o's unit: it stays while the pages' ve lie within kDec8Spread of it
+// (those of one head mostly differ by a bit or two) and else moves to the next
+// page's ve, o being multiplied by 2^(old R - new R), which is exact.  So the
+// scales cost a weight nothing: the largest error of a far key's weight, half
+// of fp16's smallest step, is 2^-32 of the row's largest weight (ve - R = -2).
+// R is held within 2^64 of the largest one before it in the item, so that o
+// stays inside fp32; a page whose V scale lies further below counts as zeros.
+// (With ve inside the maximum, as x_t + ve, a page with a large V scale pushes
+// the other pages' weights out of fp16: one scale 2^24 above the others' made
+// their part of o wrong by up to 150 times what the roundings allow.)
+// GB300, 256 decodes: 351 us while a window of 32 pages lies near R, 355 with
+// V scales anywhere within 2^60; with ve inside the maximum 348.  The check of
+// each page instead of a window's 352, the move of o as a branch between two
+// pages' products 80 against 78.5 on 64 decodes and a 448-token chunk.
 // q is scaled by a power of two per head so that its largest element is near
 // 2^12 and every element keeps its bits in fp16; e4m3 is exact in fp16.
 //
@@ -77,9 +84,10 @@ constexpr int kDec8Producers = 4;     // warps 8-11
 // pages of a stage per consumer warp: 256 head dims' worth
 inline __host__ __device__ constexpr int decode8_pages(int head_dim) { return 256 / head_dim; }
 constexpr int kDec8MaxStages = 14;
-constexpr float kDec8RescaleThreshold = 8.0f;   // log2 units
-constexpr float kDec8PShift = 7.0f;             // P <= 2^(8 + 7) in fp16
-constexpr int kDec8LShift = 48;                 // of P before it is rounded, see above
+constexpr float kDec8RescaleThreshold = 4.0f;   // log2 units
+constexpr int kDec8Spread = 2;                  // of a page's ve about the reference
+constexpr float kDec8PShift = 9.0f;             // P <= 2^(4 + 9 + 2) in fp16
+constexpr int kDec8Drop = 64;                   // the reference falls no further, see above
 constexpr int kDec8Regs = 224;        // per thread, warps 0-7
 constexpr int kDec8LightRegs = 56;    // per thread, warps 8-11
 static_assert(256 * kDec8Regs + 128 * kDec8LightRegs <= 384 * 168,
@@ -167,7 +175,7 @@ __device__ __forceinline__ void merge_rows8(const DecodeParams& p, const DecodeI
           st2 = make_float2(-INFINITY, 0.f);
           if (base + lane < it.n_splits) st2 = __ldcg(&ml[(size_t)(it.slot + base + lane) * Hq + hh[h]]);
         }
-        wgt[h] = exp2_approx(st2.x - mmax[h]);   // 0 past the pieces
+        wgt[h] = fast_exp2(st2.x - mmax[h]);   // 0 past the pieces
         lsum[h] += wgt[h] * st2.y;
       }
       const int m = min(32, it.n_splits - base);
@@ -462,6 +470,14 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
         }
 
         int tl = 0;   // this warp's page of the window of 32
+        // o's unit and the largest one so far (alike in the warp)
+        int ref = __shfl_sync(0xffffffffu, e_cur, 0) >> 8, ref_max = ref;
+        // the pages of the window of 32 that begins with page `first` all lie near it
+        const auto near = [&](int first) -> bool {
+          return __all_sync(0xffffffffu, first + lane * parts >= it.page_end ||
+                                             (unsigned)((e_cur >> 8) - ref + kDec8Spread) <= 2u * kDec8Spread);
+        };
+        bool calm = near(it.page_begin + part);
         for (int lp0 = it.page_begin + part; lp0 - part < it.page_end; lp0 += pps) {
           ok = __all_sync(0xffffffffu, mbar_wait(&full[st], ph, abort_flag));
           if (!ok) break;
@@ -495,20 +511,36 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
             // K and V of the pages are in registers: the stage goes back
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
-            float fk[U], fv[U], inv_v[U];
-            int valid[U], lo_valid[U];
+            float fk[U], fv[U];
+            int valid[U], lo_valid[U], ves[U];
+            bool moved = false;   // o's unit does not serve all of these pages
 #pragma unroll
             for (int u = 0; u < U; ++u) {
               const int ex = __shfl_sync(0xffffffffu, e_cur, (tl + u) & 31);
               const int ke = (int)(int8_t)(ex & 0xff), ve = ex >> 8;
               fk[u] = pow2i(ke);
-              fv[u] = (float)ve;
-              inv_v[u] = pow2i(-ve - kDec8LShift);
               const int lp = lp0 + u * parts;
               // (a page past the item's end: the stage holds none, no key is seen)
               valid[u] = lp < it.page_end ? min(kPageSize, it.ctx - lp * kPageSize) : 0;
+              ves[u] = ve;
+              fv[u] = pow2i(ve - ref);
               // with a sliding window the row sees keys ctx - W .. ctx - 1 only
               lo_valid[u] = p.window > 0 ? it.ctx - p.window - lp * kPageSize : 0;
+            }
+            int move[U];          // 2^move times o before the products of a page
+            if (!calm) {          // (rare, and alike in the warp)
+#pragma unroll
+              for (int u = 0; u < U; ++u) {
+                move[u] = 0;
+                if (valid[u] > 0 && (unsigned)(ves[u] - ref + kDec8Spread) > 2u * kDec8Spread) {
+                  const int to = max(ves[u], ref_max - kDec8Drop);
+                  move[u] = ref - to;
+                  moved = true;
+                  ref = to;
+                  ref_max = max(ref_max, to);
+                }
+                fv[u] = pow2i(ves[u] - ref);
+              }
             }
             // independent accumulators, so that the chains of MMAs are short
             constexpr int kQk = NQ * U <= 2 ? 2 : 1;
@@ -565,8 +597,8 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
                     a1 += s[u][x][nq][2 + e];
                   }
                   const float cs = qs[nq][e] * fk[u];
-                  x0[u][nq][e] = r < valid[u] && r >= lo_valid[u] ? fmaf(a0, cs, fv[u]) : -INFINITY;
-                  x1[u][nq][e] = r + 8 < valid[u] && r + 8 >= lo_valid[u] ? fmaf(a1, cs, fv[u]) : -INFINITY;
+                  x0[u][nq][e] = r < valid[u] && r >= lo_valid[u] ? a0 * cs : -INFINITY;
+                  x1[u][nq][e] = r + 8 < valid[u] && r + 8 >= lo_valid[u] ? a1 * cs : -INFINITY;
                   need |= fmaxf(x0[u][nq][e], x1[u][nq][e]) > m_run[nq][e] + kDec8RescaleThreshold;
                 }
               }
@@ -582,7 +614,7 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
                   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                   if (mx > m_run[nq][e] + kDec8RescaleThreshold) {
-                    alpha[nq][e] = exp2_approx(m_run[nq][e] - mx);
+                    alpha[nq][e] = fast_exp2(m_run[nq][e] - mx);
                     m_run[nq][e] = mx;
                   }
                 }
@@ -600,26 +632,24 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
               for (int e = 0; e < 2; ++e) l_part[nq][e] *= alpha[nq][e];
 #pragma unroll
               for (int u = 0; u < U; ++u) {
-                float p0[2], p1[2];   // P 2^kDec8LShift
+                float p0[2], p1[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   // no key seen yet: every x is -inf and so is P's exponent
-                  const float mu =
-                      (m_run[nq][e] == -INFINITY ? 0.f : m_run[nq][e]) - (kDec8PShift + kDec8LShift);
+                  const float mu = (m_run[nq][e] == -INFINITY ? 0.f : m_run[nq][e]) - kDec8PShift;
                   p0[e] = fast_exp2(x0[u][nq][e] - mu);
                   p1[e] = fast_exp2(x1[u][nq][e] - mu);
-                  l_part[nq][e] = fmaf(p0[e] + p1[e], inv_v[u], l_part[nq][e]);
+                  l_part[nq][e] += p0[e] + p1[e];
                 }
-                const uint64_t down = pack_f32x2(pow2i(-kDec8LShift), pow2i(-kDec8LShift));
-                unpack_f32x2(mul_f32x2(pack_f32x2(p0[0], p0[1]), down), p0[0], p0[1]);
-                unpack_f32x2(mul_f32x2(pack_f32x2(p1[0], p1[1]), down), p1[0], p1[1]);
+                const uint64_t f = pack_f32x2(fv[u], fv[u]);
+                unpack_f32x2(mul_f32x2(pack_f32x2(p0[0], p0[1]), f), p0[0], p0[1]);
+                unpack_f32x2(mul_f32x2(pack_f32x2(p1[0], p1[1]), f), p1[0], p1[1]);
                 pb[u][nq][0] = movmatrix_trans(pack_f16x2(p0[0], p0[1]));   // B: keys 2c, 2c + 1 of head r
                 pb[u][nq][1] = movmatrix_trans(pack_f16x2(p1[0], p1[1]));   // keys 8 + 2c ..
               }
             }
             // O^T += V^T P^T
-#pragma unroll
-            for (int u = 0; u < U; ++u)
+            const auto products = [&](int u) {
 #pragma unroll
               for (int jj = 0; jj < D / 16; ++jj) {
                 // bytes (key 0: dims 0, 1; key 1: dims 0, 1) -> (dim 0: keys 0, 1; dim 1: ..)
@@ -630,6 +660,23 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
 #pragma unroll
                 for (int nq = 0; nq < NQ; ++nq) mma_f16_16816(o[jj][nq], va, pb[u][nq][0], pb[u][nq][1]);
               }
+            };
+            if (!moved) {
+#pragma unroll
+              for (int u = 0; u < U; ++u) products(u);
+            } else {
+#pragma unroll
+              for (int u = 0; u < U; ++u) {
+                const float f = pow2i(move[u]);
+#pragma unroll
+                for (int jj = 0; jj < D / 16; ++jj)
+#pragma unroll
+                  for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) o[jj][nq][x] *= f;
+                products(u);
+              }
+            }
           } else {
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
@@ -646,6 +693,7 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
           } else if (tl == 32) {
             tl = 0;
             e_cur = e_next;
+            calm = near(lp0 + pps);
             raw_next = entry(it, (lp0 + pps - it.page_begin - part) / parts + 32);
           }
           if (ahead == 1) {
@@ -660,6 +708,13 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
 
         // ---------------------------------------------------------- the item's end
         const int Hq = p.num_q_heads;
+        const float unit = pow2i(ref);
+#pragma unroll
+        for (int jj = 0; jj < D / 16; ++jj)
+#pragma unroll
+          for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[jj][nq][x] *= unit;
         float l_tot[NQ][2];
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq)
@@ -705,8 +760,8 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
               for (int e = 0; e < 2; ++e) {
                 const float m2 = src[32 * k++], l2 = src[32 * k++];
                 const float mm = fmaxf(m_run[nq][e], m2);
-                wa[nq][e] = m_run[nq][e] == -INFINITY ? 0.f : exp2_approx(m_run[nq][e] - mm);
-                wb[nq][e] = m2 == -INFINITY ? 0.f : exp2_approx(m2 - mm);
+                wa[nq][e] = m_run[nq][e] == -INFINITY ? 0.f : fast_exp2(m_run[nq][e] - mm);
+                wb[nq][e] = m2 == -INFINITY ? 0.f : fast_exp2(m2 - mm);
                 m_run[nq][e] = mm;
                 l_tot[nq][e] = l_tot[nq][e] * wa[nq][e] + l2 * wb[nq][e];
               }

@@ -81,14 +81,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return v;
 }
 
-// 2^x, small results included: weights of pages whose V scales are 2^128
-// apart may differ by as much and still count alike in the sum (decode8_body.cuh).
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // *p += v at device scope, as a release of everything ordered before it and
 // an acquire of what the others released there.
 __device__ __forceinline__ int atom_add_acq_rel(int32_t* p, int v) {

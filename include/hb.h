@@ -294,8 +294,12 @@ hb_status hb_kv8_plan(const hb_batch* batch, const int32_t* h_q_len,
                       void* stream);
 
 /* hb_attention over the 8-bit cache: the same result, of the elements' values,
- * with the same masks, precision and errors; HB_ERR_INVALID_ARG for a
- * softmax_scale that is not positive and finite.  What unwritten slots of a
+ * with the same masks and errors; HB_ERR_INVALID_ARG for a softmax_scale that
+ * is not positive and finite.  Precision as hb_attention's, with two limits in
+ * decode rows: a weight is rounded to 11 bits, but not finer than 2^-32 of the
+ * row's largest weight, so a key below that counts with an error of up to that
+ * part of its V; and of a row's pages (per kv head) those whose V scale is
+ * over 2^64 below the largest may count as zeros.  What unwritten slots of a
  * page hold (NaN included) never shows, nor for a decode row what stands
  * below its window; a NaN stored as a value (V) of a chunk's own token may
  * reach the chunk's earlier rows too, as in hb_attention.  Work: decode rows
