@@ -273,6 +273,9 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
     uint32_t qph[2] = {0u, 0u};
     uint32_t issued_mask = 0, last_par_mask = 0;
     bool dep_done = false;   // griddep_wait done (before the first page with a new token)
+    // (complete already, Decode8Params: what it wrote with plain stores is read
+    // by copies of the async proxy)
+    if (!p8.wait_new) fence_proxy_async_global();
     const uint32_t qbytes = (uint32_t)(kvhb * g * D * 2);
     // lane l: block-table entry of page base + l of item x, checked where used
     auto window = [&](const DecodeItem& x, int base) -> int {

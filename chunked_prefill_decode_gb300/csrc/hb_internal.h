@@ -246,7 +246,11 @@ struct Decode8Params {
   const int8_t* k_exp;    // [num_pages, Hkv]
   const int8_t* v_exp;
   // 1: the launch before this one is the append (the pages with new tokens
-  // and their exponents wait for it); 0: the append is complete already
+  // and their exponents wait for it).  0: the append is complete already,
+  // because the launch between, the widening, lets this one start only from
+  // CTAs whose own wait for it has returned, that is when the append's grid has
+  // ended and its writes are performed; this grid starts after all of them
+  // have, so it has them without a wait (which would be for the widening).
   int32_t wait_new;
 };
 
