@@ -361,12 +361,21 @@ def _refuse(*specs):
             raise ValueError(f"{name} must be a contiguous {dtype} tensor")
         if tuple(t.shape) != tuple(shape):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    for name, t, _, _ in specs:
         if not t.is_cuda:
             raise ValueError(f"{name} must be on a CUDA device")
         if t.device.index != torch.cuda.current_device():
             raise ValueError(f"{name} is on {t.device}, the current device is "
                              f"cuda:{torch.cuda.current_device()}")
     raise ValueError("arguments on different devices")
+
+
+def _numel(t):
+    return t.numel() if isinstance(t, torch.Tensor) else 0
+
+
+def _width(t):
+    return t.shape[1] if isinstance(t, torch.Tensor) and t.dim() == 2 else 0
 
 
 def _current_device():
@@ -434,7 +443,7 @@ def hb_kv8_attention(batch, plan, q, k_cache, v_cache, k_exp, v_exp, scale, out,
     if not isinstance(plan, np.ndarray) or plan.dtype != np.uint8 or plan.nbytes < HEADER_BYTES:
         raise ValueError("plan must be the uint8 array that hb_kv8_plan returned")
     need = _PLAN_WS_TOTAL.unpack_from(plan, _PLAN_WS_TOTAL_AT)[0]
-    have = workspace.numel() if workspace is not None else need
+    have = _numel(workspace) if workspace is not None else need
     if have < need:
         raise ValueError(f"workspace has {have} bytes, the plan needs {need}")
     try:
@@ -487,11 +496,12 @@ def hb_pages_assign(q_len, context_len, free_pages, state_in, state_out, block_t
     """Block-table entries, prefix sums and (if given) slots of a step from its
     lengths on the GPU, with pages taken from the ring free_pages / state_in
     (state_out receives the ring's new state and may be state_in)."""
-    n, pages = q_len.numel(), free_pages.numel()
-    max_pages = block_table.shape[1] if block_table.dim() == 2 else 0
-    slots = slot_map.numel() if slot_map is not None else 0x7fffffff
-    rows, table, state = (n,), (n, max_pages), (4,)
+    state = (4,)
     try:
+        n, pages = q_len.numel(), free_pages.numel()
+        max_pages = block_table.shape[1] if block_table.dim() == 2 else 0
+        slots = slot_map.numel() if slot_map is not None else 0x7fffffff
+        rows, table = (n,), (n, max_pages)
         dev = q_len.get_device()
         ok = (q_len.dtype is _I32 and q_len.shape == rows and q_len.is_contiguous()
               and context_len.dtype is _I32 and context_len.shape == rows and context_len.is_contiguous()
@@ -510,12 +520,14 @@ def hb_pages_assign(q_len, context_len, free_pages, state_in, state_out, block_t
     except AttributeError:
         ok = False
     if not ok:
-        specs = [("q_len", q_len, _I32, rows), ("context_len", context_len, _I32, rows),
-                 ("free_pages", free_pages, _I32, (pages,)), ("state_in", state_in, _I64, state),
-                 ("state_out", state_out, _I64, state), ("block_table", block_table, _I32, table),
+        n = _numel(q_len)
+        specs = [("q_len", q_len, _I32, (n,)), ("context_len", context_len, _I32, (n,)),
+                 ("free_pages", free_pages, _I32, (_numel(free_pages),)),
+                 ("state_in", state_in, _I64, state), ("state_out", state_out, _I64, state),
+                 ("block_table", block_table, _I32, (n, _width(block_table))),
                  ("cu_q_len", cu_q_len, _I32, (n + 1,))]
         if slot_map is not None:
-            specs.append(("slot_map", slot_map, _I64, (slots,)))
+            specs.append(("slot_map", slot_map, _I64, (_numel(slot_map),)))
         _refuse(*specs)
     st = (_lib or load()).hb_pages_assign(
         n, slots, max_pages, pages, page_size, q_len.data_ptr(), context_len.data_ptr(),
@@ -530,10 +542,11 @@ def hb_pages_release(lengths, free_pages, state_in, state_out, block_table, page
                      stream=None):
     """The pages of the sequences with lengths > 0 (tokens in the cache) go back
     to the ring."""
-    n, pages = lengths.numel(), free_pages.numel()
-    max_pages = block_table.shape[1] if block_table.dim() == 2 else 0
-    rows, table, state = (n,), (n, max_pages), (4,)
+    state = (4,)
     try:
+        n, pages = lengths.numel(), free_pages.numel()
+        max_pages = block_table.shape[1] if block_table.dim() == 2 else 0
+        rows, table = (n,), (n, max_pages)
         dev = lengths.get_device()
         ok = (lengths.dtype is _I32 and lengths.shape == rows and lengths.is_contiguous()
               and block_table.dtype is _I32 and block_table.shape == table
@@ -546,9 +559,11 @@ def hb_pages_release(lengths, free_pages, state_in, state_out, block_table, page
     except AttributeError:
         ok = False
     if not ok:
-        _refuse(("lengths", lengths, _I32, rows), ("block_table", block_table, _I32, table),
-                ("free_pages", free_pages, _I32, (pages,)), ("state_in", state_in, _I64, state),
-                ("state_out", state_out, _I64, state))
+        n = _numel(lengths)
+        _refuse(("lengths", lengths, _I32, (n,)),
+                ("block_table", block_table, _I32, (n, _width(block_table))),
+                ("free_pages", free_pages, _I32, (_numel(free_pages),)),
+                ("state_in", state_in, _I64, state), ("state_out", state_out, _I64, state))
     st = (_lib or load()).hb_pages_release(
         n, max_pages, pages, page_size, lengths.data_ptr(), block_table.data_ptr(),
         free_pages.data_ptr(), state_in.data_ptr(), state_out.data_ptr(), _raw_stream(stream, dev))

@@ -7,6 +7,41 @@ import torch
 from _hbutil import host_batch, lib
 
 
+@pytest.mark.parametrize("junk", [[1, 2], np.zeros(2, np.int32), None, 3])
+@pytest.mark.parametrize("at", range(6))
+def test_page_calls_refuse_what_is_no_tensor(at, junk):
+    hb = lib()
+    i32, st, table = torch.zeros(2, dtype=torch.int32), torch.zeros(4, dtype=torch.int64), torch.zeros(2, 3, dtype=torch.int32)
+    args = [i32, i32, i32, st, st, table]
+    names = ["q_len", "context_len", "free_pages", "state_in", "state_out", "block_table"]
+    args[at] = junk
+    with pytest.raises(ValueError, match=names[at]):
+        hb.hb_pages_assign(*args, torch.zeros(3, dtype=torch.int32))
+    if at != 1:
+        with pytest.raises(ValueError, match="lengths" if at == 0 else names[at]):
+            hb.hb_pages_release(args[0], *args[2:])
+
+
+def test_page_calls_refuse_slots_that_are_no_tensor():
+    hb = lib()
+    i32, st, table = torch.zeros(2, dtype=torch.int32), torch.zeros(4, dtype=torch.int64), torch.zeros(2, 3, dtype=torch.int32)
+    for junk in ([1, 2], np.zeros(2, np.int64), torch.zeros(2, dtype=torch.int32), torch.zeros(2, 2, dtype=torch.int64)):
+        with pytest.raises(ValueError, match="slot_map"):
+            hb.hb_pages_assign(i32, i32, i32, st, st, table, torch.zeros(3, dtype=torch.int32), junk)
+
+
+def test_attention_refuses_a_workspace_that_is_no_tensor():
+    hb = lib()
+    b, ql, cl = host_batch(hb, [(1, 40), (5, 9)], num_pages=8)
+    plan, _ = hb.hb_kv8_plan(b, ql, cl, 152, upload=False)
+    q = torch.zeros(6, 32, 128, dtype=torch.bfloat16)
+    k = torch.zeros(8, 16, 8, 128, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    e = torch.zeros(8, 8, dtype=torch.int8)
+    for junk in ([1, 2], np.zeros(1 << 20, np.uint8), 7):
+        with pytest.raises(ValueError, match="workspace"):
+            hb.hb_kv8_attention(b, plan, q, k, k, e, e, 1.0, q, junk)
+
+
 def plan_of(hb, rows, **kw):
     b, ql, cl = host_batch(hb, rows, **kw)
     plan, _ = hb.hb_kv8_plan(b, ql, cl, 152, upload=False)
