@@ -431,8 +431,8 @@ def hb_kv8_plan(batch, q_len, context_len, num_sms, workspace=None, stream=None,
 
 
 _CHAR = ctypes.c_char
-_PLAN_WS_TOTAL = struct.Struct("<Q")     # plan_header()["ws_total"]
-_PLAN_WS_TOTAL_AT = 88 + 8 * 5
+_PLAN_SIZES = struct.Struct("<QQ")       # plan_header()["ws_total"], ["plan_bytes"]
+_PLAN_SIZES_AT = 88 + 8 * 5
 
 
 def hb_kv8_attention(batch, plan, q, k_cache, v_cache, k_exp, v_exp, scale, out, workspace,
@@ -440,9 +440,12 @@ def hb_kv8_attention(batch, plan, q, k_cache, v_cache, k_exp, v_exp, scale, out,
     """hb_attention over the 8-bit cache."""
     pages, hkv, d = batch.num_pages, batch.num_kv_heads, batch.head_dim
     rows, pool, exps = (batch.total_q, batch.num_q_heads, d), (pages, batch.page_size, hkv, d), (pages, hkv)
-    if not isinstance(plan, np.ndarray) or plan.dtype != np.uint8 or plan.nbytes < HEADER_BYTES:
+    if (not isinstance(plan, np.ndarray) or plan.dtype != np.uint8 or plan.nbytes < HEADER_BYTES
+            or not plan.flags.c_contiguous):
         raise ValueError("plan must be the uint8 array that hb_kv8_plan returned")
-    need = _PLAN_WS_TOTAL.unpack_from(plan, _PLAN_WS_TOTAL_AT)[0]
+    need, size = _PLAN_SIZES.unpack_from(plan, _PLAN_SIZES_AT)
+    if plan.nbytes < size:   # (the library reads it at places that the header gives)
+        raise ValueError(f"plan has {plan.nbytes} bytes of the {size} that hb_kv8_plan wrote")
     have = _numel(workspace) if workspace is not None else need
     if have < need:
         raise ValueError(f"workspace has {have} bytes, the plan needs {need}")

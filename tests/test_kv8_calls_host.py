@@ -42,6 +42,25 @@ def test_attention_refuses_a_workspace_that_is_no_tensor():
             hb.hb_kv8_attention(b, plan, q, k, k, e, e, 1.0, q, junk)
 
 
+def test_a_plan_cut_short_or_strided_is_refused():
+    """The library reads the plan at the places that its header gives."""
+    hb = lib()
+    b, ql, cl = host_batch(hb, [(1, 40), (5, 9)], num_pages=8)
+    plan, _ = hb.hb_kv8_plan(b, ql, cl, 152, upload=False)
+    q = torch.zeros(6, 32, 128, dtype=torch.bfloat16)
+    k = torch.zeros(8, 16, 8, 128, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    e = torch.zeros(8, 8, dtype=torch.int8)
+    call = lambda p: hb.hb_kv8_attention(b, p, q, k, k, e, e, 1.0, q, None)  # noqa: E731
+    twice = np.repeat(plan, 2)[::2]
+    assert np.array_equal(twice, plan)
+    for bad in (plan[:-1], plan[:hb.HEADER_BYTES], plan[:hb.HEADER_BYTES - 1], twice, plan.view(np.int8), plan.tobytes(), None):
+        with pytest.raises(ValueError, match="plan"):
+            call(bad)
+    for good in (plan, np.concatenate([plan, np.zeros(100, np.uint8)])):
+        with pytest.raises(ValueError, match="CUDA"):      # (gets as far as the tensors)
+            call(good)
+
+
 def plan_of(hb, rows, **kw):
     b, ql, cl = host_batch(hb, rows, **kw)
     plan, _ = hb.hb_kv8_plan(b, ql, cl, 152, upload=False)
