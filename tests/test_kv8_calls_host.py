@@ -104,3 +104,21 @@ def test_rows_that_break_the_rules_are_refused(row):
     with pytest.raises(hb.HbError) as e:
         hb.hb_plan_sizes(b, ql, cl, 152, kv8=True)
     assert e.value.status == 2
+
+
+def test_a_torch_without_its_private_shortcuts(monkeypatch):
+    """The binding falls back to torch's public calls for the current device and
+    stream."""
+    import importlib.util
+    from chunked_prefill_decode_gb300 import hb
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+
+    class Stream:
+        cuda_stream = 0x77
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: Stream if dev == 3 else None)
+    spec = importlib.util.spec_from_file_location("chunked_prefill_decode_gb300.hb_copy", hb.__file__)
+    copy = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(copy)
+    assert copy._current_device() == 3 and copy._raw_stream(None, 3) == 0x77 and copy._raw_stream(5, 3) == 5
