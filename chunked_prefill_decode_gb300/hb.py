@@ -361,6 +361,8 @@ def _refuse(*specs):
             raise ValueError(f"{name} must be a contiguous {dtype} tensor")
         if tuple(t.shape) != tuple(shape):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if max(t.shape, default=0) > _INT_MAX:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}: over 2^31 - 1")
     for name, t, _, _ in specs:
         if not t.is_cuda:
             raise ValueError(f"{name} must be on a CUDA device")
@@ -372,6 +374,9 @@ def _refuse(*specs):
 
 def _numel(t):
     return t.numel() if isinstance(t, torch.Tensor) else 0
+
+
+_INT_MAX = 0x7fffffff      # sizes go to the library as 32-bit integers
 
 
 def _width(t):
@@ -506,10 +511,11 @@ def hb_pages_assign(q_len, context_len, free_pages, state_in, state_out, block_t
     try:
         n, pages = q_len.numel(), free_pages.numel()
         max_pages = block_table.shape[1] if block_table.dim() == 2 else 0
-        slots = slot_map.numel() if slot_map is not None else 0x7fffffff
+        slots = min(slot_map.numel(), _INT_MAX) if slot_map is not None else _INT_MAX
         rows, table = (n,), (n, max_pages)
         dev = q_len.get_device()
-        ok = (q_len.dtype is _I32 and q_len.shape == rows and q_len.is_contiguous()
+        ok = (pages <= _INT_MAX and max_pages <= _INT_MAX and n <= _INT_MAX
+              and q_len.dtype is _I32 and q_len.shape == rows and q_len.is_contiguous()
               and context_len.dtype is _I32 and context_len.shape == rows and context_len.is_contiguous()
               and free_pages.dtype is _I32 and free_pages.dim() == 1 and free_pages.is_contiguous()
               and state_in.dtype is _I64 and state_in.shape == state and state_in.is_contiguous()
@@ -554,7 +560,8 @@ def hb_pages_release(lengths, free_pages, state_in, state_out, block_table, page
         max_pages = block_table.shape[1] if block_table.dim() == 2 else 0
         rows, table = (n,), (n, max_pages)
         dev = lengths.get_device()
-        ok = (lengths.dtype is _I32 and lengths.shape == rows and lengths.is_contiguous()
+        ok = (pages <= _INT_MAX and max_pages <= _INT_MAX and n <= _INT_MAX
+              and lengths.dtype is _I32 and lengths.shape == rows and lengths.is_contiguous()
               and block_table.dtype is _I32 and block_table.shape == table
               and block_table.is_contiguous()
               and free_pages.dtype is _I32 and free_pages.dim() == 1 and free_pages.is_contiguous()

@@ -30,6 +30,17 @@ def test_page_calls_refuse_slots_that_are_no_tensor():
             hb.hb_pages_assign(i32, i32, i32, st, st, table, torch.zeros(3, dtype=torch.int32), junk)
 
 
+def test_page_calls_refuse_sizes_past_32_bits():
+    """(They go to the library as 32-bit integers: 2^32 + 16 would pass as 16.)"""
+    hb = lib()
+    i32, st, table = torch.zeros(2, dtype=torch.int32), torch.zeros(4, dtype=torch.int64), torch.zeros(2, 3, dtype=torch.int32)
+    ring = torch.empty(2 ** 32 + 16, dtype=torch.int32, device="meta")
+    with pytest.raises(ValueError, match="free_pages.*2\\^31"):
+        hb.hb_pages_assign(i32, i32, ring, st, st, table, torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(ValueError, match="free_pages.*2\\^31"):
+        hb.hb_pages_release(i32, ring, st, st, table)
+
+
 def test_attention_refuses_a_workspace_that_is_no_tensor():
     hb = lib()
     b, ql, cl = host_batch(hb, [(1, 40), (5, 9)], num_pages=8)
