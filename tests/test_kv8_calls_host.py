@@ -133,3 +133,35 @@ def test_a_torch_without_its_private_shortcuts(monkeypatch):
     copy = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(copy)
     assert copy._current_device() == 3 and copy._raw_stream(None, 3) == 0x77 and copy._raw_stream(5, 3) == 5
+
+
+@pytest.mark.parametrize("rows", [[(1, 40), (5, 9)], [(300, 2000), (1, 900), (17, 17)], [(64, 5000)] * 3,
+                                  [(1, 100)] * 40 + [(2016, 8064)]])
+@pytest.mark.parametrize("geom,window", [((32, 8, 128), 0), ((8, 8, 64), 0), ((56, 8, 128), 700)])
+def test_both_caches_plans_cover_the_same_chunk_work(rows, geom, window):
+    """Every (row, kv head, token, key tile) of the chunk rows once in each plan,
+    however the two cut it into items."""
+    hb = lib()
+    b, ql, cl = host_batch(hb, rows, hq=geom[0], hkv=geom[1], d=geom[2], window=window)
+    got = []
+    for plan in (hb.hb_kv8_plan(b, ql, cl, 152, upload=False)[0], hb.hb_plan(b, ql, cl, 152, upload=False)[0]):
+        _, chk, _ = hb.plan_items(plan)
+        cover = {}
+        for seq, kvh, tok0, ntok, end, q0, q_len, ctx, begin, *_ in chk.tolist():
+            assert q_len == ql[seq] and ctx == cl[seq] and q0 == ql[:seq].sum()
+            # (an item's range of key tiles is that of its last token; a token counts those that it sees)
+            for t in range(tok0, tok0 + ntok):
+                last = (ctx - q_len + t) // 128
+                low = max(0, ctx - q_len + t - window + 1) // 128 if window else 0
+                for j in range(max(begin, low), min(end, last + 1)):
+                    key = (seq, kvh, t, j)
+                    assert key not in cover
+                    cover[key] = 1
+        got.append(cover)
+    assert got[0].keys() == got[1].keys()
+    want = 0
+    for q, c in zip(ql, cl):
+        for t in range(q if q > 1 else 0):
+            pos = c - q + t
+            want += pos // 128 - (max(0, pos - window + 1) // 128 if window else 0) + 1
+    assert len(got[0]) == want * geom[1]
