@@ -83,7 +83,9 @@ constexpr int kDec8Consumers = 8;     // warps 0-7
 constexpr int kDec8Producers = 4;     // warps 8-11
 // pages of a stage per consumer warp: 256 head dims' worth
 inline __host__ __device__ constexpr int decode8_pages(int head_dim) { return 256 / head_dim; }
-constexpr int kDec8MaxStages = 14;
+// stages that fit at most: the smallest stage is that of 5 kv heads
+constexpr int kDec8MaxStages = 5;
+static_assert(227 * 1024 / (2 * 5 * kPageSize * 256) == kDec8MaxStages, "ring of the smallest stage");
 constexpr float kDec8RescaleThreshold = 4.0f;   // log2 units
 constexpr int kDec8Spread = 2;                  // of a page's ve about the reference
 constexpr float kDec8PShift = 9.0f;             // P <= 2^(4 + 9 + 2) in fp16

@@ -26,10 +26,11 @@
 // and those that do not open their page for the batch have nothing to do.
 //
 // What bounds it: small batches the chain of loads (lengths, table entry, old
-// exponent), large ones HBM.  Batches of more pieces than fit the GPU at four
-// CTAs per SM take the form where a warp keeps K and V of a page in flight and
-// finds the place of both at once (with a place for each, 661 instructions a
-// piece and half the issue slots).  GB300, device time per call: 68 tokens (8
+// exponent), large ones HBM.  Batches of more than eight CTAs per SM of single
+// pieces (K and V apart; four are resident, so two rounds of them) take the
+// form where a warp keeps K and V of a page in flight and finds the place of
+// both at once (with a place for each, 661 instructions a piece and half the
+// issue slots).  GB300, device time per call: 68 tokens (8
 // heads of 64) 2.6 us; 256 decodes (8 heads of 128) 4.8, with page units 7.2;
 // 16201 tokens from HBM 20.8 (4.8 TB/s), from L2 15.2, with a place for each
 // 23.9 and 20.5, with one piece per warp 39.6 from L2.
@@ -307,7 +308,7 @@ cudaError_t launch_kv8_append(Append8Params p, int head_dim, int num_sms, cudaSt
   p.num_pieces = (uint32_t)pieces;
   p.by_token = kv8_append_by_token(p.total_q, p.num_seqs);
   int64_t blocks = (pieces + kA8Warps - 1) / kA8Warps;
-  const bool many = blocks > 4 * 2LL * num_sms;
+  const bool many = blocks > 8LL * num_sms;   // (see above)
   if (many) blocks = std::min<int64_t>((blocks + 1) / 2, (int64_t)a8_ctas_per_sm(head_dim) * num_sms);
   const size_t smem = p.num_seqs <= kA8SmemSeqs ? (size_t)(2 * p.num_seqs + 1) * 4 : 0;
   const auto kernel = head_dim == 128 ? (many ? kv8_append_kernel<128, true> : kv8_append_kernel<128, false>)
