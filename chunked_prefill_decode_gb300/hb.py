@@ -497,8 +497,8 @@ def pages_ring(num_pages, page_order=None, device="cuda"):
     """A ring with every page free: (free_pages, state) for hb_pages_*."""
     ring = torch.arange(num_pages, dtype=torch.int32) if page_order is None else \
         torch.as_tensor(page_order, dtype=torch.int32)
-    if ring.numel() != num_pages:
-        raise ValueError("page_order must list every page")
+    if ring.dim() != 1 or not torch.equal(ring.sort().values.cpu(), torch.arange(num_pages, dtype=torch.int32)):
+        raise ValueError("page_order must list every page once")
     return ring.to(device), torch.tensor([0, num_pages, 0, 0], dtype=torch.int64, device=device)
 
 

@@ -117,6 +117,16 @@ def test_rows_that_break_the_rules_are_refused(row):
     assert e.value.status == 2
 
 
+def test_a_ring_lists_every_page_once():
+    hb = lib()
+    for bad in ([0, 0, 1, 2], [0, 1, 2, 4], [-1, 0, 1, 2], [0, 1, 2], [0, 1, 2, 3, 3], [[0, 1], [2, 3]]):
+        with pytest.raises(ValueError, match="every page"):
+            hb.pages_ring(4, bad, device="cpu")
+    ring, state = hb.pages_ring(4, [3, 1, 0, 2], device="cpu")
+    assert ring.tolist() == [3, 1, 0, 2] and state.tolist() == [0, 4, 0, 0]
+    assert hb.pages_ring(3, device="cpu")[0].tolist() == [0, 1, 2]
+
+
 def test_a_torch_without_its_private_shortcuts(monkeypatch):
     """The binding falls back to torch's public calls for the current device and
     stream."""
