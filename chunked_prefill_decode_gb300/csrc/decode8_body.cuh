@@ -44,8 +44,8 @@
 //    at D 64), so that as many chains of products, softmax and products run
 //    side by side: a
 //    page alone is a chain of latencies (1390 cycles at D 128, hardly less at
-//    D 64, the same with the conversions left out), and filling a stage costs
-//    the producer about 750 cycles whatever it holds;
+//    D 64), and filling a stage costs the producer about 750 cycles whatever it
+//    holds;
 //  * the products are taken transposed as in decode_body.cuh.  The MMA's k
 //    index may run over the head dims in any order that q shares, so a lane
 //    takes its K operand as 16 contiguous bytes of a key (two LDS.128 per key

@@ -5,8 +5,8 @@
 // "In-flight Batching", §KV Cache 管理的协同优化: fixed-size pages that a block
 // table maps, handed out as a sequence grows and freed when it finishes.  The
 // host builder (builder.cpp) keeps that list on the host; here it is a ring
-// of page ids in device memory, so that a loop whose lengths are known on the
-// GPU (or a captured graph) needs no trip to the host for its tables.
+// of page ids in device memory, so that tables and appends need no trip to the
+// host, in a captured graph either (an attention's plan takes the lengths there).
 //
 // The mathematics is two prefix sums over the sequences: cu[s], the new
 // tokens before s, and pg[s], the new pages before s, where s takes pages

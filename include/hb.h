@@ -286,8 +286,14 @@ hb_status hb_kv8_append(const hb_batch* batch, const void* k_new, const void* v_
 /* hb_plan for hb_kv8_attention (same arguments, rules and errors, but that a
  * row may also stand still: q_len 0 with any context_len, no row of q or out).
  * A plan serves one of the two: hb_attention refuses this one, hb_kv8_attention
- * refuses hb_plan's (HB_ERR_WORKSPACE).  The workspace also holds the chunk
- * rows' pages as bf16 (4 * Hkv * D bytes per visible token of theirs). */
+ * refuses hb_plan's (HB_ERR_WORKSPACE).  The workspace also holds, if there is
+ * a chunk row, the chunk rows' visible pages as bf16 (4 * Hkv * D bytes per
+ * token, however few tokens the chunk has, and once for each row that shows a
+ * shared page) and a block table of num_seqs * max_pages_per_seq entries: 32
+ * rows of 16 tokens at a context of 8016 take 1 GB (8 heads of 128), twice
+ * what their pages take in the cache.  A captured hb_kv8_attention reads the
+ * plan in its workspace when it is replayed, so that workspace takes no other
+ * plan meanwhile. */
 hb_status hb_kv8_plan(const hb_batch* batch, const int32_t* h_q_len,
                       const int32_t* h_context_len, int32_t num_sms, void* h_plan,
                       size_t* plan_bytes, void* d_workspace, size_t* workspace_bytes,
@@ -311,10 +317,13 @@ hb_status hb_kv8_attention(const hb_batch* batch, const void* h_plan, const void
                            void* d_workspace, void* stream);
 
 /* ---------------------------------------------------------------------------
- * Page bookkeeping on the GPU: what hb_builder_* keeps on the host, for loops
- * whose lengths are known on the device.  "In-flight Batching", §KV Cache
- * 管理的协同优化: fixed-size pages handed out as sequences grow and freed when
- * they finish.
+ * Page bookkeeping on the GPU: what hb_builder_* keeps on the host.  Tables,
+ * prefix sums and free pages stay in device memory, where both appends (which
+ * need nothing from the host) can follow in the same stream or graph; the
+ * attention's plan still takes the lengths on the host.  slot_map is for a
+ * caller's own scatter: the appends here go by block_table.  "In-flight
+ * Batching", §KV Cache 管理的协同优化: fixed-size pages handed out as sequences
+ * grow and freed when they finish.
  *
  * The free pages are a ring in device memory: free_pages [num_pages] int32
  * and a state of four int64: state[0] pages taken so far (head), state[1]
