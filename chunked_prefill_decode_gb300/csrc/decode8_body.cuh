@@ -23,10 +23,11 @@
 // (With ve inside the maximum, as x_t + ve, a page with a large V scale pushes
 // the other pages' weights out of fp16: one scale 2^24 above the others' made
 // their part of o wrong by up to 150 times what the roundings allow.)
-// GB300, 256 decodes: 351 us while a window of 32 pages lies near R, 355 with
-// V scales anywhere within 2^60; with ve inside the maximum 348.  The check of
-// each page instead of a window's 352, the move of o as a branch between two
-// pages' products 80 against 78.5 on 64 decodes and a 448-token chunk.
+// GB300: 256 decodes 346 us, with ve inside the maximum 345; 64 decodes and a
+// 448-token chunk 78.8 and 78.6; 4 rows of 8192 16.4 and 16.1.  V scales anywhere
+// within 2^60 cost 1 % more.  A stage's body stands there twice, for windows of
+// 32 pages that lie near R and for others: one body with the branch for a move
+// takes 350 and 12 rows on one kv head 15.3 instead of 14.8.
 // q is scaled by a power of two per head so that its largest element is near
 // 2^12 and every element keeps its bits in fp16; e4m3 is exact in fp16.
 //
@@ -483,195 +484,191 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
                                              (unsigned)((e_cur >> 8) - ref + kDec8Spread) <= 2u * kDec8Spread);
         };
         bool calm = near(it.page_begin + part);
-        for (int lp0 = it.page_begin + part; lp0 - part < it.page_end; lp0 += pps) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&full[st], ph, abort_flag));
-          if (!ok) break;
-          if (active && lp0 < it.page_end) {
-            const uint32_t sbase = smem_u32(stages + st * L.stage_bytes) + (uint32_t)(w * kPageSize * D);
-            // byte address of 16-byte chunk x of key row `row`
-            auto chunk = [&](uint32_t base, int row, int x) -> uint32_t {
-              if constexpr (D == 128) return base + (uint32_t)(row * 128 + ((x ^ (row & 7)) << 4));
-              return base + (uint32_t)(row * 64 + ((x ^ ((row >> 1) & 3)) << 4));
-            };
-            uint4 kr[U][2][KC];            // keys r and r + 8
-            uint32_t vr[U][D / 32][4];
+        // The warp's pages lp0, lp0 + parts, .. of the stage at hand.  (Twice, so
+        // that the usual one has no branch for a unit that moves.)
+        const auto stage = [&](int lp0, auto calm_const) {
+          constexpr bool kCalm = decltype(calm_const)::value;
+          const uint32_t sbase = smem_u32(stages + st * L.stage_bytes) + (uint32_t)(w * kPageSize * D);
+          // byte address of 16-byte chunk x of key row `row`
+          auto chunk = [&](uint32_t base, int row, int x) -> uint32_t {
+            if constexpr (D == 128) return base + (uint32_t)(row * 128 + ((x ^ (row & 7)) << 4));
+            return base + (uint32_t)(row * 64 + ((x ^ ((row >> 1) & 3)) << 4));
+          };
+          uint4 kr[U][2][KC];            // keys r and r + 8
+          uint32_t vr[U][D / 32][4];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const uint32_t kbase = sbase + (uint32_t)(2 * (part + u * parts) * L.half_bytes);
+#pragma unroll
+            for (int x = 0; x < KC; ++x) {
+              kr[u][0][x] = lds128(chunk(kbase, r, KC * c + x));
+              kr[u][1][x] = lds128(chunk(kbase, r + 8, KC * c + x));
+            }
+          }
+          // V byte pairs, transposed: matrices (keys 0-7, 8-15) of chunks 2 j, 2 j + 1
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const uint32_t vbase = sbase + (uint32_t)((2 * (part + u * parts) + 1) * L.half_bytes);
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j)
+              ldsm_x4_trans(chunk(vbase, ((mi & 1) << 3) + r8, 2 * j + (mi >> 1)), vr[u][j][0],
+                            vr[u][j][1], vr[u][j][2], vr[u][j][3]);
+          }
+          // K and V of the pages are in registers: the stage goes back
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[st]);
+          float fk[U], fv[U];
+          int valid[U], lo_valid[U], ves[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int ex = __shfl_sync(0xffffffffu, e_cur, (tl + u) & 31);
+            const int ke = (int)(int8_t)(ex & 0xff), ve = ex >> 8;
+            fk[u] = pow2i(ke);
+            const int lp = lp0 + u * parts;
+            // (a page past the item's end: the stage holds none, no key is seen)
+            valid[u] = lp < it.page_end ? min(kPageSize, it.ctx - lp * kPageSize) : 0;
+            ves[u] = ve;
+            fv[u] = pow2i(ve - ref);
+            // with a sliding window the row sees keys ctx - W .. ctx - 1 only
+            lo_valid[u] = p.window > 0 ? it.ctx - p.window - lp * kPageSize : 0;
+          }
+          [[maybe_unused]] int move[U];   // 2^move times o before the products of a page
+          if constexpr (!kCalm) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-              const uint32_t kbase = sbase + (uint32_t)(2 * (part + u * parts) * L.half_bytes);
+              move[u] = 0;
+              if (valid[u] > 0 && (unsigned)(ves[u] - ref + kDec8Spread) > 2u * kDec8Spread) {
+                const int to = max(ves[u], ref_max - kDec8Drop);
+                move[u] = ref - to;
+                ref = to;
+                ref_max = max(ref_max, to);
+              }
+              fv[u] = pow2i(ves[u] - ref);
+            }
+          }
+          // independent accumulators, so that the chains of MMAs are short
+          constexpr int kQk = NQ * U <= 2 ? 2 : 1;
+          float s[U][kQk][NQ][4];
 #pragma unroll
-              for (int x = 0; x < KC; ++x) {
-                kr[u][0][x] = lds128(chunk(kbase, r, KC * c + x));
-                kr[u][1][x] = lds128(chunk(kbase, r + 8, KC * c + x));
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int x = 0; x < kQk; ++x)
+#pragma unroll
+              for (int nq = 0; nq < NQ; ++nq)
+                s[u][x][nq][0] = s[u][x][nq][1] = s[u][x][nq][2] = s[u][x][nq][3] = 0.f;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const uint4 k0 = kr[u][0][kk / 4], k1 = kr[u][1][kk / 4];
+              const uint32_t w0 = (kk & 3) == 0 ? k0.x : (kk & 3) == 1 ? k0.y : (kk & 3) == 2 ? k0.z : k0.w;
+              const uint32_t w1 = (kk & 3) == 0 ? k1.x : (kk & 3) == 1 ? k1.y : (kk & 3) == 2 ? k1.z : k1.w;
+              const uint32_t ka[4] = {f16x2_of_e4m3x2(w0), f16x2_of_e4m3x2(w1),
+                                      f16x2_of_e4m3x2(w0 >> 16), f16x2_of_e4m3x2(w1 >> 16)};
+#pragma unroll
+              for (int nq = 0; nq < NQ; ++nq)
+                mma_f16_16816(s[u][kk % kQk][nq], ka, qb[kk][nq][0], qb[kk][nq][1]);
+            }
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (valid[u] < kPageSize || lo_valid[u] > 0) {
+              // values of keys that the row does not see may be anything,
+              // NaN included: cleared, since P = 0 would not stop it
+              const auto seen = [&](int key) { return key < valid[u] && key >= lo_valid[u]; };
+              const uint32_t m0 = (seen(2 * c) ? 0xffffu : 0u) | (seen(2 * c + 1) ? 0xffff0000u : 0u);
+              const uint32_t m1 = (seen(2 * c + 8) ? 0xffffu : 0u) | (seen(2 * c + 9) ? 0xffff0000u : 0u);
+#pragma unroll
+              for (int j = 0; j < D / 32; ++j) {
+                vr[u][j][0] &= m0;
+                vr[u][j][1] &= m1;
+                vr[u][j][2] &= m0;
+                vr[u][j][3] &= m1;
               }
             }
-            // V byte pairs, transposed: matrices (keys 0-7, 8-15) of chunks 2 j, 2 j + 1
+          float x0[U][NQ][2], x1[U][NQ][2], alpha[NQ][2];
+          bool need = false;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-              const uint32_t vbase = sbase + (uint32_t)((2 * (part + u * parts) + 1) * L.half_bytes);
+          for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
-              for (int j = 0; j < D / 32; ++j)
-                ldsm_x4_trans(chunk(vbase, ((mi & 1) << 3) + r8, 2 * j + (mi >> 1)), vr[u][j][0],
-                              vr[u][j][1], vr[u][j][2], vr[u][j][3]);
-            }
-            // K and V of the pages are in registers: the stage goes back
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[st]);
-            float fk[U], fv[U];
-            int valid[U], lo_valid[U], ves[U];
-            bool moved = false;   // o's unit does not serve all of these pages
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              const int ex = __shfl_sync(0xffffffffu, e_cur, (tl + u) & 31);
-              const int ke = (int)(int8_t)(ex & 0xff), ve = ex >> 8;
-              fk[u] = pow2i(ke);
-              const int lp = lp0 + u * parts;
-              // (a page past the item's end: the stage holds none, no key is seen)
-              valid[u] = lp < it.page_end ? min(kPageSize, it.ctx - lp * kPageSize) : 0;
-              ves[u] = ve;
-              fv[u] = pow2i(ve - ref);
-              // with a sliding window the row sees keys ctx - W .. ctx - 1 only
-              lo_valid[u] = p.window > 0 ? it.ctx - p.window - lp * kPageSize : 0;
-            }
-            int move[U];          // 2^move times o before the products of a page
-            if (!calm) {          // (rare, and alike in the warp)
+            for (int e = 0; e < 2; ++e) {
+              alpha[nq][e] = 1.f;
 #pragma unroll
               for (int u = 0; u < U; ++u) {
-                move[u] = 0;
-                if (valid[u] > 0 && (unsigned)(ves[u] - ref + kDec8Spread) > 2u * kDec8Spread) {
-                  const int to = max(ves[u], ref_max - kDec8Drop);
-                  move[u] = ref - to;
-                  moved = true;
-                  ref = to;
-                  ref_max = max(ref_max, to);
+                float a0 = s[u][0][nq][e], a1 = s[u][0][nq][2 + e];
+#pragma unroll
+                for (int x = 1; x < kQk; ++x) {
+                  a0 += s[u][x][nq][e];
+                  a1 += s[u][x][nq][2 + e];
                 }
-                fv[u] = pow2i(ves[u] - ref);
+                const float cs = qs[nq][e] * fk[u];
+                x0[u][nq][e] = r < valid[u] && r >= lo_valid[u] ? a0 * cs : -INFINITY;
+                x1[u][nq][e] = r + 8 < valid[u] && r + 8 >= lo_valid[u] ? a1 * cs : -INFINITY;
+                need |= fmaxf(x0[u][nq][e], x1[u][nq][e]) > m_run[nq][e] + kDec8RescaleThreshold;
               }
             }
-            // independent accumulators, so that the chains of MMAs are short
-            constexpr int kQk = NQ * U <= 2 ? 2 : 1;
-            float s[U][kQk][NQ][4];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-              for (int x = 0; x < kQk; ++x)
-#pragma unroll
-                for (int nq = 0; nq < NQ; ++nq)
-                  s[u][x][nq][0] = s[u][x][nq][1] = s[u][x][nq][2] = s[u][x][nq][3] = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-              for (int u = 0; u < U; ++u) {
-                const uint4 k0 = kr[u][0][kk / 4], k1 = kr[u][1][kk / 4];
-                const uint32_t w0 = (kk & 3) == 0 ? k0.x : (kk & 3) == 1 ? k0.y : (kk & 3) == 2 ? k0.z : k0.w;
-                const uint32_t w1 = (kk & 3) == 0 ? k1.x : (kk & 3) == 1 ? k1.y : (kk & 3) == 2 ? k1.z : k1.w;
-                const uint32_t ka[4] = {f16x2_of_e4m3x2(w0), f16x2_of_e4m3x2(w1),
-                                        f16x2_of_e4m3x2(w0 >> 16), f16x2_of_e4m3x2(w1 >> 16)};
-#pragma unroll
-                for (int nq = 0; nq < NQ; ++nq)
-                  mma_f16_16816(s[u][kk % kQk][nq], ka, qb[kk][nq][0], qb[kk][nq][1]);
-              }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-              if (valid[u] < kPageSize || lo_valid[u] > 0) {
-                // values of keys that the row does not see may be anything,
-                // NaN included: cleared, since P = 0 would not stop it
-                const auto seen = [&](int key) { return key < valid[u] && key >= lo_valid[u]; };
-                const uint32_t m0 = (seen(2 * c) ? 0xffffu : 0u) | (seen(2 * c + 1) ? 0xffff0000u : 0u);
-                const uint32_t m1 = (seen(2 * c + 8) ? 0xffffu : 0u) | (seen(2 * c + 9) ? 0xffff0000u : 0u);
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j) {
-                  vr[u][j][0] &= m0;
-                  vr[u][j][1] &= m1;
-                  vr[u][j][2] &= m0;
-                  vr[u][j][3] &= m1;
-                }
-              }
-            float x0[U][NQ][2], x1[U][NQ][2], alpha[NQ][2];
-            bool need = false;
+          if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
             for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                alpha[nq][e] = 1.f;
+                float mx = fmaxf(x0[0][nq][e], x1[0][nq][e]);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                  float a0 = s[u][0][nq][e], a1 = s[u][0][nq][2 + e];
-#pragma unroll
-                  for (int x = 1; x < kQk; ++x) {
-                    a0 += s[u][x][nq][e];
-                    a1 += s[u][x][nq][2 + e];
-                  }
-                  const float cs = qs[nq][e] * fk[u];
-                  x0[u][nq][e] = r < valid[u] && r >= lo_valid[u] ? a0 * cs : -INFINITY;
-                  x1[u][nq][e] = r + 8 < valid[u] && r + 8 >= lo_valid[u] ? a1 * cs : -INFINITY;
-                  need |= fmaxf(x0[u][nq][e], x1[u][nq][e]) > m_run[nq][e] + kDec8RescaleThreshold;
+                for (int u = 1; u < U; ++u) mx = fmaxf(mx, fmaxf(x0[u][nq][e], x1[u][nq][e]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                if (mx > m_run[nq][e] + kDec8RescaleThreshold) {
+                  alpha[nq][e] = fast_exp2(m_run[nq][e] - mx);
+                  m_run[nq][e] = mx;
                 }
               }
-            if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+            for (int jj = 0; jj < D / 16; ++jj)
 #pragma unroll
               for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  float mx = fmaxf(x0[0][nq][e], x1[0][nq][e]);
+                for (int x = 0; x < 4; ++x) o[jj][nq][x] *= alpha[nq][x & 1];
+          }
+          uint32_t pb[U][NQ][2];
 #pragma unroll
-                  for (int u = 1; u < U; ++u) mx = fmaxf(mx, fmaxf(x0[u][nq][e], x1[u][nq][e]));
-                  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                  if (mx > m_run[nq][e] + kDec8RescaleThreshold) {
-                    alpha[nq][e] = fast_exp2(m_run[nq][e] - mx);
-                    m_run[nq][e] = mx;
-                  }
-                }
+          for (int nq = 0; nq < NQ; ++nq) {
 #pragma unroll
-              for (int jj = 0; jj < D / 16; ++jj)
+            for (int e = 0; e < 2; ++e) l_part[nq][e] *= alpha[nq][e];
 #pragma unroll
-                for (int nq = 0; nq < NQ; ++nq)
+            for (int u = 0; u < U; ++u) {
+              float p0[2], p1[2];
 #pragma unroll
-                  for (int x = 0; x < 4; ++x) o[jj][nq][x] *= alpha[nq][x & 1];
-            }
-            uint32_t pb[U][NQ][2];
-#pragma unroll
-            for (int nq = 0; nq < NQ; ++nq) {
-#pragma unroll
-              for (int e = 0; e < 2; ++e) l_part[nq][e] *= alpha[nq][e];
-#pragma unroll
-              for (int u = 0; u < U; ++u) {
-                float p0[2], p1[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  // no key seen yet: every x is -inf and so is P's exponent
-                  const float mu = (m_run[nq][e] == -INFINITY ? 0.f : m_run[nq][e]) - kDec8PShift;
-                  p0[e] = fast_exp2(x0[u][nq][e] - mu);
-                  p1[e] = fast_exp2(x1[u][nq][e] - mu);
-                  l_part[nq][e] += p0[e] + p1[e];
-                }
-                const uint64_t f = pack_f32x2(fv[u], fv[u]);
-                unpack_f32x2(mul_f32x2(pack_f32x2(p0[0], p0[1]), f), p0[0], p0[1]);
-                unpack_f32x2(mul_f32x2(pack_f32x2(p1[0], p1[1]), f), p1[0], p1[1]);
-                pb[u][nq][0] = movmatrix_trans(pack_f16x2(p0[0], p0[1]));   // B: keys 2c, 2c + 1 of head r
-                pb[u][nq][1] = movmatrix_trans(pack_f16x2(p1[0], p1[1]));   // keys 8 + 2c ..
+              for (int e = 0; e < 2; ++e) {
+                // no key seen yet: every x is -inf and so is P's exponent
+                const float mu = (m_run[nq][e] == -INFINITY ? 0.f : m_run[nq][e]) - kDec8PShift;
+                p0[e] = fast_exp2(x0[u][nq][e] - mu);
+                p1[e] = fast_exp2(x1[u][nq][e] - mu);
+                l_part[nq][e] += p0[e] + p1[e];
               }
+              const uint64_t f = pack_f32x2(fv[u], fv[u]);
+              unpack_f32x2(mul_f32x2(pack_f32x2(p0[0], p0[1]), f), p0[0], p0[1]);
+              unpack_f32x2(mul_f32x2(pack_f32x2(p1[0], p1[1]), f), p1[0], p1[1]);
+              pb[u][nq][0] = movmatrix_trans(pack_f16x2(p0[0], p0[1]));   // B: keys 2c, 2c + 1 of head r
+              pb[u][nq][1] = movmatrix_trans(pack_f16x2(p1[0], p1[1]));   // keys 8 + 2c ..
             }
-            // O^T += V^T P^T
-            const auto products = [&](int u) {
+          }
+          // O^T += V^T P^T
+          const auto products = [&](int u) {
 #pragma unroll
-              for (int jj = 0; jj < D / 16; ++jj) {
-                // bytes (key 0: dims 0, 1; key 1: dims 0, 1) -> (dim 0: keys 0, 1; dim 1: ..)
-                const uint32_t v0 = __byte_perm(vr[u][jj / 2][2 * (jj & 1)], 0u, 0x3120);
-                const uint32_t v1 = __byte_perm(vr[u][jj / 2][2 * (jj & 1) + 1], 0u, 0x3120);
-                const uint32_t va[4] = {f16x2_of_e4m3x2(v0), f16x2_of_e4m3x2(v0 >> 16),
-                                        f16x2_of_e4m3x2(v1), f16x2_of_e4m3x2(v1 >> 16)};
+            for (int jj = 0; jj < D / 16; ++jj) {
+              // bytes (key 0: dims 0, 1; key 1: dims 0, 1) -> (dim 0: keys 0, 1; dim 1: ..)
+              const uint32_t v0 = __byte_perm(vr[u][jj / 2][2 * (jj & 1)], 0u, 0x3120);
+              const uint32_t v1 = __byte_perm(vr[u][jj / 2][2 * (jj & 1) + 1], 0u, 0x3120);
+              const uint32_t va[4] = {f16x2_of_e4m3x2(v0), f16x2_of_e4m3x2(v0 >> 16),
+                                      f16x2_of_e4m3x2(v1), f16x2_of_e4m3x2(v1 >> 16)};
 #pragma unroll
-                for (int nq = 0; nq < NQ; ++nq) mma_f16_16816(o[jj][nq], va, pb[u][nq][0], pb[u][nq][1]);
-              }
-            };
-            if (!moved) {
+              for (int nq = 0; nq < NQ; ++nq) mma_f16_16816(o[jj][nq], va, pb[u][nq][0], pb[u][nq][1]);
+            }
+          };
 #pragma unroll
-              for (int u = 0; u < U; ++u) products(u);
-            } else {
-#pragma unroll
-              for (int u = 0; u < U; ++u) {
+          for (int u = 0; u < U; ++u) {
+            if constexpr (!kCalm) {
+              if (move[u] != 0) {
                 const float f = pow2i(move[u]);
 #pragma unroll
                 for (int jj = 0; jj < D / 16; ++jj)
@@ -679,9 +676,17 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
                   for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) o[jj][nq][x] *= f;
-                products(u);
               }
             }
+            products(u);
+          }
+        };
+        for (int lp0 = it.page_begin + part; lp0 - part < it.page_end; lp0 += pps) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&full[st], ph, abort_flag));
+          if (!ok) break;
+          if (active && lp0 < it.page_end) {
+            if (calm) stage(lp0, std::true_type{});
+            else stage(lp0, std::false_type{});
           } else {
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
@@ -713,13 +718,7 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
 
         // ---------------------------------------------------------- the item's end
         const int Hq = p.num_q_heads;
-        const float unit = pow2i(ref);
-#pragma unroll
-        for (int jj = 0; jj < D / 16; ++jj)
-#pragma unroll
-          for (int nq = 0; nq < NQ; ++nq)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) o[jj][nq][x] *= unit;
+        float unit = pow2i(ref);   // times o is the sum itself
         float l_tot[NQ][2];
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq)
@@ -752,7 +751,7 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
 #pragma unroll
               for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) dst[32 * k++] = o[jj][nq][x];
+                for (int x = 0; x < 4; ++x) dst[32 * k++] = o[jj][nq][x] * unit;
           }
           if (!(ok = all_here())) break;
           if (part < half) {
@@ -769,7 +768,9 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
                 wb[nq][e] = m2 == -INFINITY ? 0.f : fast_exp2(m2 - mm);
                 m_run[nq][e] = mm;
                 l_tot[nq][e] = l_tot[nq][e] * wa[nq][e] + l2 * wb[nq][e];
+                wa[nq][e] *= unit;
               }
+            unit = 1.f;
 #pragma unroll
             for (int jj = 0; jj < D / 16; ++jj)
 #pragma unroll
@@ -790,7 +791,7 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
               const int head = nq * 8 + 2 * c + e;
               if (head >= g) continue;
               if (it.n_splits == 1) {
-                const float inv = 1.f / l_tot[nq][e];
+                const float inv = unit / l_tot[nq][e];
                 uint32_t* dst = reinterpret_cast<uint32_t*>(
                     p.out + ((size_t)it.tok * Hq + head0 + head) * D + 2 * r);
 #pragma unroll
@@ -801,7 +802,8 @@ __device__ __forceinline__ void decode8_cta(const DecodeParams& p, const Decode8
                 float* dst = p.part_o + (slot * Hq + head0 + head) * D + 2 * r;
 #pragma unroll
                 for (int jj = 0; jj < D / 16; ++jj)
-                  *reinterpret_cast<float2*>(dst + jj * 16) = make_float2(o[jj][nq][e], o[jj][nq][2 + e]);
+                  *reinterpret_cast<float2*>(dst + jj * 16) =
+                      make_float2(o[jj][nq][e] * unit, o[jj][nq][2 + e] * unit);
                 if (r == 0)
                   reinterpret_cast<float2*>(p.part_ml)[slot * Hq + head0 + head] =
                       make_float2(m_run[nq][e], l_tot[nq][e]);
