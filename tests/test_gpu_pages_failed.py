@@ -124,6 +124,39 @@ def test_bad_lengths_and_an_append_behind_it(q, ctx):
     assert np.array_equal(d_table.cpu().numpy(), stale_table(2, 4, [3, 4, 5]))
 
 
+def test_captured_assign_and_append_until_the_ring_is_empty():
+    """Each replay takes three pages; when they run out, replays go on and write
+    to no page at all."""
+    hb = lib()
+    ring = Ring(PAGES, head=3, taken=PAGES - 7, seed=5)
+    q, ctx, cu = dev([32, 5]), dev([32, 5]), dev([0, 0, 0])
+    d_table, slots = dev(stale_table(2, 3, [1, 2])), torch.zeros(37, dtype=torch.int64, device="cuda")
+    caches = Caches(6)
+    kn, vn = (torch.randn(37, HKV, D, device="cuda").to(torch.bfloat16) for _ in range(2))
+    batch = hb.make_batch(2, 37, 3, PAGES, HKV, HKV, D, cu, ctx, d_table)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        hb.hb_pages_assign(q, ctx, ring.pages, ring.state, ring.state, d_table, cu, slots)
+        hb.hb_kv_append(batch, kn, vn, *caches.bf16)
+        hb.hb_kv8_append(batch, kn, vn, *caches.kv8)
+    seen = [caches.pages()]
+    for n in range(4):
+        graph.replay()
+        seen.append(caches.pages())
+        taken = sorted(int(ring.order[(3 + 3 * n + k) % PAGES]) for k in range(3)) if n < 2 else []
+        assert changed(seen[-2], seen[-1]) == taken
+        assert ring.state.tolist() == [3 + 3 * min(n + 1, 2), 10, 0, 0]
+        if n < 2:
+            hb.hb_check()
+        else:
+            with pytest.raises(hb.HbError) as e:
+                hb.hb_check()
+            assert e.value.status == 8
+
+
 def test_the_assignments_error_comes_before_what_follows_from_it():
     hb = lib()
     for q, ctx, status in (([1], [17], 8), ([3], [2], 2)):
