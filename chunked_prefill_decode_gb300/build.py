@@ -22,9 +22,9 @@ LIB = os.path.join(PKG, "libhb.so")
 
 SOURCES = ["api.cu", "kv_append.cu", "attention.cu", "linear.cu", "noalloc.cu", "selftest.cu",
            "step.cu", "pages.cu", "kv8_append.cu", "kv8_widen.cu", "attention8.cu",
-           "builder.cpp"]
+           "norm.cu", "builder.cpp"]
 HEADERS = ["hb_internal.h", "ptx.cuh", "decode_body.cuh", "chunk_body.cuh", "decode_plan.h", "kv8.cuh",
-           "decode8_body.cuh"]
+           "decode8_body.cuh", "operands.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
           "-I", INCLUDE, "-I", CSRC]

@@ -367,6 +367,15 @@ namespace hb {
 
 hb_status internal_fail(hb_status s, const char* msg) { return fail(s, "%s", msg); }
 
+hb_status internal_failf(hb_status s, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return fail(s, "%s", buf);
+}
+
 hb_status internal_ok() { return ok(); }
 
 hb_status internal_check_batch(const hb_batch* b) { return check_batch(b); }

@@ -63,7 +63,7 @@ EXPORTED = (
     "hb_selftest_wait_timeout", "hb_selftest_flag_timeout", "hb_linear", "hb_linear_workspace_size",
     "hb_timing_durations", "hb_step_layout", "hb_step_slot_create", "hb_step_slot_destroy",
     "hb_step_slot_sync", "hb_step", "hb_kv8_append", "hb_kv8_plan", "hb_kv8_attention",
-    "hb_pages_assign", "hb_pages_release",
+    "hb_pages_assign", "hb_pages_release", "hb_norm",
 )
 
 LINEAR_STORE, LINEAR_GATED, LINEAR_RESIDUAL = 0, 1, 2
@@ -81,6 +81,13 @@ HB_STEP_SECTIONS = 6
 
 class HbLinearOut(ctypes.Structure):
     _fields_ = [("y", ctypes.c_void_p * 3), ("cols", ctypes.c_int32 * 3)]
+
+
+class HbNormArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("rows", "width", "stream_type", "reserved")]
+                + [(n, ctypes.c_void_p) for n in ("x", "y", "gate", "w_post", "w_pre", "x_out", "z")]
+                + [(n, ctypes.c_int64) for n in ("x_stride", "y_stride", "gate_stride", "x_out_stride", "z_stride")]
+                + [(n, ctypes.c_float) for n in ("eps", "residual_scale", "branch_scale", "weight_offset")])
 
 
 def lib_path() -> str:
@@ -154,6 +161,8 @@ def load():
     L.hb_pages_assign.argtypes = [i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.hb_pages_release.restype = ctypes.c_int
     L.hb_pages_release.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+    L.hb_norm.restype = ctypes.c_int
+    L.hb_norm.argtypes = [P(HbNormArgs), vp]
     L.hb_launch_count.restype = i64
     L.hb_launch_count.argtypes = []
     L.hb_builder_create.restype = ctypes.c_int
@@ -795,3 +804,98 @@ def hb_linear(x, w, outs, epilogue=LINEAR_STORE, stream=None, workspace="auto"):
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(load().hb_linear(_bf16(x, "x"), _bf16(w, "w"), M, N, K, int(epilogue),
                             ctypes.byref(o), ws_ptr, ws_bytes, _stream(stream)))
+
+
+# ---------------------------------------------------------------- norms
+_F32 = torch.float32
+
+
+def _refuse_rows(*specs):
+    """Raises for the first (name, tensor, dtypes, shape) that does not fit, or
+    whose rows (the last dimensions) are not dense."""
+    for name, t, dtypes, shape in specs:
+        if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+            raise ValueError(f"{name} must be a {' or '.join(str(d) for d in dtypes)} tensor")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if max(t.shape, default=0) > _INT_MAX:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}: over 2^31 - 1")
+        if t.numel() and not t[0].is_contiguous():
+            raise ValueError(f"{name}: each row must be contiguous")
+    for name, t, _, _ in specs:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on a CUDA device")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+
+
+def hb_norm(x=None, y=None, x_out=None, z=None, w_pre=None, w_post=None, gate=None, eps=1e-6, residual_scale=1.0,
+            branch_scale=1.0, weight_offset=0.0, stream=None):
+    """The norm after a branch (w_post), its gate, the residual sum and the norm
+    before the next branch, over [rows, width] tensors (rows may be apart):
+
+        u     = norm(y, w_post), or y
+        x_out = residual_scale * x + branch_scale * gate * u
+        z     = norm(x_out, w_pre)
+
+    y, z and the weights are bf16, x and x_out both bf16 or both fp32, gate
+    [width] or [rows, width] (or [1, width]) bf16.  What is None drops out; x_out
+    and z may be x or y (in place)."""
+    lead = x if x is not None else y
+    if not isinstance(lead, torch.Tensor) or lead.dim() != 2:
+        raise ValueError("x or y must be a [rows, width] tensor")
+    shape = lead.shape
+    rows, width = shape
+    a = HbNormArgs()
+    ok = True
+    dev = lead.get_device()
+    kind = x.dtype if x is not None else (x_out.dtype if isinstance(x_out, torch.Tensor) else _BF16)
+    try:
+        if x is not None:
+            ok = x.stride(1) == 1 or width == 1
+            a.x, a.x_stride = x.data_ptr(), x.stride(0)
+        if y is not None:
+            ok = ok and y.dtype is _BF16 and y.shape == shape and y.stride(1) == 1 and y.get_device() == dev
+            a.y, a.y_stride = y.data_ptr(), y.stride(0)
+        if x_out is not None:
+            ok = (ok and x_out.dtype is kind and x_out.shape == shape and x_out.stride(1) == 1
+                  and x_out.get_device() == dev)
+            a.x_out, a.x_out_stride = x_out.data_ptr(), x_out.stride(0)
+        if z is not None:
+            ok = ok and z.dtype is _BF16 and z.shape == shape and z.stride(1) == 1 and z.get_device() == dev
+            a.z, a.z_stride = z.data_ptr(), z.stride(0)
+        if w_pre is not None:
+            ok = (ok and w_pre.dtype is _BF16 and w_pre.shape == (width,) and w_pre.is_contiguous()
+                  and w_pre.get_device() == dev)
+            a.w_pre = w_pre.data_ptr()
+        if w_post is not None:
+            ok = (ok and w_post.dtype is _BF16 and w_post.shape == (width,) and w_post.is_contiguous()
+                  and w_post.get_device() == dev)
+            a.w_post = w_post.data_ptr()
+        if gate is not None:
+            each = gate.dim() == 2 and gate.shape[0] == rows and rows > 1
+            ok = (ok and gate.dtype is _BF16 and (each or gate.numel() == width) and gate.shape[-1] == width
+                  and gate.stride(-1) == 1 and gate.get_device() == dev)
+            a.gate, a.gate_stride = gate.data_ptr(), gate.stride(0) if each else 0
+        ok = (ok and rows <= _INT_MAX and 0 < width <= _INT_MAX and (kind is _BF16 or kind is _F32) and dev >= 0
+              and dev == _current_device())
+    except (AttributeError, IndexError):
+        ok = False
+    if not ok:
+        stream_t = (kind if kind in (_BF16, _F32) else _BF16,)
+        specs = [("x", x, (_BF16, _F32), shape), ("y", y, (_BF16,), shape), ("x_out", x_out, stream_t, shape),
+                 ("z", z, (_BF16,), shape), ("w_pre", w_pre, (_BF16,), (width,)),
+                 ("w_post", w_post, (_BF16,), (width,))]
+        if gate is not None:
+            each = isinstance(gate, torch.Tensor) and gate.dim() == 2
+            specs.append(("gate", gate, (_BF16,), ((1 if _numel(gate) == width else rows), width) if each else (width,)))
+        _refuse_rows(*(s for s in specs if s[1] is not None))
+        raise ValueError("width must be > 0, and the tensors on one device")
+    if rows == 0:
+        return
+    a.rows, a.width, a.stream_type = rows, width, 1 if kind is _F32 else 0
+    a.eps, a.residual_scale, a.branch_scale, a.weight_offset = eps, residual_scale, branch_scale, weight_offset
+    st = (_lib or load()).hb_norm(ctypes.byref(a), _raw_stream(stream, dev))
+    if st:
+        _check(st)

@@ -541,11 +541,53 @@ size_t hb_linear_workspace_size(int32_t M, int32_t N, int32_t K, int32_t epilogu
                                 int32_t num_sms);
 
 /* ---------------------------------------------------------------------------
+ * Norms around the branches of a block.  (The pages name the block's linear
+ * layers and its attention; its norms are what a model adds between them.)
+ * For each of `rows` rows of `width` elements, with n(v, w) =
+ * v * rsqrt(mean(v^2) + eps) * (weight_offset + w):
+ *   u     = n(y, w_post), or y where w_post is NULL       the branch's output
+ *   x_out = residual_scale * x + branch_scale * gate * u  the residual stream
+ *   z     = n(x_out before its rounding, w_pre)           the next branch's input
+ * Terms that are not given drop out: gate NULL counts as 1; without y the
+ * stream is residual_scale * x (the first norm of a model), without x it is the
+ * branch alone; w_pre NULL gives z without weights.  x or y, and x_out or z,
+ * must be given; w_post and gate need y, w_pre needs z.
+ *   y, gate, z       device, bf16
+ *   w_post, w_pre    device, [width] bf16
+ *   x, x_out         device, bf16 or fp32 (stream_type, both alike)
+ *   *_stride         elements from row to row, 16 bytes a multiple;
+ *                    gate_stride 0: one row of gates for all
+ * width is a multiple of 8, at most 16384; pointers are 16-byte aligned.
+ * x_out or z may be x, y or a gate per row, row for row and of the same
+ * element size (in place), and overlap nothing otherwise
+ * (HB_ERR_INVALID_ARG).  Sums and means are fp32 (64 bits where a row's
+ * squares leave its range), one rounding per output; what stands between rows
+ * is neither read nor written.
+ * ------------------------------------------------------------------------- */
+typedef enum hb_stream_type {
+  HB_STREAM_BF16 = 0,
+  HB_STREAM_FP32 = 1
+} hb_stream_type;
+
+typedef struct hb_norm_args {
+  int32_t rows, width;
+  int32_t stream_type;     /* hb_stream_type of x and x_out                  */
+  int32_t reserved;        /* must be 0                                      */
+  const void *x, *y, *gate, *w_post, *w_pre;
+  void *x_out, *z;
+  int64_t x_stride, y_stride, gate_stride, x_out_stride, z_stride;
+  float eps;               /* >= 0                                           */
+  float residual_scale, branch_scale, weight_offset;
+} hb_norm_args;
+
+hb_status hb_norm(const hb_norm_args* args, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Instrumentation.  When enabled, every kernel launch of this library is
  * bracketed by CUDA events recorded on its launch stream.
  *   kernel ids: 0 = kv append (either cache), 1 = attention (decode and chunk
  *   work in one launch; over the 8-bit cache its widening launch is a record
- *   of its own), 2 = linear layer; hb_pages_* are counted but not timed
+ *   of its own), 2 = linear layer; the other calls are counted but not timed
  * ------------------------------------------------------------------------- */
 #define HB_NUM_KERNEL_IDS 3
 

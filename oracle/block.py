@@ -1,0 +1,29 @@
+"""Oracle for what a transformer block does around its attention and linear
+layers (fp64, CPU): norms, rotary positions, low-rank adapters.
+
+TEST INFRASTRUCTURE, like the rest of `oracle/`: only tests import it; it
+shares no code with the CUDA library.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+
+def rms_norm(v, w, eps, offset=0.0) -> np.ndarray:
+    """v * (offset + w) / sqrt(mean(v^2) + eps) over the last axis; w None: ones."""
+    v = np.asarray(v, np.float64)
+    gain = 1.0 if w is None else offset + np.asarray(w, np.float64)
+    with np.errstate(all="ignore"):
+        return v / np.sqrt(np.mean(v * v, -1, keepdims=True) + eps) * gain
+
+
+def norm(x=None, y=None, gate=None, w_post=None, w_pre=None, eps=1e-6, residual_scale=1.0, branch_scale=1.0,
+         offset=0.0):
+    """(new stream, its norm) of rows x, y [rows, width]."""
+    new = 0.0
+    if x is not None:
+        new = residual_scale * np.asarray(x, np.float64)
+    if y is not None:
+        u = np.asarray(y, np.float64) if w_post is None else rms_norm(y, w_post, eps, offset)
+        new = new + branch_scale * (u if gate is None else u * np.asarray(gate, np.float64))
+    return new, rms_norm(new, w_pre, eps, offset)

@@ -1,0 +1,214 @@
+"""hb_norm on the GPU against its definition in 64 bits.
+
+Tolerance: an output is rounded once (half a step: bf16 2^-8, fp32 2^-24 of
+it).  Before that, in fp32: a mean of squares is a chain of at most 32 fused
+products per thread and two trees of 5 sums (42 roundings, halved by the
+root), the root itself 2 steps, the products and sums at most 8 more; each
+2^-24 of terms no larger than |residual_scale x| + |branch_scale gate u|.  64
+roundings cover the stream's, and as many more its norm's."""
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+from _hbutil import lib
+from oracle import block as ob
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+ULP = 2.0 ** -24
+
+
+def f64(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def make(rows, width, seed, dtype=BF, gap=0, size=1.0):
+    g = torch.Generator("cuda").manual_seed(seed)
+    return (torch.randn(rows, width + gap, generator=g, device="cuda") * size).to(dtype)[:, :width]
+
+
+def case(rows, width, form, gate=None, dtype=BF, gap=0, seed=0):
+    """The tensors of a call: form is a set of letters, x y p(ost) w(eights before) o(ut) z."""
+    t = {"x": make(rows, width, seed, dtype, gap, 3.0) if "x" in form else None,
+         "y": make(rows, width, seed + 1, BF, gap) if "y" in form else None,
+         "w_post": 1 + 0.3 * make(1, width, seed + 2)[0] if "p" in form else None,
+         "w_pre": 1 + 0.3 * make(1, width, seed + 3)[0] if "w" in form else None,
+         "gate": None if gate is None else make(rows if gate == "row" else 1, width, seed + 4, BF, gap),
+         "x_out": make(rows, width, seed + 5, dtype, gap) if "o" in form else None,
+         "z": make(rows, width, seed + 6, BF, gap) if "z" in form else None}
+    if gate == "vector":
+        t["gate"] = t["gate"][0].contiguous()
+    return t
+
+
+def expected(t, **kw):
+    names = dict(eps=kw.get("eps", 1e-6), residual_scale=kw.get("residual_scale", 1.0),
+                 branch_scale=kw.get("branch_scale", 1.0), offset=kw.get("weight_offset", 0.0))
+    ins = {k: f64(t[k]) for k in ("x", "y", "gate", "w_post", "w_pre")}
+    new, z = ob.norm(**ins, **names)
+    # the size of what the stream is summed from
+    part = 0.0 if ins["x"] is None else np.abs(names["residual_scale"] * ins["x"])
+    if ins["y"] is not None:
+        zero = dict(ins, x=None, w_pre=None)
+        part = part + np.abs(ob.norm(**zero, **names)[0])
+    # what the norm multiplies the stream with
+    gain = 1.0 if ins["w_pre"] is None else np.abs(names["offset"] + ins["w_pre"])
+    with np.errstate(all="ignore"):
+        gain = gain / np.sqrt(np.mean(new * new, -1, keepdims=True) + names["eps"])
+    return new, z, part, gain
+
+
+def close(got, want, parts, rounding):
+    got = f64(got)
+    assert np.isfinite(got).all()
+    bound = np.abs(want) * rounding + parts
+    assert (np.abs(got - want) <= bound).all(), f"worst excess {(np.abs(got - want) - bound).max():.3e}"
+
+
+def check(t, want, dtype=BF):
+    new, z, part, gain = want
+    if t["x_out"] is not None:
+        close(t["x_out"], new, 64 * ULP * part, 2.0 ** -8 if dtype is BF else ULP)
+    if t["z"] is not None:
+        close(t["z"], z, 128 * ULP * (part * gain + np.abs(z)) * (1 + 2.0 ** -8), 2.0 ** -8)
+
+
+FORMS = ["xwz", "xz", "xyoz", "xywoz", "xyo", "xypo", "xypwoz", "yoz", "ypwz", "xywz"]
+
+
+@pytest.mark.parametrize("rows,width", [(1, 8), (3, 16), (5, 248), (2, 256), (1, 1000), (700, 1024), (3, 4096),
+                                        (331, 4104), (1, 8192), (2, 8200), (310, 16384), (1500, 40), (1, 7168)])
+def test_against_the_definition(rows, width):
+    hb = lib()
+    for i, (form, gate, dtype) in enumerate(itertools.product(FORMS, (None, "channel", "row"), (BF, F32))):
+        if gate and "y" not in form:
+            continue
+        if rows * width > 1 << 21 and i % 5:
+            continue
+        kw = dict(eps=1e-5, residual_scale=[1.0, 0.7][i % 2], branch_scale=[1.0, -0.4][i % 3 == 0],
+                  weight_offset=float(i % 2))
+        t = case(rows, width, form, gate, dtype, seed=10 * i)
+        want = expected(t, **kw)
+        hb.hb_norm(**t, **kw)
+        check(t, want, dtype)
+    hb.hb_check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("gap", [8, 1016])
+def test_what_stands_between_rows_stays(gap, dtype):
+    hb = lib()
+    rows, width = 37, 520
+    t = case(rows, width, "xypwoz", "row", dtype, gap)
+    for name in ("x", "y", "gate"):                          # and is not read
+        t[name]._base[:, width:] = float("nan")
+    outs = {n: t[n]._base.clone() for n in ("x_out", "z")}
+    want = expected(t)
+    hb.hb_norm(**t)
+    check(t, want, dtype)
+    for n, was in outs.items():
+        assert torch.equal(t[n]._base[:, width:], was[:, width:])
+
+
+@pytest.mark.parametrize("rows,width", [(3, 8192), (400, 640)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_in_place_gives_the_same_bits(rows, width, dtype):
+    hb = lib()
+    t = case(rows, width, "xypwoz", "row", dtype)
+    hb.hb_norm(**t)
+    for over in ([("x_out", "x")], [("x_out", "x"), ("z", "y")], [("x_out", "x"), ("z", "gate")]):
+        u = {k: v if v is None else v.clone() for k, v in t.items()}
+        for out, source in over:
+            u[out] = u[source]
+        hb.hb_norm(**u)
+        assert torch.equal(u["x_out"], t["x_out"]) and torch.equal(u["z"], t["z"])
+
+
+def test_one_row_of_gates_in_every_form():
+    hb = lib()
+    t = case(50, 264, "xyoz", "channel")
+    hb.hb_norm(**t)
+    for gate in (t["gate"][0], t["gate"].expand(50, 264), t["gate"].repeat(50, 1)):
+        u = dict(t, gate=gate, x_out=torch.empty_like(t["x_out"]), z=torch.empty_like(t["z"]))
+        hb.hb_norm(**u)
+        assert torch.equal(u["z"], t["z"]) and torch.equal(u["x_out"], t["x_out"])
+
+
+@pytest.mark.parametrize("size", [1e30, 1e-18, 1e-22])
+def test_squares_outside_of_fp32(size):
+    """A row of large or tiny values, between ordinary ones, is normed as well."""
+    hb = lib()
+    for width in (64, 4096):
+        t = case(5, width, "xypwoz")
+        for n in "xy":
+            t[n][2] = (t[n][2].float() * size).to(BF)
+        want = expected(t, eps=0.0)
+        hb.hb_norm(**t, eps=0.0)
+        check(t, want)
+
+
+def test_rows_of_zeros():
+    hb = lib()
+    t = case(4, 512, "xypwoz")
+    t["x"][1] = 0
+    t["y"][1] = 0
+    want = expected(t)
+    hb.hb_norm(**t)
+    check(t, want)
+    assert not t["z"][1].any() and not t["x_out"][1].any()
+    hb.hb_norm(**t, eps=0.0)                                  # 0 / 0, as by the formula
+    assert t["z"][1].isnan().all() and t["z"][0].isfinite().all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_values_that_are_not_finite_stay_in_their_row(bad):
+    hb = lib()
+    t = case(5, 1024, "xywoz", "row")
+    t["x"][3, 77] = bad
+    hb.hb_norm(**t)
+    new, z = (torch.from_numpy(a) for a in expected(t)[:2])
+    z[3, 77] = float("nan")                                   # (inf / inf)
+    for got, want in ((t["x_out"], new), (t["z"], z)):
+        got = got.double().cpu()
+        assert torch.equal(got.isnan(), want.isnan())
+        assert torch.equal(got.isinf(), want.isinf())
+        rows = torch.tensor([0, 1, 2, 4])
+        assert torch.allclose(got[rows], want[rows], rtol=2.0 ** -7, atol=1e-6)
+
+
+def test_captured_replayed_and_on_another_stream():
+    hb = lib()
+    t = case(64, 4096, "xywoz", "channel", F32)
+    hb.hb_norm(**t)
+    want = t["x_out"].clone(), t["z"].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    t["z"].zero_()
+    side.wait_stream(torch.cuda.current_stream())
+    hb.hb_norm(**t, stream=side)
+    side.synchronize()
+    assert torch.equal(t["z"], want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hb.hb_norm(**t)
+        hb.hb_norm(x=t["x_out"], x_out=t["x_out"], residual_scale=0.5)
+    for _ in range(3):
+        t["z"].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(t["z"], want[1]) and torch.equal(t["x_out"], 0.5 * want[0])
+
+
+def test_offsets_past_32_bits():
+    """Rows whose elements lie more than 2^32 apart."""
+    hb = lib()
+    rows, width, gap = 3, 64, (1 << 31) + 64
+    base = torch.empty(rows * gap, dtype=BF, device="cuda")
+    x = base.as_strided((rows, width), (gap, 1))
+    z = base.as_strided((rows, width), (gap, 1), 4096)
+    x.copy_(make(rows, width, 1))
+    want = ob.norm(x=f64(x))[1]
+    hb.hb_norm(x=x, z=z)
+    close(z, want, 64 * ULP * np.abs(want), 2.0 ** -8)
