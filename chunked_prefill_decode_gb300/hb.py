@@ -63,7 +63,7 @@ EXPORTED = (
     "hb_selftest_wait_timeout", "hb_selftest_flag_timeout", "hb_linear", "hb_linear_workspace_size",
     "hb_timing_durations", "hb_step_layout", "hb_step_slot_create", "hb_step_slot_destroy",
     "hb_step_slot_sync", "hb_step", "hb_kv8_append", "hb_kv8_plan", "hb_kv8_attention",
-    "hb_pages_assign", "hb_pages_release", "hb_norm",
+    "hb_pages_assign", "hb_pages_release", "hb_norm", "hb_rope_phases", "hb_rope",
 )
 
 LINEAR_STORE, LINEAR_GATED, LINEAR_RESIDUAL = 0, 1, 2
@@ -88,6 +88,15 @@ class HbNormArgs(ctypes.Structure):
                 + [(n, ctypes.c_void_p) for n in ("x", "y", "gate", "w_post", "w_pre", "x_out", "z")]
                 + [(n, ctypes.c_int64) for n in ("x_stride", "y_stride", "gate_stride", "x_out_stride", "z_stride")]
                 + [(n, ctypes.c_float) for n in ("eps", "residual_scale", "branch_scale", "weight_offset")])
+
+
+class HbRopeParams(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("factor", ctypes.c_float),
+                ("eps", ctypes.c_float), ("phases", ctypes.c_void_p), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p)]
+
+
+ROPE_SCALINGS = ("none", "linear", "base", "parts")
 
 
 def lib_path() -> str:
@@ -163,6 +172,10 @@ def load():
     L.hb_pages_release.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
     L.hb_norm.restype = ctypes.c_int
     L.hb_norm.argtypes = [P(HbNormArgs), vp]
+    L.hb_rope_phases.restype = ctypes.c_int
+    L.hb_rope_phases.argtypes = [i32, ctypes.c_double, i32] + [ctypes.c_double] * 4 + [vp]
+    L.hb_rope.restype = ctypes.c_int
+    L.hb_rope.argtypes = [P(HbBatch), P(HbRopeParams), vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp]
     L.hb_launch_count.restype = i64
     L.hb_launch_count.argtypes = []
     L.hb_builder_create.restype = ctypes.c_int
@@ -899,3 +912,125 @@ def hb_norm(x=None, y=None, x_out=None, z=None, w_pre=None, w_post=None, gate=No
     st = (_lib or load()).hb_norm(ctypes.byref(a), _raw_stream(stream, dev))
     if st:
         _check(st)
+
+
+# ---------------------------------------------------------------- rotary positions
+def rope_phases(rotary_dim, base=10000.0, scaling="none", scale_by=1.0, original_context=0, parts=(1.0, 32.0)):
+    """What each pair of a head turns by from one position to the next, in
+    2^-64 of a turn (a host uint64 array; see hb_rope_phases)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {', '.join(ROPE_SCALINGS)}")
+    out = np.zeros(max(0, int(rotary_dim)) // 2, np.uint64)
+    _check(load().hb_rope_phases(int(rotary_dim), base, ROPE_SCALINGS.index(scaling), scale_by, original_context,
+                                 parts[0], parts[1], out.ctypes.data))
+    return out
+
+
+def make_rope(rotary_dim, base=10000.0, scaling="none", scale_by=1.0, original_context=0, parts=(1.0, 32.0),
+              interleaved=False, factor=1.0, q_weight=None, k_weight=None, eps=1e-6, device="cuda") -> HbRopeParams:
+    """hb_rope's parameters, with the phases on the device.  rotary_dim 0: head
+    norms alone.  Made once per model; the tensors live as long as it."""
+    r = HbRopeParams()
+    r.rotary_dim, r.interleaved, r.factor, r.eps = int(rotary_dim), int(bool(interleaved)), factor, eps
+    keep = []
+    if r.rotary_dim:
+        phases = torch.from_numpy(rope_phases(rotary_dim, base, scaling, scale_by, original_context,
+                                              parts).view(np.int64)).to(device)
+        keep.append(phases)
+        r.phases = phases.data_ptr()
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            if w.dtype != torch.bfloat16 or w.dim() != 1 or not w.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous [head_dim] bfloat16 tensor")
+            if w.device.type != torch.device(device).type:
+                raise ValueError(f"{name} is on {w.device}, not on {device}")
+            keep.append(w)
+            setattr(r, name, w.data_ptr())
+    r.tensors, r.head_dims = tuple(keep), {w.numel() for w in (q_weight, k_weight) if w is not None}
+    r.device_index = keep[0].get_device() if keep else None
+    return r
+
+
+def _dense_heads(t):
+    """Whether a token's heads stand one behind the other."""
+    return t.stride(2) == 1 and (t.stride(1) == t.shape[2] or t.shape[1] == 1)
+
+
+def _in_place_or_dense(out, source):
+    if out is source:
+        return True
+    if out.data_ptr() == source.data_ptr():
+        return _dense_heads(out) and (out.stride(0) == source.stride(0) or out.shape[0] == 1)
+    return out.is_contiguous()
+
+
+def hb_rope(batch, rope, q, k, v, q_out, k_out, k_cache, v_cache, stream=None):
+    """Rotary positions of the batch's q [total_q, Hq, D] and k [total_q, Hkv, D]
+    (after head norms where `rope` has weights), with k and v put into their cache
+    pages.  q, k and v may be columns of one tensor (dense heads, tokens a stride
+    apart); q_out and k_out are q and k themselves or contiguous tensors; k_out
+    may be None; v, k_cache and v_cache are all None where nothing is to be
+    appended."""
+    hq, hkv, d, n = batch.num_q_heads, batch.num_kv_heads, batch.head_dim, batch.total_q
+    q_rows, k_rows, pool = (n, hq, d), (n, hkv, d), (batch.num_pages, batch.page_size, hkv, d)
+    try:
+        dev = q.get_device()
+        ok = (q.dtype is _BF16 and q.shape == q_rows and _dense_heads(q)
+              and k.dtype is _BF16 and k.shape == k_rows and _dense_heads(k)
+              and q_out.dtype is _BF16 and q_out.shape == q_rows and _in_place_or_dense(q_out, q)
+              and dev >= 0 and dev == k.get_device() == q_out.get_device() and dev == _current_device()
+              and (rope.device_index is None or rope.device_index == dev)
+              and (not rope.head_dims or rope.head_dims == {d}))
+        if k_out is not None:
+            ok = (ok and k_out.dtype is _BF16 and k_out.shape == k_rows and k_out.get_device() == dev
+                  and _in_place_or_dense(k_out, k))
+        if k_cache is not None:
+            ok = (ok and v.dtype is _BF16 and v.shape == k_rows and _dense_heads(v) and v.get_device() == dev
+                  and k_cache.dtype is _BF16 and k_cache.shape == pool and k_cache.is_contiguous()
+                  and v_cache.dtype is _BF16 and v_cache.shape == pool and v_cache.is_contiguous()
+                  and k_cache.get_device() == dev == v_cache.get_device())
+        else:
+            ok = ok and v is None and v_cache is None
+    except AttributeError:
+        ok = False
+    if not ok:
+        _refuse_rope(rope, d, (("q", q, q_rows), ("k", k, k_rows), ("v", v, k_rows)),
+                     (("q_out", q_out, q_rows, q), ("k_out", k_out, k_rows, k)),
+                     (("k_cache", k_cache, pool), ("v_cache", v_cache, pool)))
+    if n == 0:
+        return
+    # (data_ptr() of an empty pool is 0; the library refuses it)
+    st = (_lib or load()).hb_rope(
+        ctypes.byref(batch), ctypes.byref(rope), q.data_ptr(), q.stride(0), k.data_ptr(), k.stride(0),
+        v.data_ptr() if v is not None else None, v.stride(0) if v is not None else 0, q_out.data_ptr(),
+        k_out.data_ptr() if k_out is not None else None, k_cache.data_ptr() if k_cache is not None else None,
+        v_cache.data_ptr() if v_cache is not None else None, _raw_stream(stream, dev))
+    if st:
+        _check(st)
+
+
+def _refuse_rope(rope, d, ins, outs, pools):
+    if not isinstance(rope, HbRopeParams) or not hasattr(rope, "tensors"):
+        raise ValueError("rope must be what make_rope returned")
+    if rope.head_dims and rope.head_dims != {d}:
+        raise ValueError(f"the head norms' weights have {sorted(rope.head_dims)} elements, head_dim is {d}")
+    cached = [x is not None for x in (ins[2][1], pools[0][1], pools[1][1])]
+    if any(cached) != all(cached):
+        raise ValueError("v, k_cache and v_cache go together")
+    if not all(isinstance(x[1], torch.Tensor) for x in ins[:2]):
+        raise ValueError("q and k must be tensors")
+    specs = [(name, t, (_BF16,), shape) for name, t, shape in ins if t is not None or name != "v"]
+    specs += [(name, t, (_BF16,), shape) for name, t, shape, _ in outs if t is not None or name != "k_out"]
+    specs += [(name, t, (_BF16,), shape) for name, t, shape in pools if t is not None]
+    for name, t, _, _ in specs:
+        if isinstance(t, torch.Tensor) and name.endswith("cache") and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    for name, t, shape, source in outs:
+        if (isinstance(t, torch.Tensor) and isinstance(source, torch.Tensor) and t.dim() == 3 and source.dim() == 3
+                and not _in_place_or_dense(t, source)):
+            raise ValueError(f"{name} must be contiguous, or {name[0]} itself")
+    _refuse_rows(*specs)
+    if rope.device_index is not None and rope.device_index != torch.cuda.current_device():
+        raise ValueError(f"rope's tensors are on cuda:{rope.device_index}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    raise ValueError("q, k and v: heads must be dense, and all tensors on one device")

@@ -583,6 +583,75 @@ typedef struct hb_norm_args {
 hb_status hb_norm(const hb_norm_args* args, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Rotary positions.  (The pages leave a model's positions out; the attention
+ * here takes q and k as they are, so this goes between the projection that
+ * makes them and the append.)
+ *
+ * hb_rope_phases (host) writes the angle that pair i = 0 .. rotary_dim/2 - 1
+ * of a head turns by from one position to the next, as a fraction of a turn in
+ * 64-bit fixed point: phases[i] = f_i / (2 pi) * 2^64, with f_i = base^(-2 i /
+ * rotary_dim) radians, scaled for contexts longer than the model was trained
+ * on:
+ *   HB_ROPE_PLAIN   f_i
+ *   HB_ROPE_LINEAR  f_i / scale_by (positions interpolated)
+ *   HB_ROPE_BASE    with base * scale_by^(rotary_dim / (rotary_dim - 2))
+ *   HB_ROPE_PARTS   by frequency: a pair that makes t = original_context * f_i
+ *                   / (2 pi) turns over the trained context keeps f_i from t =
+ *                   high on, has f_i / scale_by up to t = low, and between
+ *                   them f_i * (g + (1 - g) / scale_by), g = (t - low) / (high
+ *                   - low)
+ * rotary_dim is a positive multiple of 16, base > 1, scale_by >= 1, 0 <= low <
+ * high (what a kind does not use is not looked at).
+ * ------------------------------------------------------------------------- */
+typedef enum hb_rope_scaling {
+  HB_ROPE_PLAIN = 0,
+  HB_ROPE_LINEAR = 1,
+  HB_ROPE_BASE = 2,
+  HB_ROPE_PARTS = 3
+} hb_rope_scaling;
+
+hb_status hb_rope_phases(int32_t rotary_dim, double base, int32_t scaling, double scale_by,
+                         double original_context, double low, double high, uint64_t* phases);
+
+typedef struct hb_rope_params {
+  int32_t rotary_dim;      /* dims of a head that turn: a multiple of 16 in     */
+                           /* [0, head_dim]; the others stay                    */
+  int32_t interleaved;     /* 0: pair i is dims (i, i + rotary_dim/2); 1: (2i,  */
+                           /* 2i+1)                                             */
+  float factor;            /* multiplies what turns (an attention factor), or 1 */
+  float eps;               /* of the head norms, >= 0                           */
+  const uint64_t* phases;  /* device, [rotary_dim/2], 16-byte aligned           */
+  const void* q_weight;    /* device, [head_dim] bf16: every q head is first    */
+  const void* k_weight;    /* x * rsqrt(mean(x^2) + eps) * q_weight (k alike);  */
+                           /* NULL: no such norm                                */
+} hb_rope_params;
+
+/*
+ * For every new token of the batch, at its position p = context_len - q_len +
+ * j: q and k heads normed (where weights are given) and turned by p, q into
+ * q_out, k into k_out (unless NULL) and into its page slot of k_cache, v as it
+ * is into its slot of v_cache (hb_kv_append's, which is then not needed).
+ * Without caches (k_cache, v_cache and v all NULL) it only turns q and k, for
+ * hb_kv8_append or an append elsewhere.  Tokens behind the last sequence are
+ * left as they were; of the batch's descriptors, sliding_window plays no part.
+ * fp32 arithmetic, one rounding; the angle is exact to 2^-32 of a turn at any
+ * position.
+ *   q, k, v          device, bf16: token rows of Hq * D and Hkv * D elements,
+ *                    *_stride elements apart (a multiple of 8; larger than the
+ *                    row where q, k and v are columns of one array)
+ *   q_out, k_out     q and k themselves (in place, their strides), or [total_q,
+ *                    heads, D] contiguous arrays that overlap no other operand
+ *   k_cache, v_cache device pools as in hb_kv_append
+ * Errors as hb_kv_append; HB_ERR_INVALID_ARG for operands that overlap.  A page
+ * id outside [0, num_pages) is skipped (q_out and k_out are written) and
+ * reported by hb_check().
+ */
+hb_status hb_rope(const hb_batch* batch, const hb_rope_params* rope, const void* q,
+                  int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                  int64_t v_stride, void* q_out, void* k_out, void* k_cache, void* v_cache,
+                  void* stream);
+
+/* ---------------------------------------------------------------------------
  * Instrumentation.  When enabled, every kernel launch of this library is
  * bracketed by CUDA events recorded on its launch stream.
  *   kernel ids: 0 = kv append (either cache), 1 = attention (decode and chunk

@@ -27,3 +27,36 @@ def norm(x=None, y=None, gate=None, w_post=None, w_pre=None, eps=1e-6, residual_
         u = np.asarray(y, np.float64) if w_post is None else rms_norm(y, w_post, eps, offset)
         new = new + branch_scale * (u if gate is None else u * np.asarray(gate, np.float64))
     return new, rms_norm(new, w_pre, eps, offset)
+
+
+def rope_frequencies(rotary_dim, base=10000.0, scaling="none", by=1.0, original=0.0, low=1.0, high=32.0) -> np.ndarray:
+    """Radians per position of pairs 0 .. rotary_dim/2 - 1."""
+    out = []
+    for i in range(rotary_dim // 2):
+        b = np.longdouble(base)
+        if scaling == "base":
+            b = b * np.longdouble(by) ** (np.longdouble(rotary_dim) / (rotary_dim - 2))
+        f = b ** (-np.longdouble(2 * i) / rotary_dim)
+        if scaling == "linear":
+            f = f / by
+        elif scaling == "parts":
+            turns = original * f / (2 * np.longdouble(np.pi))
+            if turns <= low:
+                f = f / by
+            elif turns < high:
+                g = (turns - low) / (high - low)
+                f = f * g + f / by * (1 - g)
+        out.append(f)
+    return np.array(out, np.longdouble)
+
+
+def rotate(x, angle, interleaved=False, factor=1.0) -> np.ndarray:
+    """Heads x [..., D] turned by angle [..., rotary_dim / 2] (radians)."""
+    x = np.asarray(x, np.float64)
+    out, half = x.copy(), angle.shape[-1]
+    c, s = np.cos(angle) * factor, np.sin(angle) * factor
+    for i in range(half):
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+        out[..., a] = x[..., a] * c[..., i] - x[..., b] * s[..., i]
+        out[..., b] = x[..., a] * s[..., i] + x[..., b] * c[..., i]
+    return out

@@ -30,3 +30,36 @@ def test_norm_sums_the_branches():
     new, z = ob.norm(x=x, y=y, residual_scale=0.5, branch_scale=-2.0)
     assert np.allclose(new, 0.5 * x - 2 * y, rtol=1e-15)
     assert np.allclose(z, ob.norm(x=new)[1], rtol=1e-15)
+
+
+def test_rotation_closed_forms():
+    x = np.arange(1.0, 9.0)
+    assert np.array_equal(ob.rotate(x, np.zeros(4)), x)
+    quarter = ob.rotate(x, np.full(2, np.pi / 2))             # the first four dims, pairs (0, 2) and (1, 3)
+    assert np.allclose(quarter, [-3, -4, 1, 2, 5, 6, 7, 8], atol=1e-15)
+    quarter = ob.rotate(x, np.full(2, np.pi / 2), interleaved=True, factor=2.0)
+    assert np.allclose(quarter, [-4, 2, -8, 6, 5, 6, 7, 8], atol=1e-15)
+
+
+def test_rotated_products_depend_on_distances_alone():
+    rng = np.random.default_rng(2)
+    f = ob.rope_frequencies(16).astype(np.float64)
+    q, k = rng.standard_normal((2, 16))
+    for inter in (False, True):
+        a = ob.rotate(q, 105 * f, inter) @ ob.rotate(k, 100 * f, inter)
+        b = ob.rotate(q, 5 * f, inter) @ k
+        assert np.isclose(a, b, rtol=1e-12)
+
+
+def test_frequencies():
+    assert np.allclose(ob.rope_frequencies(4, 100.0).astype(float), [1.0, 0.1])
+    assert np.allclose(ob.rope_frequencies(4, 100.0, "linear", 4.0).astype(float), [0.25, 0.025])
+    # the slowest pair of a scaled base is the slowest pair interpolated
+    for n, by in ((32, 4.0), (128, 16.0)):
+        assert np.isclose(float(ob.rope_frequencies(n, 1e4, "base", by)[-1]),
+                          float(ob.rope_frequencies(n, 1e4, "linear", by)[-1]))
+        plain, parts = (ob.rope_frequencies(n, 1e4, kind, by, 4096).astype(float) for kind in ("none", "parts"))
+        turns = 4096 * plain / (2 * np.pi)
+        assert np.allclose(parts[turns >= 32], plain[turns >= 32]) and np.allclose(parts[turns <= 1], plain[turns <= 1] / by)
+        mid = (turns > 1) & (turns < 32)
+        assert ((parts < plain) & (parts > plain / by))[mid].all() and mid.any()
