@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libhb.so")
 
 SOURCES = ["api.cu", "kv_append.cu", "attention.cu", "linear.cu", "noalloc.cu", "selftest.cu",
            "step.cu", "pages.cu", "kv8_append.cu", "kv8_widen.cu", "attention8.cu",
-           "norm.cu", "rope.cu", "builder.cpp"]
+           "norm.cu", "rope.cu", "adapters.cu", "builder.cpp"]
 HEADERS = ["hb_internal.h", "ptx.cuh", "decode_body.cuh", "chunk_body.cuh", "decode_plan.h", "kv8.cuh",
            "decode8_body.cuh", "operands.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

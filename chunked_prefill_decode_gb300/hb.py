@@ -64,6 +64,7 @@ EXPORTED = (
     "hb_timing_durations", "hb_step_layout", "hb_step_slot_create", "hb_step_slot_destroy",
     "hb_step_slot_sync", "hb_step", "hb_kv8_append", "hb_kv8_plan", "hb_kv8_attention",
     "hb_pages_assign", "hb_pages_release", "hb_norm", "hb_rope_phases", "hb_rope",
+    "hb_adapters_plan", "hb_adapters",
 )
 
 LINEAR_STORE, LINEAR_GATED, LINEAR_RESIDUAL = 0, 1, 2
@@ -97,6 +98,11 @@ class HbRopeParams(ctypes.Structure):
 
 
 ROPE_SCALINGS = ("none", "linear", "base", "parts")
+
+
+class HbAdapterPool(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("num_adapters", "max_rank", "K", "N", "slices")]
+                + [(n, ctypes.c_void_p) for n in ("a", "b", "rank", "scale")])
 
 
 def lib_path() -> str:
@@ -176,6 +182,10 @@ def load():
     L.hb_rope_phases.argtypes = [i32, ctypes.c_double, i32] + [ctypes.c_double] * 4 + [vp]
     L.hb_rope.restype = ctypes.c_int
     L.hb_rope.argtypes = [P(HbBatch), P(HbRopeParams), vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp]
+    L.hb_adapters_plan.restype = ctypes.c_int
+    L.hb_adapters_plan.argtypes = [i32, i32, vp, vp, i32, i32, i32, vp, P(sz), vp, P(sz), vp]
+    L.hb_adapters.restype = ctypes.c_int
+    L.hb_adapters.argtypes = [P(HbAdapterPool), vp, vp, P(HbLinearOut), P(HbLinearOut), vp, vp]
     L.hb_launch_count.restype = i64
     L.hb_launch_count.argtypes = []
     L.hb_builder_create.restype = ctypes.c_int
@@ -1034,3 +1044,147 @@ def _refuse_rope(rope, d, ins, outs, pools):
         raise ValueError(f"rope's tensors are on cuda:{rope.device_index}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     raise ValueError("q, k and v: heads must be dense, and all tensors on one device")
+
+
+# ---------------------------------------------------------------- low-rank adapters
+def make_adapters(a, b, rank, scale, cols) -> HbAdapterPool:
+    """The pool of one projection's adapters: a [n, len(cols), max_rank, K] and b
+    [n, sum(cols), max_rank] bf16, rank [n] int32 and scale [n] fp32 on the device
+    (they may be written into, to bring adapters in and out; they live as long as
+    the pool); cols: the columns of the projection's destinations."""
+    cols = tuple(int(c) for c in cols)
+    if not 1 <= len(cols) <= 3 or min(cols) <= 0:
+        raise ValueError("cols must be one to three positive column counts")
+    if not isinstance(a, torch.Tensor) or a.dim() != 4 or a.shape[0] == 0:
+        raise ValueError("a must be a [num_adapters, destinations, max_rank, K] tensor")
+    n, _, r, k = a.shape
+    for name, t, dtype, shape in (("a", a, _BF16, (n, len(cols), r, k)), ("b", b, _BF16, (n, sum(cols), r)),
+                                  ("rank", rank, _I32, (n,)), ("scale", scale, _F32, (n,))):
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor")
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+        if max(t.shape) > _INT_MAX:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}: over 2^31 - 1")
+        if t.device != a.device:
+            raise ValueError(f"{name} is on {t.device}, a on {a.device}")
+    p = HbAdapterPool()
+    p.num_adapters, p.max_rank, p.K, p.N, p.slices = n, r, k, sum(cols), len(cols)
+    p.a, p.b, p.rank, p.scale = a.data_ptr(), b.data_ptr(), rank.data_ptr(), scale.data_ptr()
+    p.tensors, p.cols, p.device_index = (a, b, rank, scale), cols, a.get_device()
+    return p
+
+
+_ADAPTER_PLAN_BYTES = 80
+_ADAPTER_PLAN_INTS = struct.Struct("<Iiiiiiiiiiii")
+_ADAPTER_PLAN_SIZES = struct.Struct("<QQ")      # workspace, plan
+_ADAPTER_PLAN_SIZES_AT = 48 + 2 * 8
+
+
+def adapters_plan_header(plan):
+    """The header of an adapter plan (for tests and reports)."""
+    keys = ("magic", "num_seqs", "total_q", "num_adapters", "max_ranks", "num_sms", "num_segs", "num_idle_segs",
+            "num_rows", "max_seg_rows", "max_pieces")
+    out = dict(zip(keys, _ADAPTER_PLAN_INTS.unpack_from(plan)))
+    out["ws_total"], out["plan_bytes"] = _ADAPTER_PLAN_SIZES.unpack_from(plan, _ADAPTER_PLAN_SIZES_AT)
+    return out
+
+
+def adapters_plan_items(plan):
+    """(segments [n, 3]: adapter, first row, rows; row list) of an adapter plan."""
+    h = adapters_plan_header(plan)
+    n = h["num_segs"] + h["num_idle_segs"]
+    body = plan[_ADAPTER_PLAN_BYTES:h["plan_bytes"]].tobytes()
+    return np.frombuffer(body[:16 * n], np.int32).reshape(n, 4)[:, :3], np.frombuffer(body[16 * n:], np.int32)
+
+
+def hb_adapters_plan(pools, q_len, adapter, num_sms, total_q=None, workspace=None, plan=None, stream=None, upload=True):
+    """Sort a batch's tokens by adapter: q_len and each sequence's adapter (-1: none),
+    host arrays.  `pools`: a pool or several (the step's projections) of as many
+    adapters.  Returns (plan as a host uint8 array, device workspace), for
+    hb_adapters with any of them; as hb_plan."""
+    pools = (pools,) if isinstance(pools, HbAdapterPool) else tuple(pools)
+    if not pools or any(p.num_adapters != pools[0].num_adapters for p in pools):
+        raise ValueError("the pools of a plan have as many adapters")
+    ql = np.ascontiguousarray(q_len, dtype=np.int32)
+    of = np.ascontiguousarray(adapter, dtype=np.int32)
+    if ql.ndim != 1 or ql.shape != of.shape:
+        raise ValueError(f"q_len has shape {ql.shape}, adapter {of.shape}")
+    total = int(ql.sum(dtype=np.int64)) if total_q is None else int(total_q)
+    if total > _INT_MAX:
+        raise ValueError(f"{total} tokens: over 2^31 - 1")
+    ranks = max(p.slices * p.max_rank for p in pools)
+
+    def call(plan, workspace):
+        pb = ctypes.c_size_t(plan.nbytes if plan is not None else 0)
+        wb = ctypes.c_size_t(workspace.numel() if workspace is not None else 0)
+        return load().hb_adapters_plan(
+            len(ql), total, _ptr(ql), _ptr(of), pools[0].num_adapters, ranks, int(num_sms), _ptr(plan),
+            ctypes.byref(pb), _ptr(workspace), ctypes.byref(wb), _stream(stream) if workspace is not None else None), \
+            pb.value, wb.value
+    if plan is not None and (workspace is not None or not upload):
+        st, _, _ = call(plan, workspace if upload else None)
+        if st == 0:
+            return plan, workspace if upload else None
+        if st != 4:   # anything but HB_ERR_WORKSPACE
+            _check(st)
+    st, need_p, need_w = call(None, None)
+    _check(st)
+    if plan is None or plan.nbytes < need_p:
+        plan = np.zeros(need_p, dtype=np.uint8)
+    if not upload:
+        workspace = None
+    elif workspace is None or workspace.numel() < need_w:
+        workspace = torch.empty(max(need_w, 256), dtype=torch.uint8, device="cuda")
+    _check(call(plan, workspace)[0])
+    return plan, workspace
+
+
+def hb_adapters(pool, plan, x, y, out, workspace, stream=None):
+    """out_i = y_i + scale (x A_i^T) B_i^T with each token's own adapter: x [total_q,
+    K], y and out lists of [total_q, cols_i] tensors (out may be y: in place)."""
+    if (not isinstance(plan, np.ndarray) or plan.dtype != np.uint8 or plan.nbytes < _ADAPTER_PLAN_BYTES
+            or not plan.flags.c_contiguous):
+        raise ValueError("plan must be the uint8 array that hb_adapters_plan returned")
+    need, size = _ADAPTER_PLAN_SIZES.unpack_from(plan, _ADAPTER_PLAN_SIZES_AT)
+    if plan.nbytes < size:
+        raise ValueError(f"plan has {plan.nbytes} bytes of the {size} that hb_adapters_plan wrote")
+    if not isinstance(pool, HbAdapterPool) or not hasattr(pool, "cols"):
+        raise ValueError("pool must be what make_adapters returned")
+    rows, cols = _ADAPTER_PLAN_INTS.unpack_from(plan)[2], pool.cols
+    src, dst = HbLinearOut(), HbLinearOut()
+    try:
+        dev = x.get_device()
+        ok = (x.dtype is _BF16 and x.shape == (rows, pool.K) and x.is_contiguous() and dev >= 0
+              and dev == pool.device_index and dev == _current_device() and len(y) == len(out) == len(cols)
+              and workspace.dtype is torch.uint8 and workspace.dim() == 1 and workspace.is_contiguous()
+              and workspace.numel() >= need and workspace.get_device() == dev)
+        for i, n in enumerate(cols):
+            s, d = y[i], out[i]
+            ok = (ok and s.dtype is _BF16 and s.shape == (rows, n) and s.is_contiguous() and s.get_device() == dev
+                  and (d is s or (d.dtype is _BF16 and d.shape == (rows, n) and d.is_contiguous()
+                                  and d.get_device() == dev)))
+            src.y[i], src.cols[i], dst.y[i], dst.cols[i] = s.data_ptr(), n, d.data_ptr(), n
+    except (AttributeError, TypeError, IndexError):
+        ok = False
+    if not ok:
+        for name, ts in (("y", y), ("out", out)):
+            if not isinstance(ts, (list, tuple)) or len(ts) != len(cols):
+                raise ValueError(f"{name} must be a list of {len(cols)} tensors")
+        if isinstance(workspace, torch.Tensor) and workspace.numel() < need:
+            raise ValueError(f"workspace has {workspace.numel()} bytes, the plan needs {need}")
+        _refuse(("x", x, _BF16, (rows, pool.K)),
+                *((f"{name}[{i}]", t, _BF16, (rows, n)) for name, ts in (("y", y), ("out", out))
+                  for i, (t, n) in enumerate(zip(ts, cols))),
+                ("workspace", workspace, torch.uint8, (_numel(workspace),)), ("the pool", pool.tensors[0], _BF16,
+                                                                             pool.tensors[0].shape))
+    if rows == 0:
+        return
+    try:
+        at = ctypes.byref(_CHAR.from_buffer(plan))
+    except TypeError:                                # (read-only)
+        at = plan.ctypes.data
+    st = (_lib or load()).hb_adapters(ctypes.byref(pool), at, x.data_ptr(), ctypes.byref(src), ctypes.byref(dst),
+                                      workspace.data_ptr(), _raw_stream(stream, dev))
+    if st:
+        _check(st)

@@ -652,6 +652,67 @@ hb_status hb_rope(const hb_batch* batch, const hb_rope_params* rope, const void*
                   void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection.  (The pages
+ * serve one model to all requests; an adapter per request is what lets a
+ * hybrid batch serve many models that share its weights.)  With adapter a of
+ * the sequence that token t belongs to, for each destination i of hb_linear:
+ *   out_i[t] = y_i[t] + scale[a] * (x[t] A_{a,i}^T) B_{a,i}^T
+ * A pool holds the adapters of one projection:
+ *   a      device, [num_adapters, slices, max_rank, K] bf16; slices = the
+ *          projection's destinations (1 to 3), each with ranks of its own
+ *   b      device, [num_adapters, N, max_rank] bf16, its rows as the
+ *          projection's weight rows (destination by destination)
+ *   rank   device, [num_adapters] int32: the ranks in use, read as if held to
+ *          [0, max_rank]; what stands in a and b past them is not used
+ *   scale  device, [num_adapters] fp32
+ * max_rank is a multiple of 8, at most 128; K and each destination's columns are
+ * multiples of 8.
+ * ------------------------------------------------------------------------- */
+typedef struct hb_adapter_pool {
+  int32_t num_adapters, max_rank;
+  int32_t K, N;            /* columns of x; columns of all destinations        */
+  int32_t slices;          /* destinations                                     */
+  const void *a, *b;       /* 16-byte aligned                                  */
+  const int32_t* rank;
+  const float* scale;
+} hb_adapter_pool;
+
+/*
+ * Plan (host).  Sorts the batch's tokens by adapter: needs the host copies of
+ * q_len (>= 0) and of each sequence's adapter (-1: none), and serves every pool
+ * of num_adapters adapters with at most max_ranks = slices * max_rank ranks (all
+ * projections of all layers of a step).  total_q: rows of x, y and out, at least
+ * the sum of q_len; rows behind the last sequence are neither read nor written.
+ * Buffers, sizes and upload as with hb_plan (h_plan must stay unchanged until
+ * its copy has completed; a workspace must not be shared by calls in flight at
+ * once; a captured hb_adapters reads the plan in its workspace when it is
+ * replayed, so that workspace takes no other plan meanwhile).  The workspace
+ * also holds x A^T in fp32, up to 16 parts of it (4 * max_ranks bytes per row
+ * and part; more parts where rows are few).
+ * Errors: HB_ERR_SHAPE for lengths or adapters that break the rules,
+ * HB_ERR_WORKSPACE if a buffer is too small.
+ */
+hb_status hb_adapters_plan(int32_t num_seqs, int32_t total_q, const int32_t* h_q_len,
+                           const int32_t* h_adapter, int32_t num_adapters, int32_t max_ranks,
+                           int32_t num_sms, void* h_plan, size_t* plan_bytes, void* d_workspace,
+                           size_t* workspace_bytes, void* stream);
+
+/*
+ *   x        device, [total_q, K] bf16 (the projection's input), 16-byte aligned
+ *   y, out   device, [total_q, cols[i]] bf16 each, columns alike; out may be y
+ *            (in place, e.g. hb_linear's destinations), or arrays that overlap
+ *            no other operand: rows whose sequence has no adapter are then
+ *            copied.  out must not overlap x.
+ * x A^T is summed in fp32 and enters the second product in two bf16 terms (16
+ * bits); the sum with y is rounded once.  Two launches.  Errors:
+ * HB_ERR_WORKSPACE if h_plan does not match the pool, HB_ERR_INVALID_ARG for
+ * operands that overlap, others as hb_linear.
+ */
+hb_status hb_adapters(const hb_adapter_pool* pool, const void* h_plan, const void* x,
+                      const hb_linear_out* y, const hb_linear_out* out, void* d_workspace,
+                      void* stream);
+
+/* ---------------------------------------------------------------------------
  * Instrumentation.  When enabled, every kernel launch of this library is
  * bracketed by CUDA events recorded on its launch stream.
  *   kernel ids: 0 = kv append (either cache), 1 = attention (decode and chunk

@@ -60,3 +60,24 @@ def rotate(x, angle, interleaved=False, factor=1.0) -> np.ndarray:
         out[..., a] = x[..., a] * c[..., i] - x[..., b] * s[..., i]
         out[..., b] = x[..., a] * s[..., i] + x[..., b] * c[..., i]
     return out
+
+
+def adapters(x, ys, q_len, adapter, a, b, rank, scale):
+    """The outputs of a shared projection (ys, one array per destination) with
+    each sequence's own low-rank product added: a [n, destinations, R, K], b [n,
+    sum of columns, R].  Also the sums of the products' absolute values."""
+    x = np.asarray(x, np.float64)
+    outs = [np.asarray(y, np.float64).copy() for y in ys]
+    sizes = [np.zeros_like(o) for o in outs]
+    t = 0
+    for n, i in zip(q_len, adapter):
+        if i >= 0:
+            r, col = int(rank[i]), 0
+            for j, out in enumerate(outs):
+                w = b[i, col:col + out.shape[1], :r].astype(np.float64)
+                low = a[i, j, :r].astype(np.float64)
+                out[t:t + n] += float(scale[i]) * ((x[t:t + n] @ low.T) @ w.T)
+                sizes[j][t:t + n] = abs(float(scale[i])) * ((np.abs(x[t:t + n]) @ np.abs(low).T) @ np.abs(w).T)
+                col += out.shape[1]
+        t += n
+    return outs, sizes

@@ -63,3 +63,17 @@ def test_frequencies():
         assert np.allclose(parts[turns >= 32], plain[turns >= 32]) and np.allclose(parts[turns <= 1], plain[turns <= 1] / by)
         mid = (turns > 1) & (turns < 32)
         assert ((parts < plain) & (parts > plain / by))[mid].all() and mid.any()
+
+
+def test_adapters_are_a_change_of_the_weights():
+    rng = np.random.default_rng(3)
+    x, w = rng.standard_normal((7, 12)), rng.standard_normal((10, 12))
+    a, b = rng.standard_normal((2, 2, 3, 12)), rng.standard_normal((2, 10, 3))
+    y = x @ w.T
+    outs, _ = ob.adapters(x, [y[:, :6], y[:, 6:]], [2, 1, 4], [1, -1, 0], a, b, [3, 2], [0.5, -2.0])
+    got = np.concatenate(outs, 1)
+    assert np.array_equal(got[2], y[2])
+    for rows, i, r, s in ((slice(0, 2), 1, 2, -2.0), (slice(3, 7), 0, 3, 0.5)):
+        for j, cols in enumerate((slice(0, 6), slice(6, 10))):
+            tuned = w[cols] + s * b[i, cols, :r] @ a[i, j, :r]
+            assert np.allclose(got[rows, cols], x[rows] @ tuned.T, rtol=1e-12, atol=1e-12)
