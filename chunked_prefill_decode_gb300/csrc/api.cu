@@ -404,6 +404,17 @@ hb_status internal_decode_maps(const hb_batch* b, int kvhb, const void* k_cache,
   return encode_map(vmap, v_cache, 4, dims, strides, box, "decode V");
 }
 
+// A dense [rows, cols] bf16 array in boxes of 64 columns (128-byte swizzle).
+hb_status internal_map_2d(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int box_rows,
+                          const char* what) {
+  hb_status s = get_encoder();
+  if (s != HB_OK) return s;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  return encode_map(map, base, 2, dims, strides, box, what);
+}
+
 void internal_count_launch() { g_launches.fetch_add(1); }
 
 // ---------------------------------------------------------------- launch order

@@ -1075,27 +1075,28 @@ def make_adapters(a, b, rank, scale, cols) -> HbAdapterPool:
     return p
 
 
-_ADAPTER_PLAN_BYTES = 80
-_ADAPTER_PLAN_INTS = struct.Struct("<Iiiiiiiiiiii")
+_ADAPTER_PLAN_BYTES = 88
+_ADAPTER_PLAN_INTS = struct.Struct("<I11i")
 _ADAPTER_PLAN_SIZES = struct.Struct("<QQ")      # workspace, plan
-_ADAPTER_PLAN_SIZES_AT = 48 + 2 * 8
+_ADAPTER_PLAN_SIZES_AT = 48 + 3 * 8
 
 
 def adapters_plan_header(plan):
     """The header of an adapter plan (for tests and reports)."""
-    keys = ("magic", "num_seqs", "total_q", "num_adapters", "max_ranks", "num_sms", "num_segs", "num_idle_segs",
-            "num_rows", "max_seg_rows", "max_pieces")
+    keys = ("magic", "num_seqs", "total_q", "num_adapters", "max_ranks", "num_sms", "num_long", "num_short",
+            "num_idle", "long_rows", "short_rows", "short_pieces")
     out = dict(zip(keys, _ADAPTER_PLAN_INTS.unpack_from(plan)))
     out["ws_total"], out["plan_bytes"] = _ADAPTER_PLAN_SIZES.unpack_from(plan, _ADAPTER_PLAN_SIZES_AT)
     return out
 
 
 def adapters_plan_items(plan):
-    """(segments [n, 3]: adapter, first row, rows; row list) of an adapter plan."""
+    """(segments [n, 4]: adapter, first entry of the row list, rows, first token of a
+    long tile or -1; row list) of an adapter plan."""
     h = adapters_plan_header(plan)
-    n = h["num_segs"] + h["num_idle_segs"]
+    n = h["num_long"] + h["num_short"] + h["num_idle"]
     body = plan[_ADAPTER_PLAN_BYTES:h["plan_bytes"]].tobytes()
-    return np.frombuffer(body[:16 * n], np.int32).reshape(n, 4)[:, :3], np.frombuffer(body[16 * n:], np.int32)
+    return np.frombuffer(body[:16 * n], np.int32).reshape(n, 4), np.frombuffer(body[16 * n:], np.int32)
 
 
 def hb_adapters_plan(pools, q_len, adapter, num_sms, total_q=None, workspace=None, plan=None, stream=None, upload=True):

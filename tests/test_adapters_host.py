@@ -33,28 +33,34 @@ def test_a_plan_covers_every_token_once(seed):
     segs, rows = hb.adapters_plan_items(plan)
     token = np.repeat(of, q)
     assert sorted(rows) == list(range(len(token)))
-    assert h["num_rows"] == (token >= 0).sum() and h["total_q"] == len(token) + 3
-    used = np.zeros(len(rows), int)
-    for i, (a, first, count) in enumerate(segs):
-        assert 1 <= count <= 64 and (token[rows[first:first + count]] == a).all() and (a < 0) == (i >= h["num_segs"])
-        assert (np.diff(rows[first:first + count]) > 0).all()
-        used[first:first + count] += 1
-    assert (used == 1).all()
-    live = segs[:h["num_segs"]]
-    assert (np.diff(live[:, 2]) <= 0).all() and h["max_seg_rows"] == (live[0, 2] if len(live) else 0)
-    # segments of an adapter are whole 16-row tiles but for one, and as few as can be
+    assert h["total_q"] == len(token) + 3 and h["long_rows"] + h["short_rows"] == (token >= 0).sum()
+    long, short, idle = np.split(segs, [h["num_long"], h["num_long"] + h["num_short"]])
+    assert h["num_idle"] == len(idle) and (idle[:, 0] == -1).all() and (short[:, 0] >= 0).all()
+    # segment after segment takes the row list
+    assert (segs[:, 1] == np.cumsum(segs[:, 2]) - segs[:, 2]).all() and segs[:, 2].sum() == len(rows)
+    for a, first, count, tok in segs:
+        mine = rows[first:first + count]
+        assert (token[mine] == a).all() and (np.diff(mine) > 0).all()
+        assert 1 <= count <= (128 if tok >= 0 else 16)
+        if tok >= 0:
+            assert (mine == tok + np.arange(count)).all()
+    # long tiles are the runs of 64 neighbours or more, short segments as few as can be
+    edges = np.flatnonzero(np.diff(np.concatenate([[-2], token, [-2]])))
+    runs = [(int(token[i]), j - i) for i, j in zip(edges, edges[1:])]
+    assert sum(n for a, n in runs if a >= 0 and n >= 64) == h["long_rows"]
+    assert sum(-(-n // 128) for a, n in runs if a >= 0 and n >= 64) == h["num_long"]
     for a in range(n):
-        count = (token == a).sum()
-        mine = live[live[:, 0] == a, 2]
-        assert len(mine) == -(-count // 64) and (mine % 16 != 0).sum() <= 1
+        count = sum(m for b, m in runs if b == a and m < 64)
+        assert (short[:, 0] == a).sum() == -(-count // 16)
 
 
 def test_more_parts_of_k_where_rows_are_few():
     hb = lib()
-    few, many = (hb.adapters_plan_header(plan_of(hb, [1] * n, [0] * n)) for n in (1, 64 * 400))
-    assert few["max_pieces"] == 16 and many["max_pieces"] == 1
-    for h in (few, many):
-        assert h["ws_total"] >= h["max_pieces"] * h["num_rows"] * 16 * 4
+    few, many, long = (hb.adapters_plan_header(plan_of(hb, q, np.arange(len(q)) % 2))
+                       for q in ([1], [1] * 10000, [128]))
+    assert few["short_pieces"] == 16 and many["short_pieces"] == 1 and long["num_long"] == 1
+    for h in (few, many, long):
+        assert h["ws_total"] >= (h["short_pieces"] * h["short_rows"] + 128 * h["num_long"]) * 16 * 4
 
 
 def test_the_plan_serves_several_pools():
@@ -162,7 +168,7 @@ def test_tensors_are_checked_by_name():
     plan, _ = hb.hb_adapters_plan(p, [3, 4], [0, -1], 152, upload=False)
     x, y = z(7, 64), z(7, 64)
     ws = torch.zeros(1 << 20, dtype=torch.uint8)
-    for at, junk, name in [(0, hb.HbAdapterPool(), "pool"), (1, plan[:-1], "plan"), (1, plan[:79], "plan"), (1, None, "plan"),
+    for at, junk, name in [(0, hb.HbAdapterPool(), "pool"), (1, plan[:-1], "plan"), (1, plan[:87], "plan"), (1, None, "plan"),
                            (1, np.repeat(plan, 2)[::2], "plan"), (2, z(6, 64), "x has shape"), (2, [1], "x must be"),
                            (3, y, "y must be a list"), (3, [y, y], "y must be a list"), (3, [z(7, 32)], "y.0. has shape"),
                            (4, [z(7, 64, dtype=torch.float32)], "out.0. must be"), (4, [], "out must be a list"),
