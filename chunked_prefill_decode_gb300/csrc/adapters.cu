@@ -39,6 +39,7 @@
 #include <algorithm>
 #include <climits>
 #include <cstring>
+#include <mutex>
 #include <vector>
 
 #include "adapters.h"
@@ -350,22 +351,59 @@ cudaError_t launch_expand_short(AdapterParams p, int num_sms, cudaStream_t st) {
   return launch_serialized(expand_short_kernel, (unsigned)(p.num_segs * chunks), kAdThreads, 0, st, p);
 }
 
-cudaError_t launch_shrink_long(const AdapterParams& p, const CUtensorMap& xmap, const CUtensorMap& amap, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(shrink_long_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLsSmem);
-  if (e != cudaSuccess) return e;
+cudaLaunchConfig_t shrink_long_config(int ctas, int pieces, cudaStream_t st, cudaLaunchAttribute (&attr)[2]) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.num_segs * p.groups * p.pieces);
+  cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kLsThreads);
   cfg.dynamicSmemBytes = kLsSmem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)p.pieces;
+  attr[1].val.clusterDim.x = (unsigned)pieces;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  return cfg;
+}
+
+// Clusters of 1 .. kLsMaxPieces CTAs that the device holds at a time (a cluster's
+// CTAs sit in one group of SMs, so these are fewer than SMs / CTAs); found once
+// per device.
+struct Clusters {
+  int fit[kLsMaxPieces + 1];
+};
+cudaError_t clusters_of_device(const Clusters** out) {
+  static std::mutex mu;
+  static Clusters per_device[64];
+  static bool ready[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!ready[dev]) {
+    e = cudaFuncSetAttribute(shrink_long_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLsSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(shrink_long_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    for (int n = 1; e == cudaSuccess && n <= kLsMaxPieces; ++n) {
+      cudaLaunchAttribute attr[2];
+      cudaLaunchConfig_t cfg = shrink_long_config(n, n, nullptr, attr);
+      cfg.attrs = attr + 1;   // (the cluster's size alone)
+      cfg.numAttrs = 1;
+      int fit = 0;
+      e = cudaOccupancyMaxActiveClusters(&fit, shrink_long_kernel, &cfg);
+      per_device[dev].fit[n] = fit;
+    }
+    if (e != cudaSuccess) return e;
+    ready[dev] = true;
+  }
+  *out = &per_device[dev];
+  return cudaSuccess;
+}
+
+cudaError_t launch_shrink_long(const AdapterParams& p, const CUtensorMap& xmap, const CUtensorMap& amap, cudaStream_t st) {
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = shrink_long_config(p.num_segs * p.groups * p.pieces, p.pieces, st, attr);
   return cudaLaunchKernelEx(&cfg, shrink_long_kernel, p, xmap, amap);
 }
 
@@ -606,12 +644,18 @@ extern "C" hb_status hb_adapters(const hb_adapter_pool* pool, const void* h_plan
       const int boxes = slices * ((R + 15) / 16);
       lo.groups = (boxes + kLsMaxBoxes - 1) / kLsMaxBoxes;
       lo.boxes = (boxes + lo.groups - 1) / lo.groups;
-      lo.stages = std::min(kLsMaxStages, kLsRingBytes / (kLsXBytes + lo.boxes * kLsBoxBytes));
       const int64_t ctas = (int64_t)h.num_long * lo.groups;
+      const Clusters* clusters = nullptr;
+      const cudaError_t e = clusters_of_device(&clusters);
+      if (e != cudaSuccess) return internal_failf(HB_ERR_CUDA, "adapter clusters: %s", cudaGetErrorString(e));
       int best = 1;
       int64_t best_cost = INT64_MAX;
+      // (a CTA's time is that of its units, twice as long with two on an SM, and of
+      // about 16 more for its start, the sums' exchange and its end)
       for (int n = 1; n <= std::min(kLsMaxPieces, units); ++n) {
-        const int64_t cost = (ctas * n + h.num_sms - 1) / h.num_sms * ((units + n - 1) / n + 8);
+        if (clusters->fit[n] == 0) continue;
+        const int64_t waves = (ctas + clusters->fit[n] - 1) / clusters->fit[n];
+        const int64_t cost = waves * ((units + n - 1) / n * (ctas * n > h.num_sms ? 2 : 1) + 16);
         if (cost < best_cost) best = n, best_cost = cost;
       }
       cut_k(lo, best);

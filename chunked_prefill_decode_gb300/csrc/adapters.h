@@ -52,7 +52,7 @@ struct AdapterParams {
   // long
   uint16_t* terms;                     // [2 terms, num_segs * 128, h_cols] of h, scale included
   int32_t h_cols, h_slice;             // h_slice: a destination's ranks, whole steps of 16
-  int32_t stages, boxes;               // of the shrink ring; 16-rank boxes of a CTA (at most)
+  int32_t boxes;                       // 16-rank boxes of a shrink CTA (at most)
   int* dev_error;
 };
 

@@ -27,22 +27,23 @@ namespace hb {
 constexpr int kLsThreads = 192;               // warp 0 TMA, warp 1 MMA, warps 2-5 epilogue
 constexpr int kLsXBytes = kAdTileRows * 128;  // a 64-wide K block of the x tile
 constexpr int kLsBoxBytes = 16 * 128;         // and of 16 ranks
-constexpr int kLsMaxBoxes = 16;               // N 256 (at most)
-constexpr int kLsMaxStages = 8;
-constexpr int kLsMaxPieces = 8;               // CTAs of a cluster
-constexpr int kLsRingBytes = 200 * 1024;
+constexpr int kLsMaxBoxes = 12;               // N 192 (at most)
+constexpr int kLsMaxStages = 6;
+constexpr int kLsMaxPieces = 16;              // CTAs of a cluster (at most; more than 8 only where they fit)
+constexpr int kLsRingBytes = 104 * 1024;      // two CTAs on an SM
 constexpr int kLsBarBytes = (2 * kLsMaxStages + 1) * 8 + 24;
 constexpr size_t kLsSmem = kLsRingBytes + kLsBarBytes + 1024;
 static_assert(kLsMaxBoxes * 16 * kAdTileRows * 4 <= kLsRingBytes, "the sums fit the ring");
-static_assert(kLsSmem <= 227 * 1024, "shrink smem");
+static_assert(2 * (kLsXBytes + kLsMaxBoxes * kLsBoxBytes) <= kLsRingBytes, "two stages at least");
+static_assert(2 * (kLsSmem + 1024) <= 228 * 1024, "shrink smem");
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
   return v;
 }
 
-__global__ void __launch_bounds__(kLsThreads, 1)
+__global__ void __launch_bounds__(kLsThreads, 2)
     shrink_long_kernel(const AdapterParams p, const __grid_constant__ CUtensorMap xmap,
                        const __grid_constant__ CUtensorMap amap) {
   extern __shared__ uint8_t s_raw[];
@@ -57,7 +58,7 @@ __global__ void __launch_bounds__(kLsThreads, 1)
   const int box0 = group * p.boxes, boxes = min(per_slice * p.slices - box0, p.boxes);
   if (boxes <= 0) return;                               // (the whole cluster)
   uint8_t* smem = s_raw + ((1024u - (smem_u32(s_raw) & 1023u)) & 1023u);
-  const int stage_bytes = kLsXBytes + p.boxes * kLsBoxBytes;
+  const int stage_bytes = kLsXBytes + boxes * kLsBoxBytes, stages = min(kLsMaxStages, kLsRingBytes / stage_bytes);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kLsRingBytes);
   uint64_t* empty = full + kLsMaxStages;
   uint64_t* done = empty + kLsMaxStages;
@@ -65,10 +66,11 @@ __global__ void __launch_bounds__(kLsThreads, 1)
   int* abort_i = reinterpret_cast<int*>(tmem_holder + 2);
   volatile int* abort_flag = abort_i;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float scale = __ldg(p.scale + seg.adapter);
   uint32_t tmem_cols = 32;
   while (tmem_cols < (uint32_t)boxes * 16u) tmem_cols *= 2;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -97,8 +99,8 @@ __global__ void __launch_bounds__(kLsThreads, 1)
     fence_proxy_async_global();
     int i = 0;
     for (; i < n; ++i) {
-      const int s = i % p.stages;
-      if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ((i / p.stages) & 1) ^ 1, abort_flag))) break;
+      const int s = i % stages;
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ((i / stages) & 1) ^ 1, abort_flag))) break;
       uint8_t* st = smem + s * stage_bytes;
       if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(kLsXBytes + boxes * kLsBoxBytes));
       __syncwarp();
@@ -107,13 +109,13 @@ __global__ void __launch_bounds__(kLsThreads, 1)
       __syncwarp();
     }
     // before the ring is used again or the CTA exits, what was issued has landed
-    for (int s = 0; s < p.stages && s < i; ++s) drain_wait(&full[s], ((i - 1 - s) / p.stages) & 1, abort_flag);
+    for (int s = 0; s < stages && s < i; ++s) drain_wait(&full[s], ((i - 1 - s) / stages) & 1, abort_flag);
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t idesc = idesc_bf16_f32(kAdTileRows, (uint32_t)boxes * 16u, false);
       for (int i = 0; i < n; ++i) {
-        const int s = i % p.stages;
-        if (!mbar_wait(&full[s], (i / p.stages) & 1, abort_flag)) break;
+        const int s = i % stages;
+        if (!mbar_wait(&full[s], (i / stages) & 1, abort_flag)) break;
         tc_fence_after_sync();
         const uint32_t a = smem_u32(smem + s * stage_bytes), b = a + kLsXBytes;
 #pragma unroll
@@ -146,31 +148,38 @@ __global__ void __launch_bounds__(kLsThreads, 1)
   cluster_sync_all();
   if (warp >= 2) {
     const int row = (warp & 3) * 32 + lane;
-    const float scale = __ldg(p.scale + seg.adapter);
     const uint32_t mine = smem_u32(smem) + (uint32_t)row * 4u;
-    // boxes of ranks in turn; a thread has a row's 16
-    for (int j = piece; j < boxes; j += p.pieces) {
-      float v[16];
+    // eight ranks at a time, in turn among the CTAs; a thread has a row's eight
+    for (int j = piece; j < 2 * boxes; j += p.pieces) {
+      const uint32_t at_j = (uint32_t)(j * 8 * kAdTileRows) * 4u;
+      float v[8];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = 0.f;
-      for (int q = 0; q < p.pieces; ++q) {
-        const uint32_t src = mapa_shared(mine, (uint32_t)q) + (uint32_t)(j * 16 * kAdTileRows) * 4u;
+      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+      // (eight pieces' loads on their way at a time)
+      for (int q0 = 0; q0 < p.pieces; q0 += 8) {
+        float o[8][8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] += ld_cluster_f32(src + (uint32_t)(e * kAdTileRows) * 4u);
+        for (int q = 0; q < 8; ++q) {
+          const uint32_t src = mapa_shared(mine, (uint32_t)min(q0 + q, p.pieces - 1)) + at_j;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            o[q][e] = q0 + q < p.pieces ? ld_cluster_f32(src + (uint32_t)(e * kAdTileRows) * 4u) : 0.f;
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += o[q][e];
       }
-      const int b = box0 + j, r0 = b % per_slice * 16;
-      uint32_t hi[8], lo[8];
+      const int b = box0 + (j >> 1), r0 = b % per_slice * 16 + (j & 1) * 8;
+      uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)   // (a rank that the adapter does not have may have met an infinity of x)
+      for (int e = 0; e < 4; ++e)   // (a rank that the adapter does not have may have met an infinity of x)
         two_terms(r0 + 2 * e < rank ? v[2 * e] * scale : 0.f, r0 + 2 * e + 1 < rank ? v[2 * e + 1] * scale : 0.f,
                   hi[e], lo[e]);
-      const int64_t to = ((int64_t)tile * kAdTileRows + row) * p.h_cols + b / per_slice * p.h_slice + r0;
-      uint4* dst = reinterpret_cast<uint4*>(p.terms + to);
-      dst[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      dst[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-      dst = reinterpret_cast<uint4*>(p.terms + (int64_t)p.num_segs * kAdTileRows * p.h_cols + to);
-      dst[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      dst[1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+      uint16_t* dst = p.terms + ((int64_t)tile * kAdTileRows + row) * p.h_cols + b / per_slice * p.h_slice + r0;
+      *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      dst += (int64_t)p.num_segs * kAdTileRows * p.h_cols;
+      *reinterpret_cast<uint4*>(dst) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
   }
   __syncwarp();
@@ -189,9 +198,11 @@ __global__ void __launch_bounds__(kLsThreads, 1)
 // of them.  Warp 0 brings a block's y and rows of B (and, where a tile or a
 // destination begins, the two terms of h) by TMA; warp 1 multiplies (tcgen05,
 // M 128, N 128, two terms; accumulators of two blocks in tensor memory); warps
-// 2-5 (thread = row) add y to the sums in shared memory and write the rows out
-// from there, 128 bytes at a time, only those of the tile.
-constexpr int kLeThreads = 192;
+// 2-9 (thread = row, four warps to each half of the columns) add y to the sums in
+// shared memory and write the rows out from there, 128 bytes at a time, only those
+// of the tile.
+constexpr int kLeThreads = 320;
+constexpr int kLeEpilogueWarps = 8;
 constexpr int kLeCols = 128;                            // columns of a block
 constexpr int kLePanel = 128 * 128;                     // bytes: 128 rows of 64 bf16 columns
 constexpr int kLeMaxStages = 4;
@@ -249,7 +260,7 @@ __global__ void __launch_bounds__(kLeThreads, 1)
   const int stage_bytes = (cfg.panels + 2) * kLePanel;
   uint8_t* ring = smem + cfg.hbufs * h_bytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kLeBytes);
-  uint64_t* empty = full + kLeMaxStages;     // the block's MMAs and the four epilogue warps
+  uint64_t* empty = full + kLeMaxStages;     // the block's MMAs and the epilogue warps
   uint64_t* h_full = empty + kLeMaxStages;   // [2]
   uint64_t* h_empty = h_full + 2;            // [2]
   uint64_t* acc_full = h_empty + 2;          // [2]
@@ -263,13 +274,13 @@ __global__ void __launch_bounds__(kLeThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < cfg.stages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1 + 4);
+      mbar_init(&empty[s], 1 + kLeEpilogueWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&h_full[i], 1);
       mbar_init(&h_empty[i], 1);
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
+      mbar_init(&acc_empty[i], kLeEpilogueWarps);
     }
     mbar_init(done, 1);
     *abort_i = 0;
@@ -381,7 +392,7 @@ __global__ void __launch_bounds__(kLeThreads, 1)
       drain_wait(done, 0u, abort_flag);
     }
   } else {
-    const int wq = warp & 3, row = wq * 32 + lane;
+    const int wq = warp & 3, row = wq * 32 + lane, half = warp >= 6 ? 1 : 0;
     int tile = -1, rank = 0, rows = 0;
     int64_t token = 0;
     for (int i = i0; i < i1; ++i) {
@@ -398,43 +409,37 @@ __global__ void __launch_bounds__(kLeThreads, 1)
                                        mbar_wait(&acc_full[buf], (g >> 1) & 1, abort_flag)))
         break;
       tc_fence_after_sync();
-      uint8_t* st = ring + s * stage_bytes;
+      uint8_t* panel = ring + s * stage_bytes + half * kLePanel;
       if (rank > 0) {       // (without: y as it is)
-#pragma unroll 1
-        for (int c = 0; c < kLeCols / 32; ++c) {
-          uint32_t v[32];
-          tmem_ld32(tmem + ((uint32_t)(wq * 32) << 16) + (uint32_t)(buf * kLeCols + c * 32), v);
-          tmem_ld_wait();
-          uint8_t* line = st + (c >> 1) * kLePanel + row * 128;
+        uint32_t v[64];
+        const uint32_t acc = tmem + ((uint32_t)(wq * 32) << 16) + (uint32_t)(buf * kLeCols + half * 64);
+        tmem_ld32(acc, v);
+        tmem_ld32(acc + 32, v + 32);
+        tmem_ld_wait();
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint4* to = reinterpret_cast<uint4*>(line + (((c & 1) * 4 + q) ^ (row & 7)) * 16);
-            const uint4 y = *to;
-            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-            uint32_t o[4];
+        for (int q = 0; q < 8; ++q) {
+          uint4* to = reinterpret_cast<uint4*>(panel + row * 128 + (q ^ (row & 7)) * 16);
+          const uint4 y = *to;
+          const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+          uint32_t o[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              o[e] = pack_bf16x2(bf16lo_to_f32(w[e]) + __uint_as_float(v[q * 8 + 2 * e]),
-                                 bf16hi_to_f32(w[e]) + __uint_as_float(v[q * 8 + 2 * e + 1]));
-            *to = make_uint4(o[0], o[1], o[2], o[3]);
-          }
+          for (int e = 0; e < 4; ++e)
+            o[e] = pack_bf16x2(bf16lo_to_f32(w[e]) + __uint_as_float(v[q * 8 + 2 * e]),
+                               bf16hi_to_f32(w[e]) + __uint_as_float(v[q * 8 + 2 * e + 1]));
+          *to = make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[buf]);
       // the warp's 32 rows, 8 lanes to 128 bytes
-      const int cols = p.cols[blk.slice];
-      uint16_t* out = p.out[blk.slice] + blk.col;
+      const int cols = p.cols[blk.slice], col = blk.col + half * 64 + (lane & 7) * 8;
+      uint16_t* out = p.out[blk.slice] + col;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int col = half * 64 + (lane & 7) * 8;
-#pragma unroll
-        for (int r8 = 0; r8 < 8; ++r8) {
-          const int r = wq * 32 + r8 * 4 + (lane >> 3);
-          const uint4 v = *reinterpret_cast<const uint4*>(st + half * kLePanel + r * 128 + ((lane & 7) ^ (r & 7)) * 16);
-          if (r < rows && blk.col + col < cols) *reinterpret_cast<uint4*>(out + (token + r) * cols + col) = v;
-        }
+      for (int r8 = 0; r8 < 8; ++r8) {
+        const int r = wq * 32 + r8 * 4 + (lane >> 3);
+        const uint4 v = *reinterpret_cast<const uint4*>(panel + r * 128 + ((lane & 7) ^ (r & 7)) * 16);
+        if (r < rows && col < cols) *reinterpret_cast<uint4*>(out + (token + r) * cols) = v;
       }
       // the sums stood where the next copy lands
       fence_async_shared();
