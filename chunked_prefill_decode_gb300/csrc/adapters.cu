@@ -60,7 +60,7 @@ void internal_note_other_launch(void* stream);
 namespace {
 
 constexpr int kAdThreads = 256, kAdWarps = kAdThreads / 32;
-constexpr int kAdLongRun = 64;          // neighbouring rows of an adapter from which they are long tiles
+constexpr int kAdLongRun = 128;         // neighbouring rows of an adapter from which they are long tiles
 constexpr int kAdGroupRanks = 64;       // ranks that a short shrink CTA holds (at most)
 constexpr int kAdShortPieces = 16;      // its pieces of K (at most)
 constexpr uint32_t kAdMagic = 0x32414248u;   // "HBA2"

@@ -38,14 +38,16 @@ void internal_note_other_launch(void* stream);
 
 namespace {
 
-constexpr int kRopeSmemSeqs = 6143;   // descriptors staged in shared memory up to here (48 KB)
+constexpr int kRopeSmemSeqs = 5500;   // descriptors staged in shared memory up to here (48 KB with the rest)
 constexpr int kRopeIters = 4;         // heads of a lane
-constexpr int kRopeMaxWarps = 8;
+constexpr int kRopeMaxWarps = 8;      // of a CTA
+constexpr int kRopeMaxTokens = 8;
 
 struct RopeParams {
   const int32_t *cu_q_len, *context_len, *block_table;
   int32_t num_seqs, total_q, max_pages_per_seq, num_pages;
-  int32_t hq, hkv, heads, chunks;     // heads: q's, k's and (with a cache) v's; chunks: warps per token
+  int32_t hq, hkv, heads, chunks;     // heads: q's, k's and (with a cache) v's; chunks: a CTA's warps per token
+  int32_t tokens, groups;             // a CTA's tokens (whole, or of one token a group of its warps)
   int32_t rot;
   const uint16_t *q, *k, *v;
   int64_t q_stride, k_stride, v_stride;           // elements between tokens
@@ -83,16 +85,17 @@ __device__ __forceinline__ uint4 narrow(const float* f) {
 template <int D, bool kInterleaved>
 __global__ void __launch_bounds__(32 * kRopeMaxWarps) rope_kernel(const RopeParams p) {
   extern __shared__ int32_t s_cu[];
+  __shared__ float2 s_turn[kRopeMaxTokens][D / 2];    // (cos, sin) times the factor
+  __shared__ int64_t s_slot[kRopeMaxTokens];          // in the cache, in elements; -1: none, -2: no token
   constexpr int kUnits = D / 16;            // lanes of a head
   constexpr int kHeads = 32 / kUnits;       // heads of a warp at a time
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t job = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int tok = (int)(job / p.chunks);
-  const bool live = tok < p.total_q;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int mine = warp / p.chunks;         // of the CTA's tokens
+  const int tok0 = blockIdx.x / p.groups * p.tokens, tok = tok0 + mine;
   const int unit = lane % kUnits;
-  const int head0 = (int)(job % p.chunks) * kRopeIters * kHeads + lane / kUnits;
+  const int head0 = (blockIdx.x % p.groups * p.chunks + warp % p.chunks) * kRopeIters * kHeads + lane / kUnits;
   const bool turns = unit < p.rot / 16;
   // where the lane's two vectors start in a head
   const int at0 = turns && !kInterleaved ? 8 * unit : 16 * unit;
@@ -102,8 +105,8 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps) rope_kernel(const RopePara
   for (int it = 0; it < kRopeIters; ++it) {
     const int h = head0 + it * kHeads;
     in[it][0] = in[it][1] = make_uint4(0, 0, 0, 0);
-    if (!live || h >= p.heads) continue;
-    const uint16_t* src = h < p.hq            ? p.q + tok * p.q_stride + h * D
+    if (tok >= p.total_q || h >= p.heads) continue;
+    const uint16_t* src = h < p.hq           ? p.q + tok * p.q_stride + h * D
                           : h < p.hq + p.hkv ? p.k + tok * p.k_stride + (h - p.hq) * D
                                              : p.v + tok * p.v_stride + (h - p.hq - p.hkv) * D;
     in[it][0] = ld_row(src + at0);
@@ -116,40 +119,53 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps) rope_kernel(const RopePara
     for (int i = threadIdx.x; i < p.num_seqs; i += blockDim.x) s_ctx[i] = __ldg(&p.context_len[i]);
   }
   __syncthreads();
-  if (!live) return;
   const int32_t* cu = staged ? s_cu : p.cu_q_len;
   const int32_t* ctx = staged ? s_ctx : p.context_len;
-  int lo = 0, hi = p.num_seqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cu[mid] <= tok) lo = mid; else hi = mid - 1;
-  }
-  const int q0 = cu[lo], q_len = cu[lo + 1] - q0;
-  if ((unsigned)(tok - q0) >= (unsigned)max(q_len, 0)) return;   // a token of no sequence
-  const int pos = ctx[lo] - q_len + (tok - q0);
-  if (pos < 0) {
-    if (lane == 0) report_error(p.dev_error, HB_DEVERR_INDEX);
-    return;
-  }
-  // the slot in the cache, in elements (-1: none)
-  int64_t slot = -1;
-  if (p.k_cache) {
-    const int lp = pos / kPageSize;
-    const int page = lp < p.max_pages_per_seq ? __ldg(&p.block_table[(size_t)lo * p.max_pages_per_seq + lp]) : -1;
-    if ((unsigned)page < (unsigned)p.num_pages)
-      slot = ((int64_t)page * kPageSize + pos % kPageSize) * p.hkv * D;
-    else if (lane == 0)
+  // a thread per pair of a token, and one for its slot
+  const int jobs = p.rot / 2 + 1;
+  for (int job = threadIdx.x; job < jobs * p.tokens; job += blockDim.x) {
+    const int m = job / jobs, i = job % jobs, t = tok0 + m;
+    const uint64_t phase = i > 0 ? __ldg(p.phases + i - 1) : 0;
+    int lo = 0, hi = p.num_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (cu[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    const int q0 = cu[lo], q_len = cu[lo + 1] - q0;
+    // (a token of no sequence has no position)
+    const bool live = t < p.total_q && (unsigned)(t - q0) < (unsigned)max(q_len, 0);
+    const int pos = live ? ctx[lo] - q_len + (t - q0) : -1;
+    if (i > 0) {
+      // the upper half of position times phase: a signed fraction of half a turn
+      float s, c;
+      sincospif((float)(int32_t)((phase * (uint64_t)(uint32_t)pos) >> 32) * 0x1p-31f, &s, &c);
+      s_turn[m][i - 1] = make_float2(c * p.factor, s * p.factor);
+      continue;
+    }
+    int64_t slot = live ? -1 : -2;
+    if (live && pos < 0) {
       report_error(p.dev_error, HB_DEVERR_INDEX);
+      slot = -2;
+    } else if (live && p.k_cache) {
+      const int lp = pos / kPageSize;
+      const int page = lp < p.max_pages_per_seq ? __ldg(&p.block_table[(size_t)lo * p.max_pages_per_seq + lp]) : -1;
+      if ((unsigned)page < (unsigned)p.num_pages)
+        slot = ((int64_t)page * kPageSize + pos % kPageSize) * p.hkv * D;
+      else
+        report_error(p.dev_error, HB_DEVERR_INDEX);
+    }
+    s_slot[m] = slot;
   }
+  __syncthreads();
+  const int64_t slot = s_slot[mine];
+  if (slot == -2) return;
   float c[8], s[8];
   if (turns) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      // a signed fraction of half a turn
-      const int32_t a = (int32_t)((p.phases[8 * unit + e] * (uint64_t)pos) >> 32);
-      sincospif((float)a * 0x1p-31f, &s[e], &c[e]);
-      s[e] *= p.factor;
-      c[e] *= p.factor;
+      const float2 cs = s_turn[mine][8 * unit + e];
+      c[e] = cs.x;
+      s[e] = cs.y;
     }
   }
 #pragma unroll
@@ -320,9 +336,13 @@ extern "C" hb_status hb_rope(const hb_batch* batch, const hb_rope_params* rope, 
     p.eps = rope->eps;
     const int per_warp = kRopeIters * 32 / (D / 16);
     p.chunks = (p.heads + per_warp - 1) / per_warp;
-    const int64_t jobs = T * p.chunks;
-    const int warps = (int)std::max<int64_t>(1, std::min<int64_t>(kRopeMaxWarps, jobs / (2 * num_sms)));
-    const int64_t grid = (jobs + warps - 1) / warps;
+    // CTAs of whole tokens, up to 8 warps, smaller ones where the tokens are few
+    p.groups = (p.chunks + kRopeMaxWarps - 1) / kRopeMaxWarps;
+    p.chunks = (p.chunks + p.groups - 1) / p.groups;
+    p.tokens = std::min(kRopeMaxTokens, kRopeMaxWarps / p.chunks);
+    while (p.tokens > 1 && (T + p.tokens - 1) / p.tokens < 2 * num_sms) p.tokens /= 2;
+    const int warps = p.tokens * p.chunks;
+    const int64_t grid = (T + p.tokens - 1) / p.tokens * p.groups;
     if (grid > 0x7fffffffLL) return internal_fail(HB_ERR_UNSUPPORTED, "too many tokens and heads at once");
     const size_t smem = p.num_seqs <= kRopeSmemSeqs ? (size_t)(2 * p.num_seqs + 1) * 4 : 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);

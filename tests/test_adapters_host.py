@@ -44,13 +44,13 @@ def test_a_plan_covers_every_token_once(seed):
         assert 1 <= count <= (128 if tok >= 0 else 16)
         if tok >= 0:
             assert (mine == tok + np.arange(count)).all()
-    # long tiles are the runs of 64 neighbours or more, short segments as few as can be
+    # long tiles are the runs of 128 neighbours or more, short segments as few as can be
     edges = np.flatnonzero(np.diff(np.concatenate([[-2], token, [-2]])))
     runs = [(int(token[i]), j - i) for i, j in zip(edges, edges[1:])]
-    assert sum(n for a, n in runs if a >= 0 and n >= 64) == h["long_rows"]
-    assert sum(-(-n // 128) for a, n in runs if a >= 0 and n >= 64) == h["num_long"]
+    assert sum(n for a, n in runs if a >= 0 and n >= 128) == h["long_rows"]
+    assert sum(-(-n // 128) for a, n in runs if a >= 0 and n >= 128) == h["num_long"]
     for a in range(n):
-        count = sum(m for b, m in runs if b == a and m < 64)
+        count = sum(m for b, m in runs if b == a and m < 128)
         assert (short[:, 0] == a).sum() == -(-count // 16)
 
 

@@ -157,7 +157,7 @@ def test_few_and_many_rows(rows):
 
 
 def test_more_sequences_than_shared_memory_holds():
-    for n in (6143, 6144, 9000):
+    for n in (5500, 5501, 9000):
         check_step(Step([(1, 1 + i % 40) for i in range(n)], 2, 1, 64, seed=6), 32, norms=(False, False))
 
 
