@@ -177,7 +177,7 @@ def load():
     L.hb_pages_release.restype = ctypes.c_int
     L.hb_pages_release.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
     L.hb_norm.restype = ctypes.c_int
-    L.hb_norm.argtypes = [P(HbNormArgs), vp]
+    L.hb_norm.argtypes = [vp, vp]
     L.hb_rope_phases.restype = ctypes.c_int
     L.hb_rope_phases.argtypes = [i32, ctypes.c_double, i32] + [ctypes.c_double] * 4 + [vp]
     L.hb_rope.restype = ctypes.c_int
@@ -185,7 +185,7 @@ def load():
     L.hb_adapters_plan.restype = ctypes.c_int
     L.hb_adapters_plan.argtypes = [i32, i32, vp, vp, i32, i32, i32, vp, P(sz), vp, P(sz), vp]
     L.hb_adapters.restype = ctypes.c_int
-    L.hb_adapters.argtypes = [P(HbAdapterPool), vp, vp, P(HbLinearOut), P(HbLinearOut), vp, vp]
+    L.hb_adapters.argtypes = [P(HbAdapterPool), vp, vp, vp, vp, vp, vp]
     L.hb_launch_count.restype = i64
     L.hb_launch_count.argtypes = []
     L.hb_builder_create.restype = ctypes.c_int
@@ -831,6 +831,8 @@ def hb_linear(x, w, outs, epilogue=LINEAR_STORE, stream=None, workspace="auto"):
 
 # ---------------------------------------------------------------- norms
 _F32 = torch.float32
+_NORM_ARGS = struct.Struct("<4i7Q5q4f")     # HbNormArgs
+assert _NORM_ARGS.size == ctypes.sizeof(HbNormArgs)
 
 
 def _refuse_rows(*specs):
@@ -868,42 +870,43 @@ def hb_norm(x=None, y=None, x_out=None, z=None, w_pre=None, w_post=None, gate=No
     lead = x if x is not None else y
     if not isinstance(lead, torch.Tensor) or lead.dim() != 2:
         raise ValueError("x or y must be a [rows, width] tensor")
-    shape = lead.shape
+    shape, dev = lead.shape, lead.get_device()
     rows, width = shape
-    a = HbNormArgs()
-    ok = True
-    dev = lead.get_device()
     kind = x.dtype if x is not None else (x_out.dtype if isinstance(x_out, torch.Tensor) else _BF16)
+    # (addresses and strides of what is given; the struct's fields set one by one take twice as long)
+    px = py = pg = pp = pw = po = pz = sx = sy = sg = so = sz = 0
     try:
+        ok = ((kind is _BF16 or kind is _F32) and rows <= _INT_MAX and 0 < width <= _INT_MAX and dev >= 0
+              and dev == _current_device())
         if x is not None:
-            ok = x.stride(1) == 1 or width == 1
-            a.x, a.x_stride = x.data_ptr(), x.stride(0)
+            sx, one = x.stride()
+            ok, px = ok and one == 1, x.data_ptr()
         if y is not None:
-            ok = ok and y.dtype is _BF16 and y.shape == shape and y.stride(1) == 1 and y.get_device() == dev
-            a.y, a.y_stride = y.data_ptr(), y.stride(0)
+            sy, one = y.stride()
+            ok = ok and one == 1 and y.dtype is _BF16 and y.shape == shape and y.get_device() == dev
+            py = y.data_ptr()
         if x_out is not None:
-            ok = (ok and x_out.dtype is kind and x_out.shape == shape and x_out.stride(1) == 1
-                  and x_out.get_device() == dev)
-            a.x_out, a.x_out_stride = x_out.data_ptr(), x_out.stride(0)
+            so, one = x_out.stride()
+            ok = ok and one == 1 and x_out.dtype is kind and x_out.shape == shape and x_out.get_device() == dev
+            po = x_out.data_ptr()
         if z is not None:
-            ok = ok and z.dtype is _BF16 and z.shape == shape and z.stride(1) == 1 and z.get_device() == dev
-            a.z, a.z_stride = z.data_ptr(), z.stride(0)
+            sz, one = z.stride()
+            ok = ok and one == 1 and z.dtype is _BF16 and z.shape == shape and z.get_device() == dev
+            pz = z.data_ptr()
         if w_pre is not None:
             ok = (ok and w_pre.dtype is _BF16 and w_pre.shape == (width,) and w_pre.is_contiguous()
                   and w_pre.get_device() == dev)
-            a.w_pre = w_pre.data_ptr()
+            pw = w_pre.data_ptr()
         if w_post is not None:
             ok = (ok and w_post.dtype is _BF16 and w_post.shape == (width,) and w_post.is_contiguous()
                   and w_post.get_device() == dev)
-            a.w_post = w_post.data_ptr()
+            pp = w_post.data_ptr()
         if gate is not None:
             each = gate.dim() == 2 and gate.shape[0] == rows and rows > 1
             ok = (ok and gate.dtype is _BF16 and (each or gate.numel() == width) and gate.shape[-1] == width
                   and gate.stride(-1) == 1 and gate.get_device() == dev)
-            a.gate, a.gate_stride = gate.data_ptr(), gate.stride(0) if each else 0
-        ok = (ok and rows <= _INT_MAX and 0 < width <= _INT_MAX and (kind is _BF16 or kind is _F32) and dev >= 0
-              and dev == _current_device())
-    except (AttributeError, IndexError):
+            pg, sg = gate.data_ptr(), gate.stride(0) if each else 0
+    except (AttributeError, IndexError, ValueError):
         ok = False
     if not ok:
         stream_t = (kind if kind in (_BF16, _F32) else _BF16,)
@@ -917,9 +920,9 @@ def hb_norm(x=None, y=None, x_out=None, z=None, w_pre=None, w_post=None, gate=No
         raise ValueError("width must be > 0, and the tensors on one device")
     if rows == 0:
         return
-    a.rows, a.width, a.stream_type = rows, width, 1 if kind is _F32 else 0
-    a.eps, a.residual_scale, a.branch_scale, a.weight_offset = eps, residual_scale, branch_scale, weight_offset
-    st = (_lib or load()).hb_norm(ctypes.byref(a), _raw_stream(stream, dev))
+    st = (_lib or load()).hb_norm(
+        _NORM_ARGS.pack(rows, width, 1 if kind is _F32 else 0, 0, px, py, pg, pp, pw, po, pz, sx, sy, sg, so, sz, eps,
+                        residual_scale, branch_scale, weight_offset), _raw_stream(stream, dev))
     if st:
         _check(st)
 
@@ -963,13 +966,13 @@ def make_rope(rotary_dim, base=10000.0, scaling="none", scale_by=1.0, original_c
 
 def _dense_heads(t):
     """Whether a token's heads stand one behind the other."""
-    return t.stride(2) == 1 and (t.stride(1) == t.shape[2] or t.shape[1] == 1)
+    return t.is_contiguous() or (t.stride(2) == 1 and (t.stride(1) == t.shape[2] or t.shape[1] == 1))
 
 
 def _in_place_or_dense(out, source):
     if out is source:
         return True
-    if out.data_ptr() == source.data_ptr():
+    if out.data_ptr() == source.data_ptr() and not (out.is_contiguous() and source.is_contiguous()):
         return _dense_heads(out) and (out.stride(0) == source.stride(0) or out.shape[0] == 1)
     return out.is_contiguous()
 
@@ -1079,6 +1082,8 @@ _ADAPTER_PLAN_BYTES = 88
 _ADAPTER_PLAN_INTS = struct.Struct("<I11i")
 _ADAPTER_PLAN_SIZES = struct.Struct("<QQ")      # workspace, plan
 _ADAPTER_PLAN_SIZES_AT = 48 + 3 * 8
+_LINEAR_OUT = struct.Struct("<3Q3i4x")          # HbLinearOut
+assert _LINEAR_OUT.size == ctypes.sizeof(HbLinearOut)
 
 
 def adapters_plan_header(plan):
@@ -1153,7 +1158,7 @@ def hb_adapters(pool, plan, x, y, out, workspace, stream=None):
     if not isinstance(pool, HbAdapterPool) or not hasattr(pool, "cols"):
         raise ValueError("pool must be what make_adapters returned")
     rows, cols = _ADAPTER_PLAN_INTS.unpack_from(plan)[2], pool.cols
-    src, dst = HbLinearOut(), HbLinearOut()
+    src, dst = [], []
     try:
         dev = x.get_device()
         ok = (x.dtype is _BF16 and x.shape == (rows, pool.K) and x.is_contiguous() and dev >= 0
@@ -1165,7 +1170,8 @@ def hb_adapters(pool, plan, x, y, out, workspace, stream=None):
             ok = (ok and s.dtype is _BF16 and s.shape == (rows, n) and s.is_contiguous() and s.get_device() == dev
                   and (d is s or (d.dtype is _BF16 and d.shape == (rows, n) and d.is_contiguous()
                                   and d.get_device() == dev)))
-            src.y[i], src.cols[i], dst.y[i], dst.cols[i] = s.data_ptr(), n, d.data_ptr(), n
+            src.append(s.data_ptr())
+            dst.append(d.data_ptr())
     except (AttributeError, TypeError, IndexError):
         ok = False
     if not ok:
@@ -1185,7 +1191,9 @@ def hb_adapters(pool, plan, x, y, out, workspace, stream=None):
         at = ctypes.byref(_CHAR.from_buffer(plan))
     except TypeError:                                # (read-only)
         at = plan.ctypes.data
-    st = (_lib or load()).hb_adapters(ctypes.byref(pool), at, x.data_ptr(), ctypes.byref(src), ctypes.byref(dst),
-                                      workspace.data_ptr(), _raw_stream(stream, dev))
+    none = (0,) * (3 - len(cols))
+    st = (_lib or load()).hb_adapters(ctypes.byref(pool), at, x.data_ptr(), _LINEAR_OUT.pack(*src, *none, *cols, *none),
+                                      _LINEAR_OUT.pack(*dst, *none, *cols, *none), workspace.data_ptr(),
+                                      _raw_stream(stream, dev))
     if st:
         _check(st)
