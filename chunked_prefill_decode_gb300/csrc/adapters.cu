@@ -33,6 +33,12 @@
 // Order of the launches of a call with both kinds: shrink long, shrink short,
 // expand long, expand short.  The second and the fourth need nothing of the one
 // before them: they start under it and wait for it at their end (kWaitLast).
+//
+// Measured on GB300 (a call among others in a graph, inputs not in L2): 64 decodes,
+// 48 adapters of rank 16, K 4096, N 6144 11.6 us (24 MB; 8.4 us from L2: two launches
+// of one latency chain each); 64 decodes and a chunk of 448, ranks 8-64, K 14336, N
+// 4096 39 us; 5 prompts of 1201 and 61 decodes, ranks 16-64, K 7168, N 9216 112 us.
+// All rows in 64-row segments on warp MMAs: 48 and 229 us for the last two.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -60,7 +66,10 @@ void internal_note_other_launch(void* stream);
 namespace {
 
 constexpr int kAdThreads = 256, kAdWarps = kAdThreads / 32;
-constexpr int kAdLongRun = 128;         // neighbouring rows of an adapter from which they are long tiles
+// Neighbouring rows of an adapter from which they are long tiles: a 64-token chunk
+// and 4 decodes at K 512 take 4.1 us as short segments, 9.8 us with a tile (four
+// launches instead of two).
+constexpr int kAdLongRun = 128;
 constexpr int kAdGroupRanks = 64;       // ranks that a short shrink CTA holds (at most)
 constexpr int kAdShortPieces = 16;      // its pieces of K (at most)
 constexpr uint32_t kAdMagic = 0x32414248u;   // "HBA2"
@@ -650,12 +659,11 @@ extern "C" hb_status hb_adapters(const hb_adapter_pool* pool, const void* h_plan
       if (e != cudaSuccess) return internal_failf(HB_ERR_CUDA, "adapter clusters: %s", cudaGetErrorString(e));
       int best = 1;
       int64_t best_cost = INT64_MAX;
-      // (a CTA's time is that of its units, twice as long with two on an SM, and of
-      // about 16 more for its start, the sums' exchange and its end)
+      // (a CTA's start, the sums' exchange and its end take as long as 16 units)
       for (int n = 1; n <= std::min(kLsMaxPieces, units); ++n) {
         if (clusters->fit[n] == 0) continue;
         const int64_t waves = (ctas + clusters->fit[n] - 1) / clusters->fit[n];
-        const int64_t cost = waves * ((units + n - 1) / n * (ctas * n > h.num_sms ? 2 : 1) + 16);
+        const int64_t cost = waves * ((units + n - 1) / n + 16);
         if (cost < best_cost) best = n, best_cost = cost;
       }
       cut_k(lo, best);

@@ -12,6 +12,14 @@
 // load to the last store, so that z is the norm of the sum before its rounding
 // and no operand is read twice; the two means are sums over a warp's lanes and
 // then, through shared memory, over the group's warps, in a fixed order.
+//
+// Measured on GB300 (a call among others in a graph, inputs not in L2): one row of
+// 7168 2.5 us; 512 rows of 4096, sum and norm, 5.1 us (3.3 TB/s); 2048 of 7168, both
+// norms, fp32 stream, 37.9 us (4.6 TB/s, 69 % of the copy rate); 8191 of 4096, both
+// norms, gates per row, 59.6 us (5.6 TB/s, 83 %).  Two or four vectors per thread
+// instead of one where rows are many: 65.7 us against 78 for the last one (fewer
+// warps to a row's sums).  Rows kept packed until used and weights loaded late, for
+// 85 registers and a third CTA on the SM: 39.3 us against 37.9 on 2048 rows (spills).
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -10,6 +10,11 @@
  *   hb_plan       (host) split the batch into work items; upload the plan
  *   hb_attention  attention of every new token over its sequence's pages
  *
+ * Around it, on the same batches: hb_linear (the block's projections), hb_norm,
+ * hb_rope (in hb_kv_append's place for a model with rotary positions) and
+ * hb_adapters; and, in their own sections, the 8-bit cache, pages on the GPU,
+ * steps from host memory and the batch builder.
+ *
  * The operation follows "Sarathi-Serve：以 chunked-prefills 与 stall-free batching
  * 驯服 LLM 推理的吞吐—延迟权衡", §GPU / 系统数据路径 ③ (a batch of decode tokens
  * plus prefill chunks within a token budget) and ⑤ (attention reads and
@@ -686,9 +691,12 @@ typedef struct hb_adapter_pool {
  * Buffers, sizes and upload as with hb_plan (h_plan must stay unchanged until
  * its copy has completed; a workspace must not be shared by calls in flight at
  * once; a captured hb_adapters reads the plan in its workspace when it is
- * replayed, so that workspace takes no other plan meanwhile).  The workspace
- * also holds x A^T in fp32, up to 16 parts of it (4 * max_ranks bytes per row
- * and part; more parts where rows are few).
+ * replayed, so that workspace takes no other plan meanwhile).  Runs of 128
+ * neighbouring rows of an adapter or more (prompts) are cut into tiles of up to
+ * 128 rows for the tensor cores, the other rows into segments of up to 16.  The
+ * workspace also holds x A^T: for a tile's rows two bf16 terms (4 * (max_ranks +
+ * 24) bytes each of 128 rows), for the others up to 16 parts in fp32 (4 *
+ * max_ranks bytes per row and part; more parts where rows are few).
  * Errors: HB_ERR_SHAPE for lengths or adapters that break the rules,
  * HB_ERR_WORKSPACE if a buffer is too small.
  */
@@ -704,7 +712,9 @@ hb_status hb_adapters_plan(int32_t num_seqs, int32_t total_q, const int32_t* h_q
  *            no other operand: rows whose sequence has no adapter are then
  *            copied.  out must not overlap x.
  * x A^T is summed in fp32 and enters the second product in two bf16 terms (16
- * bits); the sum with y is rounded once.  Two launches.  Errors:
+ * bits); the sum with y is rounded once.  Two launches for the tiles and two for
+ * the other rows, which run side by side.  A wait that gives up is reported by
+ * hb_check as HB_ERR_TIMEOUT.  Errors:
  * HB_ERR_WORKSPACE if h_plan does not match the pool, HB_ERR_INVALID_ARG for
  * operands that overlap, others as hb_linear.
  */
