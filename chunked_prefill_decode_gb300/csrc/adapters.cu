@@ -676,8 +676,16 @@ extern "C" hb_status hb_adapters(const hb_adapter_pool* pool, const void* h_plan
       sh.groups = (p.ranks + kAdGroupRanks - 1) / kAdGroupRanks;
       sh.group_ranks = ((p.ranks + sh.groups - 1) / sh.groups + 7) / 8 * 8;
       const int64_t ctas = (int64_t)h.num_short * sh.groups;
-      cut_k(sh, (int)std::min<int64_t>({h.short_pieces, std::max<int64_t>(1, (2LL * h.num_sms + ctas - 1) / ctas),
-                                        std::max(1, units / kAdWarps)}));
+      // (rounds of two CTAs per SM, one beside a long tile's, each as long as its warps' units and three more)
+      const int64_t slots = 2LL * h.num_sms - (h.num_long ? std::min<int64_t>(h.num_sms, (int64_t)h.num_long * lo.groups * lo.pieces) : 0);
+      int best = 1;
+      int64_t best_cost = INT64_MAX;
+      for (int n = 1; n <= std::min(h.short_pieces, std::max(1, units / kAdWarps)); ++n) {
+        const int64_t rounds = (ctas * n + slots - 1) / slots;
+        const int64_t cost = rounds * (((units + n - 1) / n + kAdWarps - 1) / kAdWarps + 3);
+        if (cost < best_cost) best = n, best_cost = cost;
+      }
+      cut_k(sh, best);
       if (ctas * sh.pieces > INT_MAX) return internal_fail(HB_ERR_UNSUPPORTED, "too many tokens at once");
     }
     LeMaps maps{};

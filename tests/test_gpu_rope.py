@@ -137,7 +137,7 @@ ROWS = [(1, 1), (1, 16), (1, 17), (5, 5), (17, 40), (1, 100000), (33, 1001), (2,
 
 
 @pytest.mark.parametrize("interleaved", [False, True])
-@pytest.mark.parametrize("hq,hkv,d", [(8, 8, 64), (32, 8, 128), (7, 1, 128), (16, 1, 64), (56, 8, 128), (32, 16, 128)])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 8, 64), (32, 8, 128), (7, 1, 128), (16, 1, 64), (56, 8, 128), (32, 16, 128), (128, 16, 128)])
 def test_against_the_definition(hq, hkv, d, interleaved):
     for i, rot in enumerate((d, d // 2, 16, 48, 0)):
         st = Step(ROWS, hq, hkv, d, seed=i, spare=i % 3, fused=bool(i % 2))
