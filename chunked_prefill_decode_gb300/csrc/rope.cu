@@ -11,12 +11,20 @@
 // the position.
 //
 // Every element is read and written once (k also into its page): HBM bounds
-// large batches, launch and latency small ones.  A warp takes one token and up
-// to 16 (D 128) or 32 (D 64) of its heads, q's, k's and v's in one list; a lane
-// holds 8 pairs of a head (two 16-byte vectors: i and i + rotary_dim / 2 in the
-// half layout, neighbours in the interleaved one), which are the same pairs in
-// each of its heads, so that it takes 8 sines and cosines for all of them.  The
-// rows' loads are issued before the row -> sequence search, as in the append.
+// large batches, launch and latency small ones.  A warp takes one token and some of
+// its heads, q's, k's and v's in one list; a lane holds 8 pairs of a head (two
+// 16-byte vectors: i and i + rotary_dim / 2 in the half layout, neighbours in the
+// interleaved one), which are the same pairs in each of its two to four heads.  The
+// warps of a token stand in one CTA, which takes the token's sines and cosines once,
+// a thread per pair, in shared memory (each lane taking its own eight: 85.4 us
+// instead of 77.8 on the largest case below, 28.0 instead of 24.5 on the one before).
+// The rows' loads are issued before the row -> sequence search, as in the append.
+//
+// Measured on GB300 (a call among others in a graph, inputs not in L2): 68 tokens
+// of 8 + 8 heads of 64 2.8 us; 512 of 32 + 8 heads of 128 4.7 us; 2048 of 56 + 8 with
+// head norms 22.0 us (3.6 TB/s; the chain of loads, search, angles, sums and stores
+// of a token is longer than its bytes); 16205 of 32 + 8 70.7 us (6.1 TB/s, 90 % of
+// the copy rate).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -39,7 +47,6 @@ void internal_note_other_launch(void* stream);
 namespace {
 
 constexpr int kRopeSmemSeqs = 5500;   // descriptors staged in shared memory up to here (48 KB with the rest)
-constexpr int kRopeIters = 4;         // heads of a lane
 constexpr int kRopeMaxWarps = 8;      // of a CTA
 constexpr int kRopeMaxTokens = 8;
 
@@ -82,8 +89,9 @@ __device__ __forceinline__ uint4 narrow(const float* f) {
                     pack_bf16x2(f[6], f[7]));
 }
 
-template <int D, bool kInterleaved>
-__global__ void __launch_bounds__(32 * kRopeMaxWarps) rope_kernel(const RopeParams p) {
+// kIters: heads of a lane; kCtas: CTAs of 8 warps that an SM's registers hold (at least).
+template <int D, bool kInterleaved, int kIters, int kCtas>
+__global__ void __launch_bounds__(32 * kRopeMaxWarps, kCtas) rope_kernel(const RopeParams p) {
   extern __shared__ int32_t s_cu[];
   __shared__ float2 s_turn[kRopeMaxTokens][D / 2];    // (cos, sin) times the factor
   __shared__ int64_t s_slot[kRopeMaxTokens];          // in the cache, in elements; -1: none, -2: no token
@@ -95,14 +103,14 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps) rope_kernel(const RopePara
   const int mine = warp / p.chunks;         // of the CTA's tokens
   const int tok0 = blockIdx.x / p.groups * p.tokens, tok = tok0 + mine;
   const int unit = lane % kUnits;
-  const int head0 = (blockIdx.x % p.groups * p.chunks + warp % p.chunks) * kRopeIters * kHeads + lane / kUnits;
+  const int head0 = (blockIdx.x % p.groups * p.chunks + warp % p.chunks) * kIters * kHeads + lane / kUnits;
   const bool turns = unit < p.rot / 16;
   // where the lane's two vectors start in a head
   const int at0 = turns && !kInterleaved ? 8 * unit : 16 * unit;
   const int at1 = turns && !kInterleaved ? p.rot / 2 + 8 * unit : 16 * unit + 8;
-  uint4 in[kRopeIters][2];
+  uint4 in[kIters][2];
 #pragma unroll
-  for (int it = 0; it < kRopeIters; ++it) {
+  for (int it = 0; it < kIters; ++it) {
     const int h = head0 + it * kHeads;
     in[it][0] = in[it][1] = make_uint4(0, 0, 0, 0);
     if (tok >= p.total_q || h >= p.heads) continue;
@@ -169,7 +177,7 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps) rope_kernel(const RopePara
     }
   }
 #pragma unroll
-  for (int it = 0; it < kRopeIters; ++it) {
+  for (int it = 0; it < kIters; ++it) {
     const int h = head0 + it * kHeads;
     const bool is_q = h < p.hq, is_k = !is_q && h < p.hq + p.hkv;
     const uint16_t* w = is_q ? p.q_weight : is_k ? p.k_weight : nullptr;
@@ -222,6 +230,13 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps) rope_kernel(const RopePara
       *reinterpret_cast<uint4*>(dst + at1) = out[1];
     }
   }
+}
+
+using RopeKernel = void (*)(RopeParams);
+template <int kIters, int kCtas>
+RopeKernel rope_kernel_of(int head_dim, bool interleaved) {
+  return head_dim == 128 ? (interleaved ? rope_kernel<128, true, kIters, kCtas> : rope_kernel<128, false, kIters, kCtas>)
+                         : (interleaved ? rope_kernel<64, true, kIters, kCtas> : rope_kernel<64, false, kIters, kCtas>);
 }
 
 }  // namespace
@@ -334,7 +349,16 @@ extern "C" hb_status hb_rope(const hb_batch* batch, const hb_rope_params* rope, 
     p.k_weight = static_cast<const uint16_t*>(rope->k_weight);
     p.factor = rope->factor;
     p.eps = rope->eps;
-    const int per_warp = kRopeIters * 32 / (D / 16);
+    // few tokens: two heads per lane, the shortest chain (68 tokens 2.8 us, with four 3.5; 512 4.7 and 4.9); many:
+    // four, three CTAs to an SM (16205 tokens 70.7 us; two CTAs 93, three heads 74); with head norms three and four
+    // (2048 tokens 22.0 us; four and three 24.8, two and four 23.0)
+    const bool few = T <= 4LL * num_sms, norms = p.q_weight || p.k_weight;
+    const int iters = few ? 2 : norms ? 3 : 4;
+    const bool inter = rope->interleaved != 0;
+    const RopeKernel kernel = few     ? rope_kernel_of<2, 1>(D, inter)
+                              : norms ? rope_kernel_of<3, 4>(D, inter)
+                                      : rope_kernel_of<4, 3>(D, inter);
+    const int per_warp = iters * 32 / (D / 16);
     p.chunks = (p.heads + per_warp - 1) / per_warp;
     // CTAs of whole tokens, up to 8 warps, smaller ones where the tokens are few
     p.groups = (p.chunks + kRopeMaxWarps - 1) / kRopeMaxWarps;
@@ -346,8 +370,6 @@ extern "C" hb_status hb_rope(const hb_batch* batch, const hb_rope_params* rope, 
     if (grid > 0x7fffffffLL) return internal_fail(HB_ERR_UNSUPPORTED, "too many tokens and heads at once");
     const size_t smem = p.num_seqs <= kRopeSmemSeqs ? (size_t)(2 * p.num_seqs + 1) * 4 : 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    auto kernel = D == 128 ? (rope->interleaved ? rope_kernel<128, true> : rope_kernel<128, false>)
-                           : (rope->interleaved ? rope_kernel<64, true> : rope_kernel<64, false>);
     const cudaError_t e = launch_serialized(kernel, (unsigned)grid, (unsigned)(32 * warps), smem, st, p);
     if (e != cudaSuccess) return internal_failf(HB_ERR_CUDA, "rope launch: %s", cudaGetErrorString(e));
     internal_note_other_launch(stream);
