@@ -37,7 +37,7 @@
 // Measured on GB300 (a call among others in a graph, inputs not in L2): 64 decodes,
 // 48 adapters of rank 16, K 4096, N 6144 11.6 us (24 MB; 8.4 us from L2: two launches
 // of one latency chain each); 64 decodes and a chunk of 448, ranks 8-64, K 14336, N
-// 4096 39 us; 5 prompts of 1201 and 61 decodes, ranks 16-64, K 7168, N 9216 112 us.
+// 4096 32 us; 5 prompts of 1201 and 61 decodes, ranks 16-64, K 7168, N 9216 100 us.
 // All rows in 64-row segments on warp MMAs: 48 and 229 us for the last two.
 #include <cuda.h>
 #include <cuda_runtime.h>
