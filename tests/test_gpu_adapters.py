@@ -84,13 +84,13 @@ class Case:
 @pytest.mark.parametrize("r", [8, 16, 24, 32, 40, 64, 104, 128])
 @pytest.mark.parametrize("cols", [(256,), (40, 8), (512, 128, 128)])
 def test_against_the_definition(cols, r):
-    q = [1, 1, 5, 1, 70, 1, 0, 1, 33, 1]
-    of = [0, 3, 1, 0, 2, -1, 1, 4, -1, 0]
+    q = [1, 1, 5, 1, 70, 1, 0, 1, 33, 1, 131, 140, 1, 260]
+    of = [0, 3, 1, 0, 2, -1, 1, 4, -1, 0, 4, -1, 2, 1]
     Case(q, of, 320, cols, 5, r, seed=r, spare=2).check_both()
 
 
 @pytest.mark.parametrize("k,n", [(8, 8), (24, 16), (56, 264), (64, 32), (1000, 776), (72, 2056), (4096, 1024), (14336, 256)])
-@pytest.mark.parametrize("rows", [[1], [1, 1, 1], [17, 1, 150]])
+@pytest.mark.parametrize("rows", [[1], [1, 1, 1], [17, 1, 150], [128, 129]])
 def test_widths(k, n, rows):
     Case(rows, [i % 2 for i in range(len(rows))], k, (n,), 2, 16, seed=k).check_both()
 
@@ -100,15 +100,18 @@ def test_ranks_of_every_kind(ranks):
     r = max(8, -(-max(ranks) // 8) * 8)
     for cols in ((96,), (96, 40)):
         Case([1, 20, 1, 4, 70], [0, 1, 2, 0, 2], 200, cols, 3, r, seed=sum(ranks), ranks=ranks).check_both()
+        Case([150, 1, 140, 4, 128], [0, 1, 2, 0, 1], 200, cols, 3, r, seed=sum(ranks), ranks=ranks).check_both()
 
 
 def test_ranks_outside_of_the_pool_are_held_to_it():
     hb = lib()
-    c = Case([1, 3, 2], [0, 1, 2], 64, (64,), 3, 16, ranks=[16, 16, 16])
-    want = c.run()[0]
-    c.rank.copy_(torch.tensor([17, 1 << 30, -5], dtype=torch.int32))
-    got = c.run()[0]
-    assert torch.equal(got[:4], want[:4]) and torch.equal(got[4:], c.y[0][4:])
+    for q in ([1, 3, 2], [130, 200, 128]):
+        c = Case(q, [0, 1, 2], 64, (64,), 3, 16, ranks=[16, 16, 16])
+        want = c.run()[0]
+        c.rank.copy_(torch.tensor([17, 1 << 30, -5], dtype=torch.int32))
+        got = c.run()[0]
+        n = q[0] + q[1]
+        assert torch.equal(got[:n], want[:n]) and torch.equal(got[n:], c.y[0][n:])
 
 
 @pytest.mark.parametrize("seed", range(4))
@@ -144,22 +147,36 @@ def test_one_request_does_not_change_another():
     assert got[6].isnan().all() and not got[9].isfinite().any()
 
 
-def test_infinities_come_through():
+def test_a_row_of_a_tile_does_not_change_another():
+    c = Case([150, 1, 135], [0, 1, 1], 512, (256, 64), 2, 24, seed=5)
+    full = c.run()
+    c.x[6] = float("nan")
+    c.x[140, 4] = float("inf")
+    c.x[200] = float("nan")
+    bad = [6, 140, 200]
+    keep = [i for i in range(286) if i not in bad]
+    for got, want in zip(c.run(), full):
+        assert torch.equal(got[keep], want[keep])
+        assert got[[6, 200]].isnan().all() and not got[140].isfinite().any()
+
+
+@pytest.mark.parametrize("n", [1, 140])
+def test_infinities_come_through(n):
     """A rank-1 adapter, and one that has no rank, next to dead ranks."""
-    c = Case([1, 1], [0, 1], 64, (64,), 2, 8, ranks=[1, 0])
+    c = Case([n, n], [0, 1], 64, (64,), 2, 8, ranks=[1, 0])
     c.a[0, 0, 0] = 1.0
     c.b[0, :, 0] = torch.where(torch.arange(64, device="cuda") % 2 == 0, 1.0, -1.0).to(BF)
     c.scale.fill_(1.0)
     c.x.fill_(0.5)
     c.x[:, 3] = float("inf")
     out = c.run()[0]
-    assert (out[0, ::2] == float("inf")).all() and (out[0, 1::2] == float("-inf")).all()
-    assert torch.equal(out[1], c.y[0][1])
+    assert (out[:n, ::2] == float("inf")).all() and (out[:n, 1::2] == float("-inf")).all()
+    assert torch.equal(out[n:], c.y[0][n:])
 
 
 def test_captured_replayed_and_on_another_stream():
     hb = lib()
-    c = Case([1] * 30 + [100], [i % 7 for i in range(31)], 512, (256, 64), 7, 16, seed=6)
+    c = Case([1] * 30 + [100, 300], [i % 7 for i in range(32)], 512, (256, 64), 7, 16, seed=6)
     want = c.run()
     plan, ws = c.plan()
     outs = [torch.empty_like(y) for y in c.y]
@@ -191,7 +208,7 @@ def test_captured_replayed_and_on_another_stream():
 
 def test_a_plan_serves_the_projections_of_a_step():
     hb = lib()
-    q, of = [1, 1, 40, 1], [2, 0, 1, 2]
+    q, of = [1, 1, 40, 1, 260], [2, 0, 1, 2, 1]
     cases = [Case(q, of, 512, (512, 128, 128), 3, 16, seed=1), Case(q, of, 1024, (256,), 3, 64, seed=2)]
     plan, ws = hb.hb_adapters_plan([c.pool for c in cases], q, of, sms())
     for _ in range(2):
@@ -200,10 +217,10 @@ def test_a_plan_serves_the_projections_of_a_step():
             hb.hb_adapters(c.pool, plan, c.x, c.y, outs, ws)
             c.check(outs)
     # planned again into the same buffers
-    plan2, ws2 = hb.hb_adapters_plan([c.pool for c in cases], q, [0, 0, 0, 0], sms(), plan=plan, workspace=ws)
+    plan2, ws2 = hb.hb_adapters_plan([c.pool for c in cases], q, [0] * 5, sms(), plan=plan, workspace=ws)
     assert ws2.data_ptr() == ws.data_ptr()
     c = cases[0]
-    c.of = [0, 0, 0, 0]
+    c.of = [0] * 5
     outs = [torch.empty_like(y) for y in c.y]
     hb.hb_adapters(c.pool, plan2, c.x, c.y, outs, ws2)
     c.check(outs)
@@ -212,7 +229,7 @@ def test_a_plan_serves_the_projections_of_a_step():
 def test_beside_the_projection():
     """hb_linear and the adapters in place: the tuned weights' product."""
     hb = lib()
-    c = Case([1] * 9 + [50], [0, 1, 2, -1, 0, 1, 2, 0, 1, 2], 512, (512, 256, 256), 3, 16, seed=8)
+    c = Case([1] * 9 + [50, 333], [0, 1, 2, -1, 0, 1, 2, 0, 1, 2, 1], 512, (512, 256, 256), 3, 16, seed=8)
     w = (torch.randn(1024, 512, device="cuda") / 512 ** 0.5).to(BF)
     hb.hb_linear(c.x, w, c.y)
     want, size = c.expected()
@@ -237,3 +254,38 @@ def test_offsets_past_32_bits():
     hb.hb_adapters(pool, plan, x, [y], [out], ws)
     want = x.double() @ a[n - 1, 0].double().T @ b[n - 1].double().T
     assert torch.allclose(out.double(), want, rtol=2.0 ** -7, atol=2e-3)
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    hb = lib()
+    cases = [Case([1] * 20 + [400], [i % 5 for i in range(21)], 1024, (512, 128), 5, 32, seed=i) for i in (1, 2)]
+    want = [c.run() for c in cases]
+    plans = [c.plan() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[torch.empty_like(y) for y in c.y] for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, (plan, ws), st, o in zip(cases, plans, streams, outs):
+            hb.hb_adapters(c.pool, plan, c.x, c.y, o, ws, stream=st)
+    torch.cuda.synchronize()
+    hb.hb_check()
+    assert all(torch.equal(a, b) for o, w in zip(outs, want) for a, b in zip(o, w))
+
+
+def test_calls_that_follow_one_another_in_place():
+    """Through one workspace, each on the last one's results, beside other launches."""
+    hb = lib()
+    c = Case([1] * 20 + [400, 7], [i % 5 for i in range(22)], 256, (256,), 5, 32, seed=3)
+    plan, ws = c.plan()
+    y = c.y[0].clone()
+    apart = c.y[0]
+    for _ in range(8):
+        hb.hb_adapters(c.pool, plan, c.x, [y], [y], ws)
+        hb.hb_norm(x=y, z=y)
+        out = torch.empty_like(apart)
+        hb.hb_adapters(c.pool, plan, c.x, [apart], [out], ws)
+        torch.cuda.synchronize()
+        apart = torch.empty_like(out)
+        hb.hb_norm(x=out, z=apart)
+        torch.cuda.synchronize()
+    assert torch.equal(y, apart)

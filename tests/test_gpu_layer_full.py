@@ -26,7 +26,7 @@ bits = workloads.bf16_bits
 BF = torch.bfloat16
 HQ, HKV, D = 8, 2, 128
 SHAPE = BlockShape(hidden=512, num_q_heads=HQ, num_kv_heads=HKV, head_dim=D, ffn=1024)
-ROWS = [(1, 300), (1, 41), (70, 70), (1, 129), (33, 600)]
+ROWS = [(1, 300), (1, 41), (150, 150), (1, 129), (33, 600)]
 OF = [1, -1, 0, 1, 2]
 
 
