@@ -964,17 +964,22 @@ def make_rope(rotary_dim, base=10000.0, scaling="none", scale_by=1.0, original_c
     return r
 
 
-def _dense_heads(t):
-    """Whether a token's heads stand one behind the other."""
-    return t.is_contiguous() or (t.stride(2) == 1 and (t.stride(1) == t.shape[2] or t.shape[1] == 1))
+def _token_stride(t, row):
+    """Elements between tokens whose heads (of `row` elements) stand one behind the
+    other; -1 where they do not.  (A stride costs three times what is_contiguous does.)"""
+    if t.is_contiguous():
+        return row
+    first, head, one = t.stride()
+    return first if one == 1 and (head == t.shape[2] or t.shape[1] == 1) else -1
 
 
-def _in_place_or_dense(out, source):
+def _in_place_or_dense(out, source, row):
+    """out: source itself, or contiguous (and not at its place with another stride)."""
     if out is source:
         return True
-    if out.data_ptr() == source.data_ptr() and not (out.is_contiguous() and source.is_contiguous()):
-        return _dense_heads(out) and (out.stride(0) == source.stride(0) or out.shape[0] == 1)
-    return out.is_contiguous()
+    if out.data_ptr() != source.data_ptr():
+        return out.is_contiguous()
+    return out.shape[0] == 1 or _token_stride(out, row) == _token_stride(source, row) >= 0
 
 
 def hb_rope(batch, rope, q, k, v, q_out, k_out, k_cache, v_cache, stream=None):
@@ -986,25 +991,28 @@ def hb_rope(batch, rope, q, k, v, q_out, k_out, k_cache, v_cache, stream=None):
     appended."""
     hq, hkv, d, n = batch.num_q_heads, batch.num_kv_heads, batch.head_dim, batch.total_q
     q_rows, k_rows, pool = (n, hq, d), (n, hkv, d), (batch.num_pages, batch.page_size, hkv, d)
+    q_row, k_row, v_stride = hq * d, hkv * d, 0
     try:
         dev = q.get_device()
-        ok = (q.dtype is _BF16 and q.shape == q_rows and _dense_heads(q)
-              and k.dtype is _BF16 and k.shape == k_rows and _dense_heads(k)
-              and q_out.dtype is _BF16 and q_out.shape == q_rows and _in_place_or_dense(q_out, q)
+        q_stride, k_stride = _token_stride(q, q_row), _token_stride(k, k_row)
+        ok = (q.dtype is _BF16 and q.shape == q_rows and q_stride >= 0
+              and k.dtype is _BF16 and k.shape == k_rows and k_stride >= 0
+              and q_out.dtype is _BF16 and q_out.shape == q_rows and _in_place_or_dense(q_out, q, q_row)
               and dev >= 0 and dev == k.get_device() == q_out.get_device() and dev == _current_device()
               and (rope.device_index is None or rope.device_index == dev)
               and (not rope.head_dims or rope.head_dims == {d}))
         if k_out is not None:
             ok = (ok and k_out.dtype is _BF16 and k_out.shape == k_rows and k_out.get_device() == dev
-                  and _in_place_or_dense(k_out, k))
+                  and _in_place_or_dense(k_out, k, k_row))
         if k_cache is not None:
-            ok = (ok and v.dtype is _BF16 and v.shape == k_rows and _dense_heads(v) and v.get_device() == dev
+            v_stride = _token_stride(v, k_row)
+            ok = (ok and v.dtype is _BF16 and v.shape == k_rows and v_stride >= 0 and v.get_device() == dev
                   and k_cache.dtype is _BF16 and k_cache.shape == pool and k_cache.is_contiguous()
                   and v_cache.dtype is _BF16 and v_cache.shape == pool and v_cache.is_contiguous()
                   and k_cache.get_device() == dev == v_cache.get_device())
         else:
             ok = ok and v is None and v_cache is None
-    except AttributeError:
+    except (AttributeError, ValueError):
         ok = False
     if not ok:
         _refuse_rope(rope, d, (("q", q, q_rows), ("k", k, k_rows), ("v", v, k_rows)),
@@ -1014,8 +1022,8 @@ def hb_rope(batch, rope, q, k, v, q_out, k_out, k_cache, v_cache, stream=None):
         return
     # (data_ptr() of an empty pool is 0; the library refuses it)
     st = (_lib or load()).hb_rope(
-        ctypes.byref(batch), ctypes.byref(rope), q.data_ptr(), q.stride(0), k.data_ptr(), k.stride(0),
-        v.data_ptr() if v is not None else None, v.stride(0) if v is not None else 0, q_out.data_ptr(),
+        ctypes.byref(batch), ctypes.byref(rope), q.data_ptr(), q_stride, k.data_ptr(), k_stride,
+        v.data_ptr() if v is not None else None, v_stride, q_out.data_ptr(),
         k_out.data_ptr() if k_out is not None else None, k_cache.data_ptr() if k_cache is not None else None,
         v_cache.data_ptr() if v_cache is not None else None, _raw_stream(stream, dev))
     if st:
@@ -1040,7 +1048,7 @@ def _refuse_rope(rope, d, ins, outs, pools):
             raise ValueError(f"{name} must be contiguous")
     for name, t, shape, source in outs:
         if (isinstance(t, torch.Tensor) and isinstance(source, torch.Tensor) and t.dim() == 3 and source.dim() == 3
-                and not _in_place_or_dense(t, source)):
+                and not _in_place_or_dense(t, source, t.shape[1] * t.shape[2])):
             raise ValueError(f"{name} must be contiguous, or {name[0]} itself")
     _refuse_rows(*specs)
     if rope.device_index is not None and rope.device_index != torch.cuda.current_device():
