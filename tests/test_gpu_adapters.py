@@ -289,3 +289,9 @@ def test_calls_that_follow_one_another_in_place():
         hb.hb_norm(x=out, z=apart)
         torch.cuda.synchronize()
     assert torch.equal(y, apart)
+
+
+def test_long_prompts_over_many_columns():
+    """Tiles for more than one round of clusters, over a long K."""
+    for cols, r in (((256,), 24), ((128, 64, 64), 64)):
+        Case([3200, 1, 3100], [0, 1, 1], 7168, cols, 2, r, seed=r, ranks=[r, r - 11]).check_both()
