@@ -677,7 +677,8 @@ extern "C" hb_status hb_adapters(const hb_adapter_pool* pool, const void* h_plan
       sh.group_ranks = ((p.ranks + sh.groups - 1) / sh.groups + 7) / 8 * 8;
       const int64_t ctas = (int64_t)h.num_short * sh.groups;
       // (rounds of two CTAs per SM, one beside a long tile's, each as long as its warps' units and three more)
-      const int64_t slots = 2LL * h.num_sms - (h.num_long ? std::min<int64_t>(h.num_sms, (int64_t)h.num_long * lo.groups * lo.pieces) : 0);
+      const int64_t long_ctas = h.num_long ? (int64_t)h.num_long * lo.groups * lo.pieces : 0;
+      const int64_t slots = 2LL * h.num_sms - std::min<int64_t>(h.num_sms, long_ctas);
       int best = 1;
       int64_t best_cost = INT64_MAX;
       for (int n = 1; n <= std::min(h.short_pieces, std::max(1, units / kAdWarps)); ++n) {

@@ -18,7 +18,7 @@
 namespace hb {
 
 // ---------------------------------------------------------------- shrink
-// A cluster of CTAs takes a tile of rows and up to 256 ranks (16 at a time, those
+// A cluster of CTAs takes a tile of rows and up to 192 ranks (16 at a time, those
 // in use, of all destinations).  Each CTA sums a piece of K: the x tile and the
 // adapter's ranks come by TMA into a ring of 64-wide K blocks, M 128, N the ranks,
 // fp32 in tensor memory.  The pieces meet through distributed shared memory: each
