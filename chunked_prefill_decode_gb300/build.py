@@ -24,7 +24,7 @@ SOURCES = ["api.cu", "kv_append.cu", "attention.cu", "linear.cu", "noalloc.cu", 
            "step.cu", "pages.cu", "kv8_append.cu", "kv8_widen.cu", "attention8.cu",
            "norm.cu", "rope.cu", "adapters.cu", "builder.cpp"]
 HEADERS = ["hb_internal.h", "ptx.cuh", "decode_body.cuh", "chunk_body.cuh", "decode_plan.h", "kv8.cuh",
-           "decode8_body.cuh", "operands.h", "adapters.h", "adapters_long.cuh"]
+           "decode8_body.cuh", "operands.h", "ring.h", "adapters.h", "adapters_long.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
           "-I", INCLUDE, "-I", CSRC]

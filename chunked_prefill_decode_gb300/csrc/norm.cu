@@ -30,6 +30,7 @@
 #include "hb_internal.h"
 #include "operands.h"
 #include "ptx.cuh"
+#include "ring.h"
 
 namespace hb {
 
@@ -275,7 +276,8 @@ __global__ void __launch_bounds__(kNsThreads, 2) norm_rows_kernel(const NormPara
     g0[i] = p.gate && !own_gates && on ? *reinterpret_cast<const uint4*>(p.gate + v * 8) : zero;
   }
   __syncthreads();
-  for (int k = 0; k < n; ++k) {
+  int k = 0;
+  for (; k < n; ++k) {
     const int64_t row = blockIdx.x + k * step;
     const uint8_t* st = s_ring + (k % cfg.stages) * cfg.stage_bytes;
     const int turn = k & 1;   // (sums of neighbouring rows stand apart: a barrier lies between a place's uses)
@@ -339,8 +341,9 @@ __global__ void __launch_bounds__(kNsThreads, 2) norm_rows_kernel(const NormPara
     }
   }
   if (t == 0 && *abort_flag) {
-    // copies in flight land before the CTA leaves
-    for (int s = 0; s < cfg.stages && s < n; ++s) drain_wait(&s_full[s], ((n - 1 - s) / cfg.stages) & 1, abort_flag);
+    // what was issued lands before the CTA leaves (fewer copies than rows: the walk ended at row k)
+    const RowRing ring(cfg.stages, n, k);
+    for (int s = 0; s < ring.used(); ++s) drain_wait(&s_full[s], ring.last_parity(s), abort_flag);
     report_error(p.dev_error, HB_DEVERR_TIMEOUT);
   }
 }

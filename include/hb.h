@@ -567,7 +567,8 @@ size_t hb_linear_workspace_size(int32_t M, int32_t N, int32_t K, int32_t epilogu
  * element size (in place), and overlap nothing otherwise
  * (HB_ERR_INVALID_ARG).  Sums and means are fp32 (64 bits where a row's
  * squares leave its range), one rounding per output; what stands between rows
- * is neither read nor written.
+ * is neither read nor written.  Many rows come by copies whose waits are
+ * bounded; one that gives up is reported by hb_check as HB_ERR_TIMEOUT.
  * ------------------------------------------------------------------------- */
 typedef enum hb_stream_type {
   HB_STREAM_BF16 = 0,
