@@ -23,7 +23,7 @@
 // Measured on GB300 (a call among others in a graph, inputs not in L2): 68 tokens
 // of 8 + 8 heads of 64 2.8 us; 512 of 32 + 8 heads of 128 4.7 us; 2048 of 56 + 8 with
 // head norms 22.0 us (3.6 TB/s; the chain of loads, search, angles, sums and stores
-// of a token is longer than its bytes); 16205 of 32 + 8 70.7 us (6.1 TB/s, 90 % of
+// of a token is longer than its bytes); 16205 of 32 + 8 71.4 us (6.0 TB/s, 89 % of
 // the copy rate).
 #include <cuda_runtime.h>
 
@@ -108,18 +108,18 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, kCtas) rope_kernel(const R
   // where the lane's two vectors start in a head
   const int at0 = turns && !kInterleaved ? 8 * unit : 16 * unit;
   const int at1 = turns && !kInterleaved ? p.rot / 2 + 8 * unit : 16 * unit + 8;
-  uint4 in[kIters][2];
-#pragma unroll
-  for (int it = 0; it < kIters; ++it) {
-    const int h = head0 + it * kHeads;
-    in[it][0] = in[it][1] = make_uint4(0, 0, 0, 0);
-    if (tok >= p.total_q || h >= p.heads) continue;
+  auto load = [&](int h, uint4 (&v)[2]) {
+    v[0] = v[1] = make_uint4(0, 0, 0, 0);
+    if (tok >= p.total_q || h >= p.heads) return;
     const uint16_t* src = h < p.hq           ? p.q + tok * p.q_stride + h * D
                           : h < p.hq + p.hkv ? p.k + tok * p.k_stride + (h - p.hq) * D
                                              : p.v + tok * p.v_stride + (h - p.hq - p.hkv) * D;
-    in[it][0] = ld_row(src + at0);
-    in[it][1] = ld_row(src + at1);
-  }
+    v[0] = ld_row(src + at0);
+    v[1] = ld_row(src + at1);
+  };
+  uint4 in[kIters][2];
+#pragma unroll
+  for (int it = 0; it < kIters; ++it) load(head0 + it * kHeads, in[it]);
   const bool staged = p.num_seqs <= kRopeSmemSeqs;
   int32_t* s_ctx = s_cu + p.num_seqs + 1;
   if (staged) {
@@ -176,23 +176,30 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, kCtas) rope_kernel(const R
       s[e] = cs.y;
     }
   }
-#pragma unroll
-  for (int it = 0; it < kIters; ++it) {
-    const int h = head0 + it * kHeads;
+  // The head's norm, turn and stores; true (and nothing stored) where its squares leave fp32's range: a sum that
+  // overflowed, or one so small that eps does not hide what underflowed.  by: what the head is scaled with before
+  // it is squared.
+  auto put = [&](int h, const uint4 (&v)[2], float by) {
     const bool is_q = h < p.hq, is_k = !is_q && h < p.hq + p.hkv;
     const uint16_t* w = is_q ? p.q_weight : is_k ? p.k_weight : nullptr;
     float x[16];
-    uint4 out[2] = {in[it][0], in[it][1]};
+    uint4 out[2] = {v[0], v[1]};
     widen(out[0], x);
     widen(out[1], x + 8);
+    bool again = false;
     if (p.q_weight || p.k_weight) {       // (all lanes of the warp take part in the sums)
+      const float eps = p.eps * by * by;
       float ss = 0.f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+      for (int e = 0; e < 16; ++e) {
+        x[e] *= by;
+        ss = fmaf(x[e], x[e], ss);
+      }
 #pragma unroll
       for (int d = kUnits / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
       if (w) {
-        const float r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
+        again = by == 1.f && !(ss <= FLT_MAX && (ss >= 1e-30f || eps >= 1e-30f));
+        const float r = rsqrtf(fmaf(ss, 1.f / D, eps));
         float g[16];
         widen(*reinterpret_cast<const uint4*>(w + at0), g);
         widen(*reinterpret_cast<const uint4*>(w + at1), g + 8);
@@ -200,7 +207,7 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, kCtas) rope_kernel(const R
         for (int e = 0; e < 16; ++e) x[e] = x[e] * r * g[e];
       }
     }
-    if (h >= p.heads) continue;
+    if (h >= p.heads || again) return again;
     if (is_q || is_k) {
       if (turns) {
 #pragma unroll
@@ -229,6 +236,31 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, kCtas) rope_kernel(const R
       *reinterpret_cast<uint4*>(dst + at0) = out[0];
       *reinterpret_cast<uint4*>(dst + at1) = out[1];
     }
+    return false;
+  };
+  uint32_t rest = 0;    // bit it: the lane's head of that turn is still to be done
+#pragma unroll
+  for (int it = 0; it < kIters; ++it)
+    if (put(head0 + it * kHeads, in[it], 1.f)) rest |= 1u << it;
+  // those heads once more, read again (nothing was written in their place) and scaled; rare, and here so that it
+  // takes no registers from the others (a sum in 64 bits above: 2048 tokens 29.0 us instead of 22.0)
+  if (!__any_sync(0xffffffffu, rest)) return;
+#pragma unroll 1
+  for (int it = 0; it < kIters; ++it) {
+    if (!__any_sync(0xffffffffu, rest >> it & 1)) continue;
+    const int h = head0 + it * kHeads;
+    const bool there = rest >> it & 1;
+    uint4 v[2];
+    load(there ? h : p.heads, v);
+    float most = 0.f;
+    float x[16];
+    widen(v[0], x);
+    widen(v[1], x + 8);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(x[e]));
+#pragma unroll
+    for (int d = kUnits / 2; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+    put(there ? h : p.heads, v, most < 1.f ? 0x1p100f : 0x1p-100f);
   }
 }
 
@@ -350,7 +382,7 @@ extern "C" hb_status hb_rope(const hb_batch* batch, const hb_rope_params* rope, 
     p.factor = rope->factor;
     p.eps = rope->eps;
     // few tokens: two heads per lane, the shortest chain (68 tokens 2.8 us, with four 3.5; 512 4.7 and 4.9); many:
-    // four, three CTAs to an SM (16205 tokens 70.7 us; two CTAs 93, three heads 74); with head norms three and four
+    // four, three CTAs to an SM (16205 tokens 71.4 us; two CTAs 93, three heads 74); with head norms three and four
     // (2048 tokens 22.0 us; four and three 24.8, two and four 23.0)
     const bool few = T <= 4LL * num_sms, norms = p.q_weight || p.k_weight;
     const int iters = few ? 2 : norms ? 3 : 4;

@@ -640,7 +640,8 @@ typedef struct hb_rope_params {
  * Without caches (k_cache, v_cache and v all NULL) it only turns q and k, for
  * hb_kv8_append or an append elsewhere.  Tokens behind the last sequence are
  * left as they were; of the batch's descriptors, sliding_window plays no part.
- * fp32 arithmetic, one rounding; the angle is exact to 2^-32 of a turn at any
+ * fp32 arithmetic (a head whose squares leave its range is scaled for its
+ * mean), one rounding; the angle is exact to 2^-32 of a turn at any
  * position.
  *   q, k, v          device, bf16: token rows of Hq * D and Hkv * D elements,
  *                    *_stride elements apart (a multiple of 8; larger than the

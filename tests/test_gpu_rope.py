@@ -329,3 +329,47 @@ def test_rotated_cache_feeds_the_attention():
     hb.hb_check()
     for a, b in zip(*outs):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("size", [1e30, 1e36, 1e-18, 1e-22, 1e-38, 1e-40])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("tokens,d", [(9, 128), (9, 64), (2000, 128), (2000, 64)])
+def test_head_norms_of_squares_outside_of_fp32(tokens, d, interleaved, size):
+    """A head of large or tiny values, between ordinary ones, is normed as well."""
+    hb = lib()
+    st = Step([(tokens, tokens + 20)], 8, 2, d, seed=16)
+    for x, heads in ((st.q, (0, 5)), (st.k, (1,))):
+        for h in heads:
+            x[1::3, h] = (x[1::3, h].float() * size).to(BF)
+    rope = hb.make_rope(d // 2, interleaved=interleaved, eps=0.0, q_weight=st.weights[0], k_weight=st.weights[1])
+    q, k = torch.empty_like(st.q), torch.empty_like(st.k)
+    hb.hb_rope(st.batch, rope, st.q, st.k, st.v, q, k, st.kc, st.vc)
+    hb.hb_check()
+    angle = angles(d // 2, range(20, 20 + tokens))
+    for got, x, w in ((q, st.q, st.weights[0]), (k, st.k, st.weights[1])):
+        normed = torch.from_numpy(ob.rms_norm(f64(x), f64(w), 0.0))
+        check(got, expected(normed, None, angle, interleaved, 1.0))
+    slot = torch.arange(20, 20 + tokens)
+    page = torch.from_numpy(st.table[0, slot.numpy() // 16].astype(np.int64)).cuda()
+    assert torch.equal(st.kc[page, (slot % 16).cuda()], k)
+
+
+def test_head_norms_of_zeros_and_of_values_that_are_not_finite():
+    """As by the formula, and in their own head alone: with eps zeros stay zeros, without 0 / 0."""
+    hb = lib()
+    for eps in (1e-6, 0.0):
+        st = Step([(6, 20)], 8, 2, 64, seed=17)
+        st.q[2, 3] = 0
+        st.q[4, 1, 7] = float("inf")
+        st.k[1, 0, 9] = float("nan")
+        rope = hb.make_rope(64, eps=eps, q_weight=st.weights[0], k_weight=st.weights[1])
+        q, k = torch.empty_like(st.q), torch.empty_like(st.k)
+        hb.hb_rope(st.batch, rope, st.q, st.k, st.v, q, k, st.kc, st.vc)
+        assert q[2, 3].isnan().all() if eps == 0.0 else not q[2, 3].any()
+        # inf / inf in its pair, finite values over an infinite root: zeros
+        bad = (~torch.isfinite(q[4, 1])).nonzero().flatten().tolist()
+        assert bad == [7, 39] and not q[4, 1][[i for i in range(64) if i not in bad]].any()
+        assert k[1, 0].isnan().all()
+        q[2, 3] = q[4, 1] = 0
+        k[1, 0] = 0
+        assert torch.isfinite(q).all() and torch.isfinite(k).all()
