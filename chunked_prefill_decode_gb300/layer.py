@@ -160,14 +160,16 @@ class HybridBlock:
         residual stream after the attention block ("h", for checking the stages
         one by one).  With norms, blocks in a row share a launch between them:
         next_weight (the next block's w_pre[0]) leaves its normed input in
-        bufs["z"], and normed=True says that the block before did."""
+        bufs["z"], and normed=True says that the block before did (in these bufs)."""
         T = x.shape[0]
-        b = bufs if bufs is not None else self.buffers(T)
         s = self.shape
         if self.norms is not None and (x.dtype is torch.float32) != self.norms.stream_fp32:
             raise ValueError(f"x is {x.dtype}, norms.stream_fp32 is {self.norms.stream_fp32}")
         if self.norms is None and (normed or next_weight is not None):
             raise ValueError("a block without norms takes no normed input and leaves none")
+        if normed and bufs is None:
+            raise ValueError("normed: the block before left its normed input in its buffers, so bufs must be given")
+        b = bufs if bufs is not None else self.buffers(T)
         inp = x
         if self.norms is not None:
             inp = b["z"]
