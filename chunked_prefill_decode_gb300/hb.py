@@ -957,6 +957,8 @@ def make_rope(rotary_dim, base=10000.0, scaling="none", scale_by=1.0, original_c
                 raise ValueError(f"{name} must be a contiguous [head_dim] bfloat16 tensor")
             if w.device.type != torch.device(device).type:
                 raise ValueError(f"{name} is on {w.device}, not on {device}")
+            if keep and w.get_device() != keep[0].get_device():
+                raise ValueError(f"{name} is on {w.device}, not on {keep[0].device}")
             keep.append(w)
             setattr(r, name, w.data_ptr())
     r.tensors, r.head_dims = tuple(keep), {w.numel() for w in (q_weight, k_weight) if w is not None}

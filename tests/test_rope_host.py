@@ -110,3 +110,25 @@ def test_tensors_are_checked_by_name():
     for bad in (z(64, dtype=torch.float32), z(2, 64), z(128)[::2]):
         with pytest.raises(ValueError, match="k_weight"):
             hb.make_rope(64, k_weight=bad, device="cpu")
+
+
+class Weight:
+    """A head norm's weight on a device that is not here."""
+    dtype = torch.bfloat16
+
+    def __init__(self, index):
+        self.index, self.device = index, torch.device("cuda", index)
+
+    dim = lambda self: 1  # noqa: E731
+    is_contiguous = lambda self: True  # noqa: E731
+    numel = lambda self: 64  # noqa: E731
+    data_ptr = lambda self: AT + (self.index << 24)  # noqa: E731
+    get_device = lambda self: self.index  # noqa: E731
+
+
+def test_head_norms_are_on_one_device():
+    hb = lib()
+    assert hb.make_rope(0, q_weight=Weight(1), k_weight=Weight(1)).device_index == 1
+    for q, k in ((0, 1), (1, 0)):
+        with pytest.raises(ValueError, match="k_weight is on cuda"):
+            hb.make_rope(0, q_weight=Weight(q), k_weight=Weight(k))
