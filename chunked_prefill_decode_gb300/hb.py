@@ -1114,6 +1114,14 @@ def adapters_plan_items(plan):
     return np.frombuffer(body[:16 * n], np.int32).reshape(n, 4), np.frombuffer(body[16 * n:], np.int32)
 
 
+def _host_int32(name, values):
+    """A host array of whole numbers as int32; those that do not fit are refused, not cut."""
+    a = np.asarray(values)
+    if a.size and (a.dtype.kind not in "iu" or int(a.min()) < -_INT_MAX - 1 or int(a.max()) > _INT_MAX):
+        raise ValueError(f"{name} must be whole numbers of 32 bits")
+    return np.ascontiguousarray(a, dtype=np.int32)
+
+
 def hb_adapters_plan(pools, q_len, adapter, num_sms, total_q=None, workspace=None, plan=None, stream=None, upload=True):
     """Sort a batch's tokens by adapter: q_len and each sequence's adapter (-1: none),
     host arrays.  `pools`: a pool or several (the step's projections) of as many
@@ -1122,8 +1130,7 @@ def hb_adapters_plan(pools, q_len, adapter, num_sms, total_q=None, workspace=Non
     pools = (pools,) if isinstance(pools, HbAdapterPool) else tuple(pools)
     if not pools or any(p.num_adapters != pools[0].num_adapters for p in pools):
         raise ValueError("the pools of a plan have as many adapters")
-    ql = np.ascontiguousarray(q_len, dtype=np.int32)
-    of = np.ascontiguousarray(adapter, dtype=np.int32)
+    ql, of = _host_int32("q_len", q_len), _host_int32("adapter", adapter)
     if ql.ndim != 1 or ql.shape != of.shape:
         raise ValueError(f"q_len has shape {ql.shape}, adapter {of.shape}")
     total = int(ql.sum(dtype=np.int64)) if total_q is None else int(total_q)

@@ -177,3 +177,21 @@ def test_tensors_are_checked_by_name():
         args[at] = junk
         with pytest.raises(ValueError, match=name):
             hb.hb_adapters(*args)
+
+
+@pytest.mark.parametrize("kw", [dict(of=np.array([0, 1 << 32])), dict(of=np.array([0, (1 << 32) - 1], np.uint64)),
+                                dict(of=np.array([0.0, 1.7])), dict(of=[0, 1 << 40]), dict(q=np.array([1, (1 << 32) + 2])),
+                                dict(q=np.array([1, -(1 << 31) - 1])), dict(q=["1", "2"])])
+def test_numbers_past_32_bits_are_refused(kw):
+    """(Cut to 32 bits they would name another adapter, or another length.)"""
+    with pytest.raises(ValueError, match="32 bits"):
+        plan_of(lib(), **{"q": [1, 2], "of": [0, 1], **kw})
+
+
+def test_host_numbers_of_any_width():
+    hb = lib()
+    want = plan_of(hb, [1, 2], [0, -1]).tobytes()
+    for kind in (np.int8, np.int16, np.int64):
+        assert plan_of(hb, np.array([1, 2], kind), np.array([0, -1], kind)).tobytes() == want
+    assert plan_of(hb, np.array([1, 2], np.uint8), torch.tensor([0, -1])).tobytes() == want
+    assert hb.adapters_plan_header(plan_of(hb, [], [], total_q=0))["total_q"] == 0
