@@ -603,6 +603,9 @@ extern "C" hb_status hb_adapters(const hb_adapter_pool* pool, const void* h_plan
         if ((s = check_apart(o, {out->y[j], T, 2LL * out->cols[j], 2LL * out->cols[j], names[1][j]}, false)) != HB_OK)
           return s;
     }
+    // (the workspace is written, with x A^T)
+    for (int j = 0; j < num_in; ++j)
+      if (j != 5 && (s = check_apart(in[5], in[j], false)) != HB_OK) return s;
     AdapterParams p{};
     int num_sms = 0;
     if ((s = internal_device(&p.dev_error, &num_sms)) != HB_OK) return s;

@@ -712,7 +712,7 @@ hb_status hb_adapters_plan(int32_t num_seqs, int32_t total_q, const int32_t* h_q
  *   y, out   device, [total_q, cols[i]] bf16 each, columns alike; out may be y
  *            (in place, e.g. hb_linear's destinations), or arrays that overlap
  *            no other operand: rows whose sequence has no adapter are then
- *            copied.  out must not overlap x.
+ *            copied.  out must not overlap x, nor the workspace any operand.
  * x A^T is summed in fp32 and enters the second product in two bf16 terms (16
  * bits); the sum with y is rounded once.  Two launches for the tiles and two for
  * the other rows, which run side by side.  A wait that gives up is reported by

@@ -195,3 +195,11 @@ def test_host_numbers_of_any_width():
         assert plan_of(hb, np.array([1, 2], kind), np.array([0, -1], kind)).tobytes() == want
     assert plan_of(hb, np.array([1, 2], np.uint8), torch.tensor([0, -1])).tobytes() == want
     assert hb.adapters_plan_header(plan_of(hb, [], [], total_q=0))["total_q"] == 0
+
+
+@pytest.mark.parametrize("kw", [dict(ws=AT + (8 << 24)), dict(ws=AT + (9 << 24) + 256), dict(ws=AT), dict(ws=AT + (1 << 24)),
+                                dict(ws=AT + (2 << 24)), dict(ws=AT + (3 << 24)), dict(x=AT + (11 << 24) + 64)])
+def test_a_workspace_over_an_operand_is_refused(kw):
+    hb = lib()
+    assert call(hb, **kw) == 1
+    assert b"the workspace and" in hb.load().hb_last_error()
