@@ -6,9 +6,10 @@
 // a sin + b cos) times the attention factor.  p f_i reaches 10^6 radians in long
 // contexts, where an fp32 product is off by tenths.  So f_i is held as a
 // fraction of a turn in 64-bit fixed point (`phases`): p times it, modulo 2^64,
-// is p f_i modulo one turn with nothing lost, and its upper 32 bits are the
-// angle to 2^-32 of a turn (from the table's 53 bits: p 2^-55 turns), whatever
-// the position.
+// is p times the table's value modulo one turn with nothing lost.  Its upper 32
+// bits become an fp32 fraction of half a turn (off by 2^-26 of a turn at most,
+// whatever the position); the table, computed in 64 bits, is off by less than
+// 2^-51 of a turn (2^-54 as measured), which the position multiplies.
 //
 // Every element is read and written once (k also into its page): HBM bounds
 // large batches, launch and latency small ones.  A warp takes one token and some of

@@ -607,7 +607,8 @@ hb_status hb_norm(const hb_norm_args* args, void* stream);
  *                   them f_i * (g + (1 - g) / scale_by), g = (t - low) / (high
  *                   - low)
  * rotary_dim is a positive multiple of 16, base > 1, scale_by >= 1, 0 <= low <
- * high (what a kind does not use is not looked at).
+ * high (what a kind does not use is not looked at).  64-bit arithmetic: a phase is
+ * off by less than 2^-51 of a turn.
  * ------------------------------------------------------------------------- */
 typedef enum hb_rope_scaling {
   HB_ROPE_PLAIN = 0,
@@ -641,8 +642,10 @@ typedef struct hb_rope_params {
  * hb_kv8_append or an append elsewhere.  Tokens behind the last sequence are
  * left as they were; of the batch's descriptors, sliding_window plays no part.
  * fp32 arithmetic (a head whose squares leave its range is scaled for its
- * mean), one rounding; the angle is exact to 2^-32 of a turn at any
- * position.
+ * mean), one rounding.  An angle is position times phase modulo a turn, exact as
+ * an integer at any position; it is off by 2^-26 of a turn at most where its
+ * upper 32 bits become an fp32 number, and by the position times what the phase
+ * itself is off (hb_rope_phases: less than 2^-51 of a turn).
  *   q, k, v          device, bf16: token rows of Hq * D and Hkv * D elements,
  *                    *_stride elements apart (a multiple of 8; larger than the
  *                    row where q, k and v are columns of one array)

@@ -12,6 +12,7 @@ import pytest
 import torch
 
 from _hbutil import lib
+from _turns import exact_angles, exact_turns
 from oracle import block as ob
 
 pytestmark = pytest.mark.gpu
@@ -373,3 +374,22 @@ def test_head_norms_of_zeros_and_of_values_that_are_not_finite():
         q[2, 3] = q[4, 1] = 0
         k[1, 0] = 0
         assert torch.isfinite(q).all() and torch.isfinite(k).all()
+
+
+@pytest.mark.parametrize("pos", [5, 1 << 20, (1 << 24) + 1, (1 << 31) - 20])
+@pytest.mark.parametrize("scaling,by", [("none", 1.0), ("parts", 16.0), ("base", 4.0)])
+def test_far_positions_against_exact_angles(pos, scaling, by):
+    """The phases themselves are off by less than 2^-51 of a turn (test_rope_host.py), times the position."""
+    hb = lib()
+    d, n = 128, 5
+    st = Step([(n, 40)], 4, 2, d, seed=18)
+    st.dev[1].fill_(pos + n)
+    kw = dict(base=5e5, scaling=scaling)
+    q, k = run(st, d, norms=(False, False), cached=False, scale_by=by, original_context=8192, **kw)
+    hb.hb_check()
+    angle = np.array(exact_angles(exact_turns(d, by=by, **kw), range(pos, pos + n)))
+    for got, x in ((q, st.q), (k, st.k)):
+        want, bound = expected(x, None, angle, False, 1.0)
+        size = np.abs(f64(x))
+        size = np.concatenate([size[..., :d // 2] + size[..., d // 2:]] * 2, -1)
+        check(got, (want, bound + 2 * math.pi * (pos + n) * 2.0 ** -51 * (1 + 2.0 ** -8) * size))

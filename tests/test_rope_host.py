@@ -1,12 +1,14 @@
 """hb_rope and hb_rope_phases on the host (no GPU): the phases against the
 frequencies' definition, and the refusals."""
 import ctypes
+from decimal import Decimal
 
 import numpy as np
 import pytest
 import torch
 
 from _hbutil import host_batch, lib
+from _turns import exact_turns
 from oracle import block as ob
 
 AT = 1 << 32      # device addresses that no call here follows
@@ -132,3 +134,16 @@ def test_head_norms_are_on_one_device():
     for q, k in ((0, 1), (1, 0)):
         with pytest.raises(ValueError, match="k_weight is on cuda"):
             hb.make_rope(0, q_weight=Weight(q), k_weight=Weight(k))
+
+
+@pytest.mark.parametrize("scaling,by", [("none", 1.0), ("linear", 3.0), ("base", 8.0), ("parts", 16.0), ("parts", 1.5)])
+@pytest.mark.parametrize("rot,base", [(16, 10000.0), (64, 5e5), (128, 1e6), (80, 1.5), (48, 1e8), (112, 1e4)])
+def test_phases_are_off_by_less_than_2_to_the_minus_51_of_a_turn(rot, base, scaling, by):
+    """What far positions multiply.  f <= 1 is computed in 64 bits: with u = 2^-53, its
+    exponent is off by u and the power's base by 4 u (a power and a product, by at most 8
+    here), which moves f by at most |f ln f| u + 4 u (f ln f is at most 1 / e); the power
+    itself rounds by 2 u, the share of the parts by 6 u, the division by a turn by 2 u, and
+    the fixed point cuts 2^-64.  Under 16 u of f, over a turn of 6.28: less than 3 u, or 2^-51."""
+    got = lib().rope_phases(rot, base, scaling, by, original_context=8192, parts=(1.0, 32.0))
+    worst = max(abs(Decimal(int(p)) / 2 ** 64 - t) for p, t in zip(got, exact_turns(rot, base, scaling, by)))
+    assert worst < Decimal(3) / 2 ** 53
