@@ -212,3 +212,61 @@ def test_offsets_past_32_bits():
     want = ob.norm(x=f64(x))[1]
     hb.hb_norm(x=x, z=z)
     close(z, want, 64 * ULP * np.abs(want), 2.0 ** -8)
+
+
+def walked(rows, width):
+    """The rows that the CTAs of the row-walking kernel meet, CTA by CTA (rows, rows a grid apart, ..), for shapes that it
+    takes: bf16 streams of 1024 to 8192 columns and 4 Mi elements or more."""
+    assert 1024 <= width <= 8192 and rows * width >= 4 << 20
+    threads = -(-(-(-width // 8 // 4)) // 32) * 32
+    grid = min(rows, min(16, 512 // threads) * torch.cuda.get_device_properties(0).multi_processor_count)
+    return [list(range(c, rows, grid)) for c in range(grid)]
+
+
+WALKED = [(4200, 1032), (2600, 2056), (1300, 4096), (1100, 8192)]
+
+
+@pytest.mark.parametrize("size", [1e30, 1e-18, 1e-22])
+@pytest.mark.parametrize("rows,width", WALKED)
+def test_squares_outside_of_fp32_in_walked_rows(rows, width, size):
+    """All rows of one CTA (its sums in 64 bits one behind the other), the second ones of some, the last one of another,
+    in y, in x, in both."""
+    hb = lib()
+    ctas = walked(rows, width)
+    special = ctas[5] + [c[1] for c in ctas[10:14]] + [ctas[20][-1], rows - 1]
+    assert len(ctas[5]) >= 2
+    t = case(rows, width, "xypwoz", "row")
+    for i, r in enumerate(special):
+        for n in ("y", "x", "xy")[i % 3] if i >= len(ctas[5]) else "xy":
+            t[n][r] = (t[n][r].float() * size).to(BF)
+    want = expected(t, eps=0.0)
+    hb.hb_norm(**t, eps=0.0)
+    hb.hb_check()
+    check(t, want)
+
+
+@pytest.mark.parametrize("rows,width", WALKED)
+def test_zeros_and_values_that_are_not_finite_stay_in_their_walked_row(rows, width):
+    hb = lib()
+    ctas = walked(rows, width)
+    t = case(rows, width, "xypwoz", "row")
+    plain = {k: v if v is None else v.clone() for k, v in t.items()}
+    hb.hb_norm(**plain, eps=0.0)
+    zeros, nans, infs = ctas[3], ctas[4][:1] + ctas[6][1:], [ctas[7][0], ctas[8][-1]]
+    for n in "xy":
+        t[n][zeros] = 0
+    t["x"][nans, 77] = float("nan")
+    t["y"][infs, width - 1] = float("-inf")
+    hb.hb_norm(**t, eps=0.0)
+    hb.hb_check()
+    bad = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    bad[zeros + nans + infs] = True
+    for n in ("x_out", "z"):
+        assert torch.equal(t[n][~bad], plain[n][~bad])
+    # 0 / 0 as by the formula; a NaN in its element of the stream and all of its norm; inf / inf likewise
+    assert t["x_out"][zeros].isnan().all() and t["z"][zeros].isnan().all()
+    assert (t["x_out"][nans].isnan().sum(1) == 1).all() and t["z"][nans].isnan().all()
+    assert t["x_out"][infs, -1].isnan().all() and t["x_out"][infs, :-1].isfinite().all() and t["z"][infs].isnan().all()
+    # with an eps zeros stay zeros
+    hb.hb_norm(**t, eps=1e-6)
+    assert not t["x_out"][zeros].any() and not t["z"][zeros].any()
