@@ -692,7 +692,8 @@ typedef struct hb_adapter_pool {
  * q_len (>= 0) and of each sequence's adapter (-1: none), and serves every pool
  * of num_adapters adapters with at most max_ranks = slices * max_rank ranks (all
  * projections of all layers of a step).  total_q: rows of x, y and out, at least
- * the sum of q_len; rows behind the last sequence are neither read nor written.
+ * the sum of q_len; rows behind the last sequence are not written, and what a
+ * tile's copies (whole boxes of 128 rows) read of them is not used.
  * Buffers, sizes and upload as with hb_plan (h_plan must stay unchanged until
  * its copy has completed; a workspace must not be shared by calls in flight at
  * once; a captured hb_adapters reads the plan in its workspace when it is
