@@ -99,9 +99,13 @@ __device__ __forceinline__ T row_sum(T v, T* part, int warps, int bar) {
 // sum that overflowed, or one so small that eps does not hide what
 // underflowed) are summed again in 64 bits: rare, and the same for all threads
 // of the row.
-template <int kVecs>
-__device__ __forceinline__ float row_scale(const float (&f)[kVecs][8], float* part, double* wide, int warps,
-                                           int bar, const NormParams& p) {
+// kNoEps (eps is 0, the only one that lets a root fall below 2^-100, where fp32 may not
+// hold its inverse): such a row is scaled by 2^64, f here and `stage`, where f was read
+// from and is read from again (this thread's vectors of a staged row, blockDim.x
+// apart; or NULL).  Other calls do without: 62.4 us instead of 60.4 on 8191 gated rows of 4096.
+template <int kVecs, bool kNoEps>
+__device__ __forceinline__ float row_scale(float (&f)[kVecs][8], float* part, double* wide, int warps, int bar,
+                                           const NormParams& p, uint4* stage = nullptr) {
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i)
@@ -115,12 +119,24 @@ __device__ __forceinline__ float row_scale(const float (&f)[kVecs][8], float* pa
 #pragma unroll
     for (int e = 0; e < 8; ++e) dd = fma((double)f[i][e], (double)f[i][e], dd);
   dd = row_sum(dd, wide, warps, bar);
-  return (float)(1.0 / sqrt(dd / (8.0 * p.vecs) + (double)p.eps));
+  double root = sqrt(dd / (8.0 * p.vecs) + (double)p.eps);
+  if (kNoEps && root > 0.0 && root < 0x1p-100) {
+    root *= 0x1p64;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[i][e] *= 0x1p64f;
+      const int v = threadIdx.x + i * (int)blockDim.x;
+      if (stage && v < p.vecs) stage[v] = narrow8(f[i]);   // (exact)
+    }
+    if (stage) fence_async_shared();   // (the next row's copy lands there)
+  }
+  return (float)(1.0 / root);
 }
 
 // kVecs: vectors per thread.  The row's threads take vectors t, t + threads,
 // ..; those past the row hold zeros.
-template <int kVecs, bool kWide>
+template <int kVecs, bool kWide, bool kNoEps>
 __global__ void __launch_bounds__(norm_max_threads(kVecs)) norm_kernel(const NormParams p) {
   __shared__ float s_part[2][32];
   __shared__ double s_wide[2][32];
@@ -167,7 +183,7 @@ __global__ void __launch_bounds__(norm_max_threads(kVecs)) norm_kernel(const Nor
     wz[i] = p.w_pre && on[i] ? *reinterpret_cast<const uint4*>(p.w_pre + at[i]) : zero;
   }
   if (p.w_post) {
-    const float r = row_scale<kVecs>(u, s_part[0] + slot, s_wide[0] + slot, warps, bar, p);
+    const float r = row_scale<kVecs, kNoEps>(u, s_part[0] + slot, s_wide[0] + slot, warps, bar, p);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       float w[8];
@@ -206,7 +222,7 @@ __global__ void __launch_bounds__(norm_max_threads(kVecs)) norm_kernel(const Nor
     }
   }
   if (p.z) {
-    const float r = row_scale<kVecs>(x, s_part[1] + slot, s_wide[1] + slot, warps, bar, p);
+    const float r = row_scale<kVecs, kNoEps>(x, s_part[1] + slot, s_wide[1] + slot, warps, bar, p);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       if (!on[i]) continue;
@@ -233,6 +249,7 @@ struct NsCfg {
   int32_t stages, stage_bytes, x_at, gate_at;   // a stage: y | x | gate (where each row has its own)
 };
 
+template <bool kNoEps>
 __global__ void __launch_bounds__(kNsThreads, 2) norm_rows_kernel(const NormParams p, const NsCfg cfg) {
   constexpr int kVecs = kNsVecs;
   extern __shared__ __align__(128) uint8_t s_ring[];
@@ -279,7 +296,7 @@ __global__ void __launch_bounds__(kNsThreads, 2) norm_rows_kernel(const NormPara
   int k = 0;
   for (; k < n; ++k) {
     const int64_t row = blockIdx.x + k * step;
-    const uint8_t* st = s_ring + (k % cfg.stages) * cfg.stage_bytes;
+    uint8_t* st = s_ring + (k % cfg.stages) * cfg.stage_bytes;
     const int turn = k & 1;   // (sums of neighbouring rows stand apart: a barrier lies between a place's uses)
     bool ok = mbar_wait(&s_full[k % cfg.stages], (k / cfg.stages) & 1, abort_flag);
     float x[kVecs][8];
@@ -290,7 +307,7 @@ __global__ void __launch_bounds__(kNsThreads, 2) norm_rows_kernel(const NormPara
         const int v = t + i * (int)blockDim.x;
         widen8(v < p.vecs ? reinterpret_cast<const uint4*>(st)[v] : zero, x[i]);
       }
-      r = row_scale<kVecs>(x, s_part[turn][0], s_wide[turn][0], warps, 1, p);
+      r = row_scale<kVecs, kNoEps>(x, s_part[turn][0], s_wide[turn][0], warps, 1, p, reinterpret_cast<uint4*>(st));
     }
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
@@ -327,7 +344,7 @@ __global__ void __launch_bounds__(kNsThreads, 2) norm_rows_kernel(const NormPara
       }
     }
     if (p.z) {
-      r = row_scale<kVecs>(x, s_part[turn][1], s_wide[turn][1], warps, 1, p);
+      r = row_scale<kVecs, kNoEps>(x, s_part[turn][1], s_wide[turn][1], warps, 1, p);
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) {
         const int v = t + i * (int)blockDim.x;
@@ -349,14 +366,17 @@ __global__ void __launch_bounds__(kNsThreads, 2) norm_rows_kernel(const NormPara
 }
 
 cudaError_t launch_rows(const NormParams& p, const NsCfg& cfg, int grid, int block, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(norm_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmem / 2);
+  const auto kernel = p.eps > 0.f ? norm_rows_kernel<false> : norm_rows_kernel<true>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNsSmem / 2);
   if (e != cudaSuccess) return e;
-  return launch_serialized(norm_rows_kernel, (unsigned)grid, (unsigned)block, (size_t)cfg.stages * cfg.stage_bytes, st, p, cfg);
+  return launch_serialized(kernel, (unsigned)grid, (unsigned)block, (size_t)cfg.stages * cfg.stage_bytes, st, p, cfg);
 }
 
 template <int kVecs>
 cudaError_t launch(const NormParams& p, bool wide, unsigned grid, unsigned block, cudaStream_t st) {
-  return launch_serialized(wide ? norm_kernel<kVecs, true> : norm_kernel<kVecs, false>, grid, block, 0, st, p);
+  const auto kernel = p.eps > 0.f ? (wide ? norm_kernel<kVecs, true, false> : norm_kernel<kVecs, false, false>)
+                                  : (wide ? norm_kernel<kVecs, true, true> : norm_kernel<kVecs, false, true>);
+  return launch_serialized(kernel, grid, block, 0, st, p);
 }
 
 }  // namespace

@@ -270,3 +270,31 @@ def test_zeros_and_values_that_are_not_finite_stay_in_their_walked_row(rows, wid
     # with an eps zeros stay zeros
     hb.hb_norm(**t, eps=1e-6)
     assert not t["x_out"][zeros].any() and not t["z"][zeros].any()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("form", ["xypwoz", "xywoz", "xwz", "ypwz", "ypoz"])
+@pytest.mark.parametrize("rows,width", [(5, 64), (5, 1024), (5, 2048), (5, 16384), (2600, 2056)])
+@pytest.mark.parametrize("size", [1e-34, 1e-38, 1e-40])
+def test_rows_of_numbers_below_the_smallest_normal_one(rows, width, form, dtype, size):
+    """The root of such a row has no inverse in fp32.  Below 2^-126 a number's step is fixed: each of the four
+    operations that make the sum may be off by half of 2^-149, the stream's rounding to bf16 by half of 2^-133, and
+    z's by as much (an element of an ordinary row may be as small)."""
+    hb = lib()
+    kw = dict(eps=0.0, residual_scale=0.7, branch_scale=-0.4)
+    t = case(rows, width, form, None, dtype)
+    special = [2] if rows == 5 else walked(rows, width)[5] + [rows - 1]
+    for n in "xy":
+        if t[n] is not None:
+            t[n][special] = (t[n][special].double() * size).to(t[n].dtype)
+    want = expected(t, **kw)
+    hb.hb_norm(**t, **kw)
+    hb.hb_check()
+    new, z, part, gain = want
+    step = 4 * 2.0 ** -150
+    if t["x_out"] is not None:
+        narrow = 2.0 ** -134 if dtype is BF else 2.0 ** -150
+        close(t["x_out"], new, 64 * ULP * part + step + narrow, 2.0 ** -8 if dtype is BF else ULP)
+    if t["z"] is not None:
+        close(t["z"], z, 128 * ULP * (part * gain + np.abs(z)) * (1 + 2.0 ** -8) + step * gain * (1 + 2.0 ** -8) + 2.0 ** -134,
+              2.0 ** -8)
