@@ -8,7 +8,7 @@
 //
 // With ranks r of 8 to 128 a byte of x, y or an adapter meets about r
 // operations where the tensor cores need 284 per byte of HBM: the bytes bound
-// it, each row of x and y and each adapter in use moved once.
+// it, each row of x and y and each adapter in use moved once from HBM.
 //
 // The plan (host) sorts the batch's rows by adapter, so that requests of one
 // adapter share its reads wherever they stand in the batch, and cuts them into
@@ -68,7 +68,9 @@ namespace {
 constexpr int kAdThreads = 256, kAdWarps = kAdThreads / 32;
 // Neighbouring rows of an adapter from which they are long tiles: a 64-token chunk
 // and 4 decodes at K 512 take 4.1 us as short segments, 9.8 us with a tile (four
-// launches instead of two).
+// launches instead of two).  Measured for that K and rank alone, and not between 64 rows
+// and 128.  (A shorter run of more than 16 rows reads its adapter once per segment, from
+// L2.)
 constexpr int kAdLongRun = 128;
 constexpr int kAdGroupRanks = 64;       // ranks that a short shrink CTA holds (at most)
 constexpr int kAdShortPieces = 16;      // its pieces of K (at most)

@@ -384,7 +384,8 @@ extern "C" hb_status hb_rope(const hb_batch* batch, const hb_rope_params* rope, 
     p.eps = rope->eps;
     // few tokens: two heads per lane, the shortest chain (68 tokens 2.8 us, with four 3.5; 512 4.7 and 4.9); many:
     // four, three CTAs to an SM (16205 tokens 71.4 us; two CTAs 93, three heads 74); with head norms three and four
-    // (2048 tokens 22.0 us; four and three 24.8, two and four 23.0)
+    // (2048 tokens 22.0 us; four and three 24.8, two and four 23.0; 64 registers spill 22 to 50 bytes).  Between 512
+    // and 2048 tokens nothing was measured; below the border head norms go with the few.
     const bool few = T <= 4LL * num_sms, norms = p.q_weight || p.k_weight;
     const int iters = few ? 2 : norms ? 3 : 4;
     const bool inter = rope->interleaved != 0;

@@ -942,7 +942,10 @@ def rope_phases(rotary_dim, base=10000.0, scaling="none", scale_by=1.0, original
 def make_rope(rotary_dim, base=10000.0, scaling="none", scale_by=1.0, original_context=0, parts=(1.0, 32.0),
               interleaved=False, factor=1.0, q_weight=None, k_weight=None, eps=1e-6, device="cuda") -> HbRopeParams:
     """hb_rope's parameters, with the phases on the device.  rotary_dim 0: head
-    norms alone.  Made once per model; the tensors live as long as it."""
+    norms alone.  scaling "parts" goes by the turns that a pair makes over
+    original_context, linearly between the two of `parts`; ramps over the pair
+    index and factors per pair are other tables, which this does not make.  Made
+    once per model; the tensors live as long as it."""
     r = HbRopeParams()
     r.rotary_dim, r.interleaved, r.factor, r.eps = int(rotary_dim), int(bool(interleaved)), factor, eps
     keep = []

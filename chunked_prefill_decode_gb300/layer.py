@@ -21,7 +21,8 @@ What a model adds to it is on request (BlockNorms, hb.make_rope, hb.make_adapter
     x = r x + s gate norm(branch)  after it       hb_norm (with the next z)
     q, k turned by their positions                hb_rope (in hb_kv_append's place)
     + scale (x A^T) B^T  with each request's      hb_adapters (q, k, v; the output
-      own adapter                                 and down projections)
+      own adapter                                 and down projections; not gate and
+                                                  up, whose epilogue applies silu)
 
 Weights are synthetic (seeded, N(0, 1/fan_in) in bf16): no trained weights
 are needed to time or check the block.  The residual stream x is updated in

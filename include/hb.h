@@ -605,7 +605,9 @@ hb_status hb_norm(const hb_norm_args* args, void* stream);
  *                   / (2 pi) turns over the trained context keeps f_i from t =
  *                   high on, has f_i / scale_by up to t = low, and between
  *                   them f_i * (g + (1 - g) / scale_by), g = (t - low) / (high
- *                   - low)
+ *                   - low): linear in t, not in the pair's index.  A model that
+ *                   was trained with another ramp, or with a factor per pair,
+ *                   needs phases of its own: hb_rope takes any
  * rotary_dim is a positive multiple of 16, base > 1, scale_by >= 1, 0 <= low <
  * high (what a kind does not use is not looked at).  64-bit arithmetic: a phase is
  * off by less than 2^-51 of a turn.
